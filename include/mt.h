@@ -28,6 +28,19 @@
  *                     attention-projection and vocabulary compression passages
  *                     before Dispatch Policy.
  *
+ * around them, the parts of a step that read and write a paged cache of keys
+ * and values, and the last step before a token is drawn:
+ *
+ *   mt_rope_append    per-head RMSNorm (optional) and rotary positions with
+ *                     one or several axes of q and k, k and v written to the
+ *                     cache's pages
+ *   mt_paged_attention  attention of every sequence's new tokens (one for a
+ *                     decode step, a chunk of a prompt, or both in one batch)
+ *                     over its pages, causal, with an optional sliding window
+ *                     and first tokens that stay visible
+ *   mt_logit_penalties  biases, penalties for repeated tokens and
+ *                     allowed-token masks on the vocabulary's logits
+ *
  * plus the offline packer mt_pack_affine (affine group quantisation of fp32
  * weights into the stored layout), and the warmed executor mt_mlp_plan_*
  * that runs L such layers back to back as one persistent kernel.
@@ -102,7 +115,9 @@ typedef enum mt_status {
   MT_ERR_FORMAT = 5,  /* unknown weight format, dtype, bit width or option */
   MT_ERR_ALIAS = 6,   /* an output overlaps an input it may not overlap */
   MT_ERR_CUDA = 7,    /* a CUDA runtime call failed (see mt_last_cuda_error) */
-  MT_ERR_TIMEOUT = 8  /* a bounded device-side wait expired (mt_device_error) */
+  MT_ERR_TIMEOUT = 8, /* a bounded device-side wait expired (mt_device_error) */
+  MT_ERR_PAGE = 9     /* a page-table entry read on the device is out of range
+                         (mt_device_error) */
 } mt_status;
 
 /* Output element type of a call.  Inputs are always bf16. */
@@ -435,12 +450,172 @@ mt_status mt_mlp_stack_run_noalloc(const mt_mlp_layer* layers, int L, int d, int
                                    mt_wfmt fmt, float eps, const void* values,
                                    const void* residual, void* out_y, void* stream);
 
+/*
+ * ---- Paged cache: the calls between the q/k/v and the o projection
+ *
+ * A cache holds num_pages pages of page_size tokens; element (page, t, h, e)
+ * of K (and of V) is at page * page_stride + t * token_stride + h * head_stride
+ * + e, e < head_dim, so that [page][t][h][e] and [page][h][t][e] orders, and K
+ * and V interleaved in one allocation, are all views of this form.
+ */
+typedef struct mt_paged_cache {
+  void* k;              /* bf16, device, 16-byte aligned */
+  void* v;
+  int64_t page_stride;  /* in elements, multiples of 8, the same for K and V */
+  int64_t token_stride;
+  int64_t head_stride;
+  int num_pages;
+  int page_size;        /* tokens of a page, 1 .. 65536 */
+  int kv_heads;
+  int head_dim;         /* a multiple of 8, 16 .. 256 */
+} mt_paged_cache;
+
+/*
+ * The sequences of one step.  Their new tokens are rows of one [T][...]
+ * tensor, sequence after sequence; token p of sequence b lives in the cache
+ * at page pages[b][p / page_size], row p % page_size.  The arrays are read on
+ * the device (4-byte aligned): lengths outside their ranges are clamped to
+ * them, and an entry of `pages` that is needed but not in [0, num_pages) is
+ * not followed (the call that meets one reads zeros, writes nothing, and sets
+ * the device error word to MT_ERR_PAGE).  Entries of pages no token sees are
+ * not read.
+ */
+typedef struct mt_paged_batch {
+  const int32_t* q_start; /* [B + 1] first row of each sequence's new tokens, not
+                             decreasing; rows of T outside [q_start[0],
+                             q_start[B]) belong to no sequence */
+  const int32_t* kv_len;  /* [B] tokens in the cache, the new ones among them:
+                             new token i of n has position kv_len - n + i */
+  const int32_t* pages;   /* [B][pages_ld] page indices */
+  int64_t pages_ld;       /* entries between rows of pages, >= max_pages */
+  int B;                  /* 1 .. 1024 */
+  int T;                  /* rows, 0 .. 2^22 */
+  int max_pages;          /* entries of a row; max_pages * page_size <= 2^30 */
+  int max_q;              /* the most new tokens of a sequence, as far as the
+                             host knows: it chooses between kernels, and any
+                             value gives the same results */
+} mt_paged_batch;
+
+typedef enum mt_rope_pairing {
+  MT_ROPE_HALF = 0,     /* elements i and i + rot/2 turn together */
+  MT_ROPE_ADJACENT = 1  /* elements 2i and 2i + 1 turn together */
+} mt_rope_pairing;
+
+/*
+ * Rotary positions of q and k, with the cache write of k and v.
+ *   q        : bf16 [T][q_heads][head_dim], rows q_stride elements apart
+ *   k, v     : bf16 [T][kv_heads][head_dim], rows k_stride / v_stride apart
+ *              (views of one projection's output rows, for instance)
+ *   q_norm, k_norm : bf16 [head_dim] gains of an RMSNorm over each head's
+ *              elements before the rotation (eps added to the mean square), or
+ *              NULL for none
+ *   positions: int32 [n_axes][T]: a token's position on each axis (time,
+ *              height and width of a picture; one axis for text).  Negative
+ *              ones turn backwards.
+ *   inv_freq : float [rot/2], angle of pair i = positions[axis[i]] *
+ *              inv_freq[i] radians
+ *   axis     : uint8 [rot/2], the axis that each pair follows (values from
+ *              n_axes on mean the last axis), or NULL: all follow axis 0
+ *   rot      : elements of a head that turn, a multiple of 16, 0 < rot <=
+ *              head_dim; the others pass through
+ *   q_out    : bf16 [T][q_heads][head_dim], rows q_out_stride apart; may be q
+ *              itself (the same address and stride)
+ * Row t of sequence b goes to the cache position of its token; a token whose
+ * position is not in the cache (kv_len - n + i < 0, or a page out of range)
+ * is not written.  Rows that belong to no sequence are neither read nor
+ * written; T = 0 does nothing (the row pointers may then be NULL).
+ * The angle is taken modulo one turn in 64-bit integers before its sine and
+ * cosine, so that it is as exact at position 2^30 as at 1 (an fp32 product
+ * would be off by 2^-24 of the angle, whole turns at long positions);
+ * everything else is fp32, with one rounding to bf16.
+ * Limits: 1 <= n_axes <= 8; 1 <= q_heads <= 1024; 1 <= kv_heads <= 1024;
+ *         strides multiples of 8; pointers 16-byte aligned (positions,
+ *         inv_freq 4, axis 1).
+ */
+mt_status mt_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                         const void* v, int64_t v_stride, int q_heads, const void* q_norm,
+                         const void* k_norm, float eps, const int32_t* positions, int n_axes,
+                         const float* inv_freq, const uint8_t* axis, int rot,
+                         mt_rope_pairing pairing, void* q_out, int64_t q_out_stride,
+                         const mt_paged_cache* cache, const mt_paged_batch* batch, void* stream);
+
+/*
+ * Attention of the new tokens over the paged cache.  With p_i the position of
+ * new token i, key j is visible to it if
+ *   j <= p_i and (window == 0 or j > p_i - window or j < sinks),
+ * and for query head h (reading key/value head h / (q_heads / kv_heads))
+ *   s_j = scale * q_i . k_j,  lse = log(sum_j exp(s_j)),
+ *   out_i = sum_j exp(s_j - lse) v_j          over the visible keys j.
+ * A token that sees no key has out 0 and lse -inf.
+ *   q        : bf16 [T][q_heads][head_dim], rows q_stride elements apart
+ *   cache    : the keys and values, the new tokens' among them
+ *   out      : [T][q_heads][head_dim] of out_dtype, rows out_stride apart
+ *   lse      : float [T][q_heads], or NULL
+ *   workspace: at least mt_paged_attention_workspace_bytes(...) bytes, 16-byte
+ *              aligned, contents of no account: partial results where one
+ *              sequence's keys are shared out over several SMs (joined in key
+ *              order by a second kernel, so results do not vary between runs)
+ * Rows that belong to no sequence are neither read nor written; T = 0 does
+ * nothing (the row pointers may then be NULL).
+ * Products are bf16 with fp32 accumulation, softmax statistics fp32.  The
+ * weights exp(s_j - max) enter the product with V as bf16 (one rounding of
+ * 2^-8 each) in the kernel for long chunks, and as a sum of two bf16 (2^-16)
+ * in the kernel for few rows, which serves all fp32 outputs.
+ * A non-finite V of a key that is beyond kv_len, or that no new token of the
+ * row's tile sees, does not reach the output.
+ * Limits: 1 <= q_heads <= 1024, q_heads % kv_heads == 0, q_heads / kv_heads <=
+ *         128; scale > 0 and finite; window >= 0; sinks >= 0; strides
+ *         multiples of 8; pointers 16-byte aligned (lse 4).
+ */
+size_t mt_paged_attention_workspace_bytes(int T, int B, int q_heads, int kv_heads, int head_dim);
+mt_status mt_paged_attention(const void* q, int64_t q_stride, int q_heads,
+                             const mt_paged_cache* cache, const mt_paged_batch* batch, float scale,
+                             int window, int sinks, void* out, int64_t out_stride,
+                             mt_dtype out_dtype, float* lse, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
+ * Biases, penalties for repeated tokens and allowed-token masks, in this
+ * order, on the logits of B sequences:
+ *   x = logit + bias
+ *   token in the history:    x = x > 0 ? x / repetition : x * repetition
+ *   token generated n times: x = x - (frequency * n + presence)    for n > 0
+ *   token not allowed:       x = -inf
+ *   logits, out : [B][V] of dtype, rows logits_ld / out_ld elements apart; out
+ *                 may be logits (the same address and stride)
+ *   history     : int32 token ids of all sequences; history_start int32
+ *                 [B + 1] (not decreasing) gives each one's range.  The first
+ *                 prompt_len[b] tokens (NULL: none) of a range are its
+ *                 prompt's, the others were generated.  Ids outside [0, V)
+ *                 are passed over (padding).  All NULL for no history.
+ *   repetition, presence, frequency : float [B], each may be NULL (1, 0, 0)
+ *   bias_ids int32, bias_values float, bias_start int32 [B + 1]: each
+ *                 sequence's biased tokens; of several entries for one token
+ *                 the last counts.  All NULL for none.
+ *   allowed     : uint32 [B][allowed_ld], bit t % 32 of word t / 32 set if
+ *                 token t is allowed; NULL: all are
+ *   n_history, n_bias : entries of history and of bias_ids (ranges are
+ *                 clamped to them)
+ * Arithmetic is fp32 with one rounding to dtype; counts are integers, so that
+ * results do not depend on the order of the history.
+ * Limits: 0 <= B <= 65535 (0 does nothing), 1 <= V <= 2^24; arrays aligned to their elements;
+ *         logits_ld, out_ld >= V; allowed_ld >= ceil(V / 32).
+ */
+mt_status mt_logit_penalties(const void* logits, int64_t logits_ld, void* out, int64_t out_ld,
+                             mt_dtype dtype, int B, int V, const int32_t* history,
+                             const int32_t* history_start, const int32_t* prompt_len,
+                             int n_history, const float* repetition, const float* presence,
+                             const float* frequency, const int32_t* bias_ids,
+                             const float* bias_values, const int32_t* bias_start, int n_bias,
+                             const uint32_t* allowed, int64_t allowed_ld, void* stream);
+
 /* Library options.  Returns MT_ERR_FORMAT for an unknown option. */
 mt_status mt_set_option(mt_option opt, int value);
 int mt_get_option(mt_option opt);
 
-/* Device error word: MT_ERR_TIMEOUT if a kernel's bounded wait expired since
- * the word was last cleared, 0 otherwise, -1 if it cannot be read.  Reading it
+/* Device error word: MT_ERR_TIMEOUT if a kernel's bounded wait expired, or
+ * MT_ERR_PAGE if a kernel met a page out of range, since the word was last
+ * cleared, 0 otherwise, -1 if it cannot be read.  Reading it
  * synchronises with the device (cudaMemcpyFromSymbol); clear != 0 resets it. */
 int mt_device_error(int clear);
 

@@ -17,6 +17,13 @@ Calls (same names as the C ABI):
   :func:`mt_prefill_linear_bias` -- the same epilogues for many activation
   rows (prefill) on the tcgen05 tensor cores, with a caller-owned workspace
   of :func:`mt_prefill_workspace_bytes` bytes.
+* :func:`mt_rope_append` -- per-head RMSNorm and rotary positions (one or
+  several axes) of q and k, k and v written to a paged cache.
+* :func:`mt_paged_attention` -- attention of each sequence's new tokens over its
+  pages, causal, with an optional window and always-visible first tokens
+  (workspace of :func:`mt_paged_attention_workspace_bytes` bytes).
+* :func:`mt_logit_penalties` -- biases, penalties for repeated tokens and
+  allowed-token masks on logits.
 * :func:`mt_pack_affine` / :func:`mt_unpack_affine` -- affine group packer.
 * :func:`mt_pack_mx` -- MXFP8 / MXFP4 block-scaled packer (E8M0 scales).
 * :func:`mt_mlp_plan_create` / :func:`mt_mlp_plan_run` / :func:`mt_mlp_plan_destroy`
@@ -43,12 +50,14 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 MT_OK, MT_ERR_NULL, MT_ERR_SHAPE, MT_ERR_GROUP, MT_ERR_ALIGN = 0, 1, 2, 3, 4
-MT_ERR_FORMAT, MT_ERR_ALIAS, MT_ERR_CUDA, MT_ERR_TIMEOUT = 5, 6, 7, 8
+MT_ERR_FORMAT, MT_ERR_ALIAS, MT_ERR_CUDA, MT_ERR_TIMEOUT, MT_ERR_PAGE = 5, 6, 7, 8, 9
 MT_BF16, MT_F32 = 0, 1
 MT_W_BF16, MT_W_AFFINE8, MT_W_AFFINE4, MT_W_MXFP8, MT_W_MXFP4 = 0, 1, 2, 3, 4
 MT_OPT_PDL, MT_OPT_GEMV, MT_OPT_TEST_BARRIER_EXTRA, MT_OPT_ACT_BITS = 0, 1, 2, 3
 
-_P, _I, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+MT_ROPE_HALF, MT_ROPE_ADJACENT = 0, 1
+
+_P, _I, _F, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_int64
 _SIGS = {
     "mt_add_rmsnorm": (_I, [_P, _P, _P, _F, _P, _P, _I, _I, _I, _P]),
     "mt_swiglu_gateup": (_I, [_P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _P]),
@@ -70,6 +79,10 @@ _SIGS = {
     "mt_mlp_plan_create": (_I, [_P, _I, _I, _I, _I, _I, _F, _P]),
     "mt_mlp_plan_run": (_I, [_P, _P, _P, _P, _P, _P]),
     "mt_mlp_plan_destroy": (_I, [_P]),
+    "mt_rope_append": (_I, [_P, _L, _P, _L, _P, _L, _I, _P, _P, _F, _P, _I, _P, _P, _I, _I, _P, _L, _P, _P, _P]),
+    "mt_paged_attention_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I]),
+    "mt_paged_attention": (_I, [_P, _L, _I, _P, _P, _F, _I, _I, _P, _L, _I, _P, _P, ctypes.c_size_t, _P]),
+    "mt_logit_penalties": (_I, [_P, _L, _P, _L, _I, _I, _I, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _I, _P, _L, _P]),
     "mt_mlp_stack_run_noalloc": (_I, [_P, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -87,6 +100,18 @@ class MlpLayer(ctypes.Structure):
 class MlpTrace(ctypes.Structure):
     """``mt_mlp_trace``: optional per-layer outputs (device pointers or NULL)."""
     _fields_ = [(n, _P) for n in ("out_sum", "out_norm", "h", "y")]
+
+
+class PagedCache(ctypes.Structure):
+    """``mt_paged_cache``: K and V pages and their strides in elements."""
+    _fields_ = [("k", _P), ("v", _P), ("page_stride", _L), ("token_stride", _L), ("head_stride", _L),
+                ("num_pages", _I), ("page_size", _I), ("kv_heads", _I), ("head_dim", _I)]
+
+
+class PagedBatch(ctypes.Structure):
+    """``mt_paged_batch``: one step's sequences, rows and page table."""
+    _fields_ = [("q_start", _P), ("kv_len", _P), ("pages", _P), ("pages_ld", _L), ("B", _I), ("T", _I),
+                ("max_pages", _I), ("max_q", _I)]
 
 
 class MTError(RuntimeError):
@@ -303,6 +328,166 @@ def mt_mlp_stack_run_noalloc(layers, d, f, group, fmt, eps, values, residual, ou
     _check(_lib.mt_mlp_stack_run_noalloc(arr, len(layers), int(d), int(f), int(group), int(fmt),
                                          float(eps), _ptr(values), _ptr(residual), _ptr(out_y),
                                          _stream(stream)), "mt_mlp_stack_run_noalloc")
+
+
+def _typed(name, t, dtype, dim):
+    if t.dtype != dtype or t.dim() != dim:
+        raise TypeError(f"{name}: a {dim}-dimensional {dtype} tensor is required, got {t.dim()}-dimensional {t.dtype}")
+
+
+def _flat(name, t, dtype, dim=1):
+    if t is None:
+        return None
+    _typed(name, t, dtype, dim)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor is required")
+    return t.data_ptr()
+
+
+def _head_rows(name, t, dtype, T, H, D):
+    """Pointer and row stride of a [T, H, D] tensor whose heads lie side by side."""
+    _typed(name, t, dtype, 3)
+    if tuple(t.shape) != (T, H, D):
+        raise ValueError(f"{name}: shape {(T, H, D)} is required, got {tuple(t.shape)}")
+    st = t.stride()
+    if (D > 1 and st[2] != 1) or (H > 1 and st[1] != D):
+        raise ValueError(f"{name}: heads must lie side by side in a row")
+    return t.data_ptr(), (st[0] if T > 1 else max(st[0], H * D))
+
+
+def _paged(k_cache, v_cache, pages, q_start, kv_len, T, max_q):
+    """The cache and batch arguments from tensors: caches [pages, page, heads, dim]
+    (any strides with contiguous dim, the same for both), pages int32 [B, n],
+    q_start int32 [B + 1], kv_len int32 [B]."""
+    import torch
+    i32 = torch.int32
+    _typed("k_cache", k_cache, torch.bfloat16, 4)
+    _typed("v_cache", v_cache, torch.bfloat16, 4)
+    n, page, heads, dim = k_cache.shape
+    st = k_cache.stride()
+    if v_cache.shape != k_cache.shape or v_cache.stride() != st:
+        raise ValueError("k_cache and v_cache must have the same shape and strides")
+    if dim > 1 and st[3] != 1:
+        raise ValueError("k_cache: the last dimension must be contiguous")
+    _typed("pages", pages, i32, 2)
+    B, width = pages.shape
+    if width > 1 and pages.stride(1) != 1:
+        raise ValueError("pages: the last dimension must be contiguous")
+    ks, kl = _flat("q_start", q_start, i32), _flat("kv_len", kv_len, i32)
+    if q_start.shape[0] != B + 1 or kv_len.shape[0] != B:
+        raise ValueError(f"q_start must have {B + 1} entries and kv_len {B}")
+    cache = PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1], st[2], n, page, heads, dim)
+    batch = PagedBatch(ks, kl, pages.data_ptr(), max(pages.stride(0), width) if B == 1 else pages.stride(0), B, T, width,
+                       int(max_q))
+    return cache, batch
+
+
+def mt_rope_append(q, k, v, positions, inv_freq, q_out, k_cache, v_cache, pages, q_start, kv_len, axis=None,
+                   q_norm=None, k_norm=None, eps=1e-6, pairing=MT_ROPE_HALF, stream=None) -> None:
+    """Rotary positions of q and k (after an optional per-head RMSNorm), k and v
+    written to their cache positions.  q [T, q_heads, dim], k and v [T,
+    kv_heads, dim] (bf16, rows at any stride); positions int32 [T] or [n_axes,
+    T]; inv_freq float [rot / 2]; axis uint8 [rot / 2] or None (axis 0)."""
+    import torch
+    if q.dim() != 3:
+        raise TypeError("q: a 3-dimensional tensor is required")
+    T, H, D = q.shape
+    cache, batch = _paged(k_cache, v_cache, pages, q_start, kv_len, T, 1)
+    bf = torch.bfloat16
+    qp, qs = _head_rows("q", q, bf, T, H, D)
+    kp, ks = _head_rows("k", k, bf, T, cache.kv_heads, D)
+    vp, vs = _head_rows("v", v, bf, T, cache.kv_heads, D)
+    op, os_ = _head_rows("q_out", q_out, bf, T, H, D)
+    if D != cache.head_dim:
+        raise ValueError(f"the cache's head size is {cache.head_dim}, q's is {D}")
+    pp = _flat("positions", positions, torch.int32, positions.dim() if positions.dim() in (1, 2) else 1)
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    if positions.shape[-1] != T:
+        raise ValueError(f"positions: {T} tokens are required")
+    fp = _flat("inv_freq", inv_freq, torch.float32)
+    half = inv_freq.shape[0]
+    ap = _flat("axis", axis, torch.uint8)
+    if axis is not None and axis.shape[0] != half:
+        raise ValueError(f"axis: {half} entries are required")
+    np_, kn = _flat("q_norm", q_norm, bf), _flat("k_norm", k_norm, bf)
+    for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+        if w is not None and w.shape[0] != D:
+            raise ValueError(f"{name}: {D} entries are required")
+    _check(_lib.mt_rope_append(qp, qs, kp, ks, vp, vs, H, np_, kn, eps, pp, axes, fp, ap, 2 * half, pairing, op, os_,
+                               ctypes.byref(cache), ctypes.byref(batch), _stream(stream)), "mt_rope_append")
+
+
+def mt_paged_attention_workspace_bytes(T, B, q_heads, kv_heads, head_dim) -> int:
+    return int(_lib.mt_paged_attention_workspace_bytes(int(T), int(B), int(q_heads), int(kv_heads), int(head_dim)))
+
+
+def mt_paged_attention(q, k_cache, v_cache, pages, q_start, kv_len, max_q, scale, out, workspace, lse=None, window=0,
+                       sinks=0, stream=None) -> None:
+    """Attention of the new tokens q [T, q_heads, dim] over the paged cache;
+    out [T, q_heads, dim] (bf16 or fp32), lse float [T, q_heads] or None,
+    window 0 for none.  max_q: the most new tokens of a sequence (a hint)."""
+    import torch
+    if q.dim() != 3:
+        raise TypeError("q: a 3-dimensional tensor is required")
+    T, H, D = q.shape
+    cache, batch = _paged(k_cache, v_cache, pages, q_start, kv_len, T, max_q)
+    if D != cache.head_dim:
+        raise ValueError(f"the cache's head size is {cache.head_dim}, q's is {D}")
+    qp, qs = _head_rows("q", q, torch.bfloat16, T, H, D)
+    f32 = out.dtype == torch.float32
+    op, os_ = _head_rows("out", out, torch.float32 if f32 else torch.bfloat16, T, H, D)
+    lp = _flat("lse", lse, torch.float32, 2)
+    if lse is not None and tuple(lse.shape) != (T, H):
+        raise ValueError(f"lse: shape {(T, H)} is required")
+    _check(_lib.mt_paged_attention(qp, qs, H, ctypes.byref(cache), ctypes.byref(batch), scale, window, sinks, op, os_,
+                                   MT_F32 if f32 else MT_BF16, lp, workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), _stream(stream)), "mt_paged_attention")
+
+
+def mt_logit_penalties(logits, out, history=None, history_start=None, prompt_len=None, repetition=None, presence=None,
+                       frequency=None, bias_ids=None, bias_values=None, bias_start=None, allowed=None,
+                       stream=None) -> None:
+    """Biases, penalties for repeated tokens and allowed-token masks on logits
+    [B, V] (bf16 or fp32) into out (which may be logits); ragged int32 history
+    and bias lists with [B + 1] starts, allowed int32 [B, words] bits."""
+    import torch
+    i32, f32 = torch.int32, torch.float32
+    _typed("logits", logits, f32 if logits.dtype == f32 else torch.bfloat16, 2)
+    _typed("out", out, logits.dtype, 2)
+    B, V = logits.shape
+    if out.shape != logits.shape or (V > 1 and (logits.stride(1) != 1 or out.stride(1) != 1)):
+        raise ValueError("logits and out must have the same shape and contiguous rows")
+    args = []
+    for name, t, dt, n in (("history", history, i32, None), ("history_start", history_start, i32, B + 1),
+                           ("prompt_len", prompt_len, i32, B), ("repetition", repetition, f32, B),
+                           ("presence", presence, f32, B), ("frequency", frequency, f32, B),
+                           ("bias_ids", bias_ids, i32, None), ("bias_values", bias_values, f32, None),
+                           ("bias_start", bias_start, i32, B + 1)):
+        args.append(_flat(name, t, dt))
+        if n is not None and t is not None and t.shape[0] != n:
+            raise ValueError(f"{name}: {n} entries are required")
+    hist, start, prompt, rep, pres, freq, ids, values, bstart = args
+    n_hist = history.shape[0] if history is not None else 0
+    n_bias = bias_ids.shape[0] if bias_ids is not None else 0
+    if bias_values is not None and bias_values.shape[0] != n_bias:
+        raise ValueError("bias_ids and bias_values must have the same length")
+    # an empty tensor has no address: a list without entries is no list
+    if not n_hist:
+        hist = start = prompt = None
+    if not n_bias:
+        ids = values = bstart = None
+    ap, ald = None, 0
+    if allowed is not None:
+        _typed("allowed", allowed, i32, 2)
+        if allowed.shape[0] != B or (allowed.shape[1] > 1 and allowed.stride(1) != 1):
+            raise ValueError(f"allowed: {B} contiguous rows are required")
+        ap, ald = allowed.data_ptr(), (allowed.stride(0) if B > 1 else allowed.shape[1])
+        if allowed.shape[1] * 32 < V:
+            raise ValueError(f"allowed: {(V + 31) // 32} words a row are required")
+    _check(_lib.mt_logit_penalties(logits.data_ptr(), logits.stride(0) if B > 1 else V, out.data_ptr(),
+                                   out.stride(0) if B > 1 else V, MT_F32 if logits.dtype == f32 else MT_BF16, B, V,
+                                   hist, start, prompt, n_hist, rep, pres, freq, ids, values, bstart, n_bias, ap, ald,
+                                   _stream(stream)), "mt_logit_penalties")
 
 
 def mt_set_option(opt: int, value: int) -> None:

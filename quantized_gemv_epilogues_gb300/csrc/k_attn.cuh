@@ -1,0 +1,321 @@
+// k_attn.cuh - mt_paged_attention: how the work of a batch is shared out over
+// the GPU, and the joining of the parts.
+//
+// Mathematics.  Row r of a tile is one (new token, query head) pair; with
+// s_j = scale * q_r . k_j over the visible keys, any set of keys gives a part
+// (m, l, o) = (max s_j, sum exp(s_j - m), sum exp(s_j - m) v_j), and parts
+// join by (m, sum l_i e^(m_i - m), sum o_i e^(m_i - m)).  The kernels keep m
+// in units of log2 e, so that every exponential is an exp2.
+//
+// Sharing out.  The query heads of one key/value head and the new tokens of
+// one sequence are packed into tiles of R rows, which read each key and value
+// once for all of their rows.  A tile's visible keys are blocks of BK: those
+// with sinks, then those from the first row's window to the last row's
+// position.  All (sequence, key/value head, tile, block) units form one line,
+// and CTA c of a persistent grid takes the c-th equal stretch of it: lengths
+// are only known on the device, sequences differ by orders of magnitude, and
+// this balances every mixture to one block.  A tile that a stretch boundary
+// cuts leaves parts in the workspace (at most two per CTA), which a second
+// kernel joins in key order; the sum's order depends only on the lengths.
+#pragma once
+#include <float.h>
+
+#include "k_paged.cuh"
+
+namespace mt {
+
+struct AttnArgs {
+  PagedArgs pg;
+  const uint16_t* q;
+  int64_t q_stride;
+  void* out;
+  int64_t out_stride;
+  float* lse;  // or nullptr
+  int out_f32;
+  int q_heads, group;
+  float scale_log2;  // scale * log2 e
+  int window, sinks;
+  int tile_tokens;  // tokens of a tile, 0: tiles of packed rows that may start within a token
+  int min_units;    // fewest blocks of a CTA's stretch
+  float* part_o;    // [2 * CTAs][R][DP]
+  float2* part_ml;  // [2 * CTAs][R]
+  int4* cut;        // [CTAs][2]: the tile that begins in CTA c's stretch and ends in a later one
+};
+
+// The blocks of a tile: block i of n is key block i < sink ? i : i - sink + win.
+struct TileSpan {
+  int first_pos, last_pos;  // positions of the tile's first and last token
+  int key_end;              // keys [0, key_end) reach the last token
+  int win_lo;               // first key of the first token's window
+  int sink, win, n;
+};
+template <int BK>
+__device__ __forceinline__ TileSpan tile_span(const PagedSeq& s, int i0, int i1, int window, int sinks) {
+  TileSpan t;
+  t.first_pos = s.kv - s.n + i0;
+  t.last_pos = s.kv - s.n + i1;
+  t.key_end = max(t.last_pos + 1, 0);
+  t.win_lo = window > 0 ? max(t.first_pos - window + 1, 0) : 0;
+  const int end = (t.key_end + BK - 1) / BK;
+  t.win = min(t.win_lo / BK, end);
+  t.sink = (min(sinks, t.key_end) + BK - 1) / BK;
+  if (t.win <= t.sink) t.win = t.sink = 0;
+  t.n = max(t.sink + end - t.win, 1);  // a tile that sees no key still has its output to write
+  return t;
+}
+__device__ __forceinline__ int span_block(const TileSpan& t, int i) { return i < t.sink ? i : i - t.sink + t.win; }
+
+// Tile rt of a sequence: its first packed row, its rows and its tokens.
+struct TileRows {
+  int p0, rows, i0, i1;
+};
+template <int R>
+__device__ __forceinline__ TileRows tile_rows(const AttnArgs& a, const PagedSeq& s, int rt) {
+  const int per = a.tile_tokens ? a.tile_tokens * a.group : R;
+  TileRows t;
+  t.p0 = rt * per;
+  t.rows = min(per, s.n * a.group - t.p0);
+  t.i0 = t.p0 / a.group;
+  t.i1 = (t.p0 + t.rows - 1) / a.group;
+  return t;
+}
+template <int R>
+__device__ __forceinline__ int tile_count(const AttnArgs& a, const PagedSeq& s) {
+  const int per = a.tile_tokens ? a.tile_tokens * a.group : R;
+  return (s.n * a.group + per - 1) / per;  // n <= 2^22, group <= 128: within 31 bits
+}
+
+// A position in the line of units.
+struct Cursor {
+  int b, h, rt, i, tiles;
+  PagedSeq s;
+  TileSpan t;
+  TileRows r;
+};
+
+template <int R, int BK>
+__device__ __forceinline__ void cursor_tile(const AttnArgs& a, Cursor& c) {
+  c.r = tile_rows<R>(a, c.s, c.rt);
+  c.t = tile_span<BK>(c.s, c.r.i0, c.r.i1, a.window, a.sinks);
+}
+// The next unit (there is one).
+template <int R, int BK>
+__device__ __forceinline__ void cursor_next(const AttnArgs& a, Cursor& c) {
+  if (++c.i < c.t.n) return;
+  c.i = 0;
+  if (++c.rt == c.tiles) {
+    c.rt = 0;
+    if (++c.h == a.pg.kv_heads) {
+      c.h = 0;
+      do {
+        if (++c.b >= a.pg.B) { c.b = a.pg.B - 1; break; }  // past the end: never used
+        c.s = paged_seq(a.pg, c.b);
+      } while (c.s.n == 0);
+      c.tiles = tile_count<R>(a, c.s);
+      if (c.s.n == 0) return;
+    }
+  }
+  cursor_tile<R, BK>(a, c);
+}
+
+// The plan's shared memory: may overlap what the kernel uses after it.
+struct PlanShared {
+  long long pre[PG_MAX_B + 1];  // units before each sequence
+  long long sum[32];
+  int big[PG_MAX_B];
+  int n_big;
+};
+
+// Units of every sequence, their running sums, and the start of this CTA's
+// stretch: [u0, u1) of all units, `per` to a CTA.  Every thread of the block
+// (NT of them) calls it and gets the same answers; ends with a barrier.
+template <int R, int BK, int NT>
+__device__ void plan(const AttnArgs& a, PlanShared* sh, int cta, int ctas, long long* u0, long long* u1, long long* per,
+                     Cursor* cur) {
+  const PagedArgs& pg = a.pg;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) sh->n_big = 0;
+  __syncthreads();
+  // a sequence's units, one thread each; those of many tiles go to the whole block
+  for (int b = tid; b < pg.B; b += NT) {
+    const PagedSeq s = paged_seq(pg, b);
+    const int tiles = tile_count<R>(a, s);
+    long long n = 0;
+    if (tiles <= 4) {
+      for (int rt = 0; rt < tiles; ++rt) {
+        const TileRows r = tile_rows<R>(a, s, rt);
+        n += tile_span<BK>(s, r.i0, r.i1, a.window, a.sinks).n;
+      }
+    } else {
+      sh->big[atomicAdd(&sh->n_big, 1)] = b;
+    }
+    sh->pre[b + 1] = n * pg.kv_heads;
+  }
+  __syncthreads();
+  for (int k = 0; k < sh->n_big; ++k) {
+    const int b = sh->big[k];
+    const PagedSeq s = paged_seq(pg, b);
+    const int tiles = tile_count<R>(a, s);
+    long long n = 0;
+    for (int rt = tid; rt < tiles; rt += NT) {
+      const TileRows r = tile_rows<R>(a, s, rt);
+      n += tile_span<BK>(s, r.i0, r.i1, a.window, a.sinks).n;
+    }
+    atomicAdd(reinterpret_cast<unsigned long long*>(&sh->pre[b + 1]), (unsigned long long)(n * pg.kv_heads));
+  }
+  __syncthreads();
+  // running sums: a run of sequences per thread, then over the threads
+  const int run = (pg.B + NT - 1) / NT, b0 = min(tid * run, pg.B), b1 = min(b0 + run, pg.B);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += sh->pre[b + 1];
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) sh->sum[warp] = inc;
+  __syncthreads();
+  long long base = inc - mine;
+  for (int w = 0; w < warp; ++w) base += sh->sum[w];
+  for (int b = b0; b < b1; ++b) {
+    base += sh->pre[b + 1];
+    sh->pre[b + 1] = base;
+  }
+  if (tid == 0) sh->pre[0] = 0;
+  __syncthreads();
+  const long long total = sh->pre[pg.B];
+  *per = max((total + ctas - 1) / ctas, (long long)a.min_units);
+  *u0 = min((long long)cta * *per, total);
+  *u1 = min(*u0 + *per, total);
+  Cursor c = {};
+  if (*u0 < *u1) {
+    int lo = 0, hi = pg.B;  // the sequence with pre[lo] <= u0 < pre[lo + 1]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (sh->pre[mid] <= *u0) lo = mid;
+      else hi = mid;
+    }
+    c.b = lo;
+    c.s = paged_seq(pg, lo);
+    c.tiles = tile_count<R>(a, c.s);
+    const long long each = (sh->pre[lo + 1] - sh->pre[lo]) / pg.kv_heads, at = *u0 - sh->pre[lo];
+    c.h = (int)(at / each);
+    long long rest = at - (long long)c.h * each;
+    // the tile: 32 at a time, by every warp for itself
+    for (int rt0 = 0; rt0 < c.tiles; rt0 += 32) {
+      const int rt = rt0 + lane;
+      long long n = 0;
+      if (rt < c.tiles) {
+        const TileRows r = tile_rows<R>(a, c.s, rt);
+        n = tile_span<BK>(c.s, r.i0, r.i1, a.window, a.sinks).n;
+      }
+      long long in = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, in, o);
+        if (lane >= o) in += v;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, in > rest);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        c.rt = rt0 + l;
+        c.i = (int)(rest - __shfl_sync(0xffffffffu, in - n, l));
+        break;
+      }
+      rest -= __shfl_sync(0xffffffffu, in, 31);
+    }
+    cursor_tile<R, BK>(a, c);
+  }
+  *cur = c;
+  __syncthreads();
+}
+
+// Records the tile that begins in CTA `cta`'s stretch and ends in CTA `last`'s
+// (or none): what the joining kernel needs to write its rows.
+__device__ __forceinline__ void put_cut(const AttnArgs& a, int cta, int last, const Cursor& c) {
+  a.cut[2 * cta] = make_int4(last, c.s.row0, c.h, c.r.p0);
+  a.cut[2 * cta + 1] = make_int4(c.r.rows, 0, 0, 0);
+}
+
+__device__ __forceinline__ float exp2_(float x) { return exp2f(x); }
+
+// One CTA of 128 threads joins rows y, y + gridDim.y, ... of the tile cut at
+// the end of CTA x's stretch.  The parts are shared out over the four warps,
+// whose sums are added in order.
+template <int R, int DP>
+__global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int c0 = blockIdx.x;
+  const int4 k0 = a.cut[2 * c0];
+  const int c1 = k0.x;
+  if (c1 <= c0) return;
+  const int rows = a.cut[2 * c0 + 1].x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int V = DP / 32;  // columns a lane
+  __shared__ float o_sh[4][DP];
+  __shared__ float2 ml_sh[4];
+  const int parts = c1 - c0 + 1, per = (parts + 3) / 4;
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    float m = -INFINITY, l = 0.f, o[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = 0.f;
+    const int p_end = min(parts, (warp + 1) * per);
+#pragma unroll 4
+    for (int p = warp * per; p < p_end; ++p) {
+      const int64_t slot = 2 * (int64_t)(c0 + p) + (p == 0 ? 1 : 0);
+      const float2 ml = a.part_ml[slot * R + r];
+      const float* src = a.part_o + (slot * R + r) * DP + lane * 2;
+      float2 v[V / 2];
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) v[i] = *reinterpret_cast<const float2*>(src + 64 * i);
+      const float mn = fmaxf(m, ml.x), ms = mn == -INFINITY ? 0.f : mn;
+      const float f0 = exp2_(m - ms), f1 = exp2_(ml.x - ms);
+      l = l * f0 + ml.y * f1;
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        o[2 * i] = o[2 * i] * f0 + v[i].x * f1;
+        o[2 * i + 1] = o[2 * i + 1] * f0 + v[i].y * f1;
+      }
+      m = mn;
+    }
+    __syncthreads();
+    if (lane == 0) ml_sh[warp] = make_float2(m, l);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) *reinterpret_cast<float2*>(&o_sh[warp][64 * i + 2 * lane]) = make_float2(o[2 * i], o[2 * i + 1]);
+    __syncthreads();
+    float M = -INFINITY, L = 0.f, f[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) M = fmaxf(M, ml_sh[w].x);
+    const float ms = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      f[w] = exp2_(ml_sh[w].x - ms);
+      L += ml_sh[w].y * f[w];
+    }
+    const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+    const int pr = k0.w + r, t = k0.y + pr / a.group, h = k0.z * a.group + pr % a.group;
+    const int D = a.pg.head_dim;
+    for (int d = threadIdx.x; d < D; d += 128) {
+      float x = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) x += o_sh[w][d] * f[w];
+      x *= inv;
+      const int64_t at = (int64_t)t * a.out_stride + (int64_t)h * D + d;
+      if (a.out_f32) reinterpret_cast<float*>(a.out)[at] = x;
+      else reinterpret_cast<uint16_t*>(a.out)[at] = f2bf(x);
+    }
+    if (threadIdx.x == 0 && a.lse)
+      a.lse[(int64_t)t * a.q_heads + h] = L > 0.f || L != L ? (ms + log2f(L)) * 0.6931471805599453f : -INFINITY;
+  }
+}
+
+// Launchers (k_attn_rows.cu, k_attn_tile.cu): the main kernel and the join.
+struct AttnPlanSize {
+  int ctas, rows, dp;
+};
+mt_status launch_attn_rows(AttnArgs a, void* ws, const Launch& l, const DeviceInfo* di);
+size_t attn_rows_ws(int head_dim, int sms);
+
+}  // namespace mt

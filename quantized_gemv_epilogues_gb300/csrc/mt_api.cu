@@ -16,7 +16,8 @@ static std::atomic<int> g_opt_gemv{0};
 static std::atomic<int> g_opt_barrier_extra{0};
 static std::atomic<int> g_opt_act_bits{16};
 
-// Device error word: kernels with bounded waits record MT_ERR_TIMEOUT here.
+// Device error word: kernels with bounded waits record MT_ERR_TIMEOUT here, the
+// paged-cache kernels MT_ERR_PAGE.
 __device__ int g_device_error;
 
 // Looked up on every call (no allocation, no synchronisation): a cached
@@ -367,6 +368,7 @@ const char* mt_status_string(mt_status s) {
     case MT_ERR_ALIAS: return "MT_ERR_ALIAS: output overlaps an input";
     case MT_ERR_CUDA: return "MT_ERR_CUDA: a CUDA runtime call failed";
     case MT_ERR_TIMEOUT: return "MT_ERR_TIMEOUT: a bounded device wait expired";
+    case MT_ERR_PAGE: return "MT_ERR_PAGE: a page index read on the device is out of range";
     default: return "unknown mt_status";
   }
 }
