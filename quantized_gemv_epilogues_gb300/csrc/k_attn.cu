@@ -2,9 +2,20 @@
 // the choice of kernel.
 #include <math.h>
 
+#include <algorithm>
+
 #include "k_attn.cuh"
 
 using namespace mt;
+
+namespace {
+
+size_t attn_ws(int head_dim, const DeviceInfo* di) {
+  const int sms = di ? di->sm_count : 152;
+  return std::max(attn_rows_ws(head_dim, sms), attn_tile_ws(head_dim, sms));
+}
+
+}  // namespace
 
 extern "C" {
 
@@ -12,7 +23,7 @@ size_t mt_paged_attention_workspace_bytes(int T, int B, int q_heads, int kv_head
   if (T < 0 || B < 1 || q_heads < 1 || kv_heads < 1 || head_dim < 16 || head_dim > 256) return 0;
   int derr = 0;
   const DeviceInfo* di = device_info(&derr);
-  return attn_rows_ws(head_dim, di ? di->sm_count : 152);
+  return attn_ws(head_dim, di);
 }
 
 mt_status mt_paged_attention(const void* q, int64_t q_stride, int q_heads, const mt_paged_cache* cache,
@@ -33,7 +44,7 @@ mt_status mt_paged_attention(const void* q, int64_t q_stride, int q_heads, const
     return MT_ERR_ALIGN;
   int derr = 0;
   const DeviceInfo* di = device_info(&derr);
-  const size_t need = attn_rows_ws(D, di ? di->sm_count : 152);
+  const size_t need = attn_ws(D, di);
   if (workspace_bytes < need) return MT_ERR_SHAPE;
   const ByteRange iq = byte_range(q, rows_bytes(T, q_stride, (int64_t)q_heads * D, 2));
   const ByteRange ro = byte_range(out, rows_bytes(T, out_stride, (int64_t)q_heads * D, out_dtype == MT_F32 ? 4 : 2));
@@ -60,6 +71,7 @@ mt_status mt_paged_attention(const void* q, int64_t q_stride, int q_heads, const
   a.window = window;
   a.sinks = sinks;
   const Launch l{(cudaStream_t)stream, mt_get_option(MT_OPT_PDL) != 0};
+  if ((int64_t)batch->max_q * a.group > 16 && attn_tile_takes(a)) return launch_attn_tile(a, workspace, l, di);
   return launch_attn_rows(a, workspace, l, di);
 }
 

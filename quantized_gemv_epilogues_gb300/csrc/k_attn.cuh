@@ -312,10 +312,10 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
 }
 
 // Launchers (k_attn_rows.cu, k_attn_tile.cu): the main kernel and the join.
-struct AttnPlanSize {
-  int ctas, rows, dp;
-};
 mt_status launch_attn_rows(AttnArgs a, void* ws, const Launch& l, const DeviceInfo* di);
 size_t attn_rows_ws(int head_dim, int sms);
+mt_status launch_attn_tile(AttnArgs a, void* ws, const Launch& l, const DeviceInfo* di);
+size_t attn_tile_ws(int head_dim, int sms);
+bool attn_tile_takes(const AttnArgs& a);
 
 }  // namespace mt
