@@ -178,6 +178,9 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return r;
 }
 
+// Bits [0, n), n clamped to 0 .. 32.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
+
 // The piece of a tile that this CTA works on next, as every role sees it.
 struct Segment {
   Cursor c;        // c.i: its first block
@@ -212,6 +215,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   __shared__ __align__(8) uint64_t bars[2 * NS + 11];
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
+  __shared__ Segment seg_sh[2];  // the softmax warpgroups' pieces (in registers they would displace parts of S)
+  __shared__ int more_sh[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto kv_full = [&](int i) { return smem_u32(&bars[i]); };
   auto kv_free = [&](int i) { return smem_u32(&bars[NS + i]); };
@@ -269,8 +274,12 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     return false;
   };
 
-  if (u0 < u1) {
-    if (warp == AT_TMA) {
+  // a softmax thread holds a row of S, the other warps need few registers:
+  // 2 x 128 x 208 + 128 x 80 of the launch's 384 x 168
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (u0 >= u1) {
+    } else if (warp == AT_TMA) {
       // ---- K and V blocks
       const int boxes = AT_BK / box_rows;
       int st = 0;             // blocks asked for (K and V each count)
@@ -418,7 +427,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       } while (ok && seg_next(a, g));
       commit(mma_done);  // completes when every MMA issued above has
       (void)mbar_wait_bounded(mma_done, 0);
-    } else if (warp < 8) {
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if (u0 < u1) {
       // ---- softmax of tile s, row r
       const int s = warp >> 2, r = tid & 127, G = a.group, tps = a.tile_tokens >> 1;
       const uint32_t lanes = tbase + ((uint32_t)((warp & 3) * 32) << 16);
@@ -427,19 +439,31 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       const uint64_t c2 = pair(c, c);
       uint32_t sp = 0, op = 0;  // s_full and o_full phases passed
       bool ok = true;
+      const Segment& sg = seg_sh[s];
+      if (r == 0) seg_sh[s] = g;
+      auto wg_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + s) : "memory"); };
+      // the next piece, for the whole warpgroup; false at the end (or after an abort of any of its warps)
+      auto advance = [&]() -> bool {
+        wg_sync();
+        if (r == 0) more_sh[s] = !*abort_flag && seg_next(a, seg_sh[s]);
+        wg_sync();
+        return more_sh[s] != 0;
+      };
+      wg_sync();
       do {
-        const int n = seg_blocks(a, g, s);
-        const int tok0 = g.c.r.i0 + s * tps;
-        if (tok0 > g.c.r.i1) continue;  // no rows
+        if (!ok) continue;
+        const int n = seg_blocks(a, sg, s);
+        const int tok0 = sg.c.r.i0 + s * tps;
+        if (tok0 > sg.c.r.i1) continue;  // no rows of this tile
         const int tok = tok0 + r / G;
-        const bool row = r < tps * G && tok <= g.c.r.i1;
-        const int base = g.c.s.kv - g.c.s.n;  // position of the sequence's first new token
+        const bool row = r < tps * G && tok <= sg.c.r.i1;
+        const int base = sg.c.s.kv - sg.c.s.n;  // position of the sequence's first new token
         const int pos = row ? base + tok : -1;
-        const int pos_first = base + tok0, pos_last = base + min(tok0 + tps - 1, g.c.r.i1);
+        const int pos_first = base + tok0, pos_last = base + min(tok0 + tps - 1, sg.c.r.i1);
         float m = -INFINITY;  // reference maximum, in units of scores
         float l = 0.f;
         for (int j = 0; j < n; ++j) {
-          const int k0 = span_block(g.c.t, g.c.i + j) * AT_BK;
+          const int k0 = span_block(sg.c.t, sg.c.i + j) * AT_BK;
           ok = wait(s_full(s), sp & 1);
           ++sp;
           if (!ok) break;
@@ -453,10 +477,18 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           // every row sees the whole block, unless it reaches past the first row or out of the last row's window
           const bool clear = k0 + AT_BK - 1 <= pos_first && (a.window == 0 || k0 > pos_last - a.window || k0 + AT_BK <= a.sinks);
           if (!clear) {
-            const int hi = pos - k0, lo = a.window ? hi - a.window : -1, sk = a.sinks - k0;
+            // a bit for each key that the row sees: [lo, hi) and the sinks [0, sk).
+            // The empty statement keeps the selects inside the branch (without it
+            // every block paid for them: 2200 of a block's 5800 cycles)
+            asm volatile("");
+            const int hi = pos - k0 + 1, lo = a.window ? hi - a.window : 0, sk = min(a.sinks - k0, hi);
 #pragma unroll
-            for (int i = 0; i < 128; ++i)
-              if (i > hi || (i <= lo && i >= sk)) x[i] = 0xFF800000u;
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t w = (low_bits(hi - 32 * q) & ~low_bits(lo - 32 * q)) | low_bits(sk - 32 * q);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!((w >> i) & 1u)) x[32 * q + i] = 0xFF800000u;
+            }
           }
           float mx[4];
 #pragma unroll
@@ -510,19 +542,19 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(p_full(s));
         }
-        if (!ok) break;
+        if (!ok) continue;
         // ---- the piece's rows
-        const bool whole = g.c.i == 0 && g.left >= g.c.t.n;
+        const bool whole = sg.c.i == 0 && sg.left >= sg.c.t.n;
         if (n > 0) {
           ok = wait(o_full(s), op & 1);
           ++op;
-          if (!ok) break;
+          if (!ok) continue;
           tc_fence_after();
         }
         const float f = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
-        const int D = a.pg.head_dim, h = g.c.h * G + r % G;
-        const int64_t t = g.c.s.row0 + tok;
-        const int64_t slot = (2 * (int64_t)blockIdx.x + (g.c.i == 0 ? 1 : 0)) * AT_R + s * tps * G + r;
+        const int D = a.pg.head_dim, h = sg.c.h * G + r % G;
+        const int64_t t = sg.c.s.row0 + tok;
+        const int64_t slot = (2 * (int64_t)blockIdx.x + (sg.c.i == 0 ? 1 : 0)) * AT_R + s * tps * G + r;
 #pragma unroll
         for (int q = 0; q < DP / 32; ++q) {
           uint32_t o[32];
@@ -556,10 +588,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           if (!whole) a.part_ml[slot] = make_float2(ml, l);
           else if (a.lse) a.lse[t * a.q_heads + h] = l > 0.f || l != l ? ((m == -INFINITY ? 0.f : ml) + log2f(l)) * 0.6931471805599453f : -INFINITY;
         }
-        if (!whole && g.c.i == 0 && tid == 0) put_cut(a, blockIdx.x, (int)((u1 - g.left + g.c.t.n - 1) / per), g.c);
+        if (!whole && sg.c.i == 0 && tid == 0) put_cut(a, blockIdx.x, (int)((u1 - sg.left + sg.c.t.n - 1) / per), sg.c);
         // the reads of O above come before the next piece's products, which this warpgroup's P allows
         tc_fence_before();
-      } while (seg_next(a, g));
+      } while (advance());
     }
   }
   tc_fence_before();
