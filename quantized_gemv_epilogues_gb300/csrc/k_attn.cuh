@@ -240,9 +240,10 @@ __device__ __forceinline__ void put_cut(const AttnArgs& a, int cta, int last, co
 
 __device__ __forceinline__ float exp2_(float x) { return exp2f(x); }
 
-// One CTA of 128 threads joins rows y, y + gridDim.y, ... of the tile cut at
-// the end of CTA x's stretch.  The parts are shared out over the four warps,
-// whose sums are added in order.
+// Joins the tile cut at the end of CTA x's stretch.  A warp takes a row: the
+// parts one after the other, their loads in flight together.  Where a tile has
+// more than eight parts the block's four warps share them out, and add up in
+// order.
 template <int R, int DP>
 __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
   pdl_wait();
@@ -252,18 +253,20 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
   const int c1 = k0.x;
   if (c1 <= c0) return;
   const int rows = a.cut[2 * c0 + 1].x;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int V = DP / 32;  // columns a lane
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, D = a.pg.head_dim;
+  constexpr int V = DP / 32;  // columns a lane, in pairs 64 apart
   __shared__ float o_sh[4][DP];
   __shared__ float2 ml_sh[4];
-  const int parts = c1 - c0 + 1, per = (parts + 3) / 4;
-  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+  const int parts = c1 - c0 + 1;
+  const bool share = parts > 8;
+  const int per = share ? (parts + 3) / 4 : parts, p0 = share ? min(parts, warp * per) : 0, p1 = min(parts, p0 + per);
+  const int step = share ? gridDim.y : 4 * gridDim.y;
+  for (int r = share ? blockIdx.y : blockIdx.y * 4 + warp; r < rows; r += step) {
     float m = -INFINITY, l = 0.f, o[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = 0.f;
-    const int p_end = min(parts, (warp + 1) * per);
 #pragma unroll 4
-    for (int p = warp * per; p < p_end; ++p) {
+    for (int p = p0; p < p1; ++p) {
       const int64_t slot = 2 * (int64_t)(c0 + p) + (p == 0 ? 1 : 0);
       const float2 ml = a.part_ml[slot * R + r];
       const float* src = a.part_o + (slot * R + r) * DP + lane * 2;
@@ -280,34 +283,45 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
       }
       m = mn;
     }
-    __syncthreads();
-    if (lane == 0) ml_sh[warp] = make_float2(m, l);
+    if (share) {
+      __syncthreads();
+      if (lane == 0) ml_sh[warp] = make_float2(m, l);
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) *reinterpret_cast<float2*>(&o_sh[warp][64 * i + 2 * lane]) = make_float2(o[2 * i], o[2 * i + 1]);
-    __syncthreads();
-    float M = -INFINITY, L = 0.f, f[4];
+      for (int i = 0; i < V / 2; ++i) *reinterpret_cast<float2*>(&o_sh[warp][64 * i + 2 * lane]) = make_float2(o[2 * i], o[2 * i + 1]);
+      __syncthreads();
+      if (warp) continue;
+      m = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) M = fmaxf(M, ml_sh[w].x);
-    const float ms = M == -INFINITY ? 0.f : M;
+      for (int w = 0; w < 4; ++w) m = fmaxf(m, ml_sh[w].x);
+      l = 0.f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      f[w] = exp2_(ml_sh[w].x - ms);
-      L += ml_sh[w].y * f[w];
+      for (int i = 0; i < V; ++i) o[i] = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float f = exp2_(ml_sh[w].x - (m == -INFINITY ? 0.f : m));
+        l += ml_sh[w].y * f;
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+          const float2 y = *reinterpret_cast<const float2*>(&o_sh[w][64 * i + 2 * lane]);
+          o[2 * i] += y.x * f;
+          o[2 * i + 1] += y.y * f;
+        }
+      }
     }
-    const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+    const bool any = l > 0.f || l != l;
+    const float inv = any ? 1.f / l : 0.f;
     const int pr = k0.w + r, t = k0.y + pr / a.group, h = k0.z * a.group + pr % a.group;
-    const int D = a.pg.head_dim;
-    for (int d = threadIdx.x; d < D; d += 128) {
-      float x = 0.f;
+    const int64_t at = (int64_t)t * a.out_stride + (int64_t)h * D;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) x += o_sh[w][d] * f[w];
-      x *= inv;
-      const int64_t at = (int64_t)t * a.out_stride + (int64_t)h * D + d;
-      if (a.out_f32) reinterpret_cast<float*>(a.out)[at] = x;
-      else reinterpret_cast<uint16_t*>(a.out)[at] = f2bf(x);
+    for (int i = 0; i < V / 2; ++i) {
+      const int d = 64 * i + 2 * lane;  // D is even
+      if (d < D) {
+        const float x = o[2 * i] * inv, y = o[2 * i + 1] * inv;
+        if (a.out_f32) *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out) + at + d) = make_float2(x, y);
+        else *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.out) + at + d) = (uint32_t)f2bf(x) | ((uint32_t)f2bf(y) << 16);
+      }
     }
-    if (threadIdx.x == 0 && a.lse)
-      a.lse[(int64_t)t * a.q_heads + h] = L > 0.f || L != L ? (ms + log2f(L)) * 0.6931471805599453f : -INFINITY;
+    if (lane == 0 && a.lse) a.lse[(int64_t)t * a.q_heads + h] = any ? ((m == -INFINITY ? 0.f : m) + log2f(l)) * 0.6931471805599453f : -INFINITY;
   }
 }
 

@@ -20,8 +20,11 @@
 //    which TMA fills with zeros.  Rows beyond the sequence's end in its last
 //    page may hold anything: the producer zeroes V's before handing it on (a
 //    weight of zero times NaN is NaN).
-//  * One softmax warpgroup per tile, one row per thread, so that maxima and
-//    sums need no exchange.  The row's reference maximum moves only when a
+//  * Two softmax warpgroups per tile, one row per thread and half of a block's
+//    keys each; the halves of a row exchange their maxima through shared
+//    memory.  (With one warpgroup a tile's chain of S, softmax, P V, S ... is
+//    the bound: 1860 of 3520 cycles a block were softmax latency, against 2048
+//    of MMA for both tiles.)  The row's reference maximum moves only when a
 //    score exceeds it by more than 2^8 (8 in log2 units): fp32 sums and bf16
 //    weights lose nothing by weights up to 2^8, and O is rescaled in tensor
 //    memory only then - once or twice a row, typically.  When S of block j is
@@ -46,8 +49,9 @@ namespace mt {
 
 namespace {
 
-constexpr int AT_BK = 128, AT_R = 256, AT_THREADS = 384;
-constexpr int AT_TMA = 8, AT_MMA = 9, AT_Q = 10;  // warps 0-3 and 4-7: softmax of tile 0 and 1
+constexpr int AT_BK = 128, AT_R = 256, AT_THREADS = 640;
+constexpr int AT_SOFT = 16;  // warps 0-15: softmax; tile warp / 8, columns' half (warp / 4) % 2, rows 32 (warp % 4) on
+constexpr int AT_TMA = 16, AT_MMA = 17, AT_Q = 18, AT_WALK = 19;
 
 template <int DP>
 struct AtShape {
@@ -56,8 +60,6 @@ struct AtShape {
   static constexpr int TILE = CH * HALF;             // a Q tile, or a K or V block
   static constexpr int NS = DP == 128 ? 5 : 10;      // ring stages
   static constexpr size_t OFF_KV = 2 * (size_t)TILE;
-  static constexpr size_t SMEM = 1024 + OFF_KV + (size_t)NS * TILE;
-  static_assert(SMEM <= 226 * 1024, "shared memory plan");
   static_assert((size_t)NS * TILE >= sizeof(PlanShared), "the plan uses the ring's memory");
 };
 
@@ -82,14 +84,6 @@ __device__ __forceinline__ void at_ld_done32(uint32_t* r) {
                  "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
                  "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
                  "+r"(r[29]), "+r"(r[30]), "+r"(r[31]) : : "memory");
-}
-__device__ __forceinline__ void at_st32(uint32_t taddr, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::
-               "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-                 "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-                 "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-                 "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
-                 "r"(r[31]) : "memory");
 }
 __device__ __forceinline__ void at_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::
@@ -181,28 +175,36 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 // Bits [0, n), n clamped to 0 .. 32.
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
 
-// The piece of a tile that this CTA works on next, as every role sees it.
-struct Segment {
-  Cursor c;        // c.i: its first block
-  long long left;  // units of the CTA's stretch from here on
+// A piece of a tile: the part of its blocks that lies in this CTA's stretch.
+// One warp walks the stretch and puts the pieces into a small ring in shared
+// memory for the others (each walking for itself cost them registers and, at
+// every piece, two thousand cycles of index arithmetic).
+struct Piece {
+  int n[2];       // blocks for each of the two 128-row tiles (0: it has no rows, or sees none of them)
+  int first;      // the piece's first block within the tile's
+  int sink, win;  // as TileSpan
+  int key_end, win_lo;
+  int kv, base;   // the sequence's tokens; the position of its first new one
+  int b, h, row0, i0, i1, p0;
+  int whole;      // the tile's only piece: its rows are written, not its parts
+  int stop;       // no piece: the stretch has ended
 };
-// Blocks of the piece for 128-row tile s of the two (0: none, or no rows).
-__device__ __forceinline__ int seg_blocks(const AttnArgs& a, const Segment& g, int s) {
-  const int tps = a.tile_tokens >> 1, first = g.c.r.i0 + s * tps;
-  if (first > g.c.r.i1) return 0;
-  const int last = min(first + tps - 1, g.c.r.i1);
-  const int end = (max(g.c.s.kv - g.c.s.n + last + 1, 0) + AT_BK - 1) / AT_BK;
-  const int all = min(g.c.t.sink, end) + max(0, end - g.c.t.win);
-  return min(max(all - g.c.i, 0), (int)min((long long)(g.c.t.n - g.c.i), g.left));
+constexpr int AT_PIECES = 4;
+
+// What follows the tiles in shared memory (all of it is dynamic, so that the
+// tiles start where it starts, on a 1024-byte boundary).
+struct AtShared {
+  uint64_t bars[2 * 10 + 6 + 4 + 2 + 2 * AT_PIECES];
+  uint32_t tmem;
+  int abort;
+  Piece piece[AT_PIECES];
+  float half[2][2][128];  // a tile's two halves' row maxima (or sums)
+};
+template <int DP>
+constexpr size_t at_smem() {
+  return AtShape<DP>::OFF_KV + (size_t)AtShape<DP>::NS * AtShape<DP>::TILE + sizeof(AtShared);
 }
-// To the next piece; false at the stretch's end.
-__device__ __forceinline__ bool seg_next(const AttnArgs& a, Segment& g) {
-  g.left -= g.c.t.n - g.c.i;
-  if (g.left <= 0) return false;
-  g.c.i = g.c.t.n - 1;
-  cursor_next<AT_R, AT_BK>(a, g.c);
-  return true;
-}
+static_assert(at_smem<128>() <= 227 * 1024 && at_smem<64>() <= 227 * 1024, "shared memory plan");
 
 template <int DP>
 __global__ void __launch_bounds__(AT_THREADS, 1)
@@ -210,21 +212,20 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
                      const __grid_constant__ CUtensorMap vmap, const AttnArgs a, const int box_rows) {
   using S = AtShape<DP>;
   constexpr int NS = S::NS;
-  extern __shared__ unsigned char at_raw[];
-  unsigned char* smem = at_raw + ((1024u - (smem_u32(at_raw) & 1023u)) & 1023u);
-  __shared__ __align__(8) uint64_t bars[2 * NS + 11];
-  __shared__ uint32_t tmem_sh;
-  __shared__ int abort_sh;
-  __shared__ Segment seg_sh[2];  // the softmax warpgroups' pieces (in registers they would displace parts of S)
-  __shared__ int more_sh[2];
+  extern __shared__ __align__(1024) unsigned char smem[];
+  AtShared& sh = *reinterpret_cast<AtShared*>(smem + S::OFF_KV + (size_t)NS * S::TILE);
+  uint64_t* bars = sh.bars;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto kv_full = [&](int i) { return smem_u32(&bars[i]); };
   auto kv_free = [&](int i) { return smem_u32(&bars[NS + i]); };
   auto s_full = [&](int s) { return smem_u32(&bars[2 * NS + s]); };      // S of a block is in tensor memory
   auto p_full = [&](int s) { return smem_u32(&bars[2 * NS + 2 + s]); };  // P is (and O rescaled)
   auto o_full = [&](int s) { return smem_u32(&bars[2 * NS + 4 + s]); };  // O of the piece is complete
-  const uint32_t q_full = smem_u32(&bars[2 * NS + 6]), q_free = smem_u32(&bars[2 * NS + 7]);
-  const uint32_t tail_bar = smem_u32(&bars[2 * NS + 8]), mma_done = smem_u32(&bars[2 * NS + 9]);
+  auto q_full = [&](int s) { return smem_u32(&bars[2 * NS + 6 + s]); };
+  auto q_free = [&](int s) { return smem_u32(&bars[2 * NS + 8 + s]); };
+  const uint32_t tail_bar = smem_u32(&bars[2 * NS + 10]), mma_done = smem_u32(&bars[2 * NS + 11]);
+  auto piece_full = [&](int k) { return smem_u32(&bars[2 * NS + 12 + k % AT_PIECES]); };
+  auto piece_free = [&](int k) { return smem_u32(&bars[2 * NS + 12 + AT_PIECES + k % AT_PIECES]); };
   auto q_tile = [&](int s) { return smem_u32(smem + (size_t)s * S::TILE); };
   auto stage = [&](int i) { return smem_u32(smem + S::OFF_KV + (size_t)i * S::TILE); };
 
@@ -235,245 +236,325 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(s_full(s), 1);
-      mbar_init(p_full(s), 4);  // one arrival per softmax warp
+      mbar_init(p_full(s), 8);  // one arrival per softmax warp
       mbar_init(o_full(s), 1);
+      mbar_init(q_full(s), 1);
+      mbar_init(q_free(s), 1);
     }
-    mbar_init(q_full, 1);
-    mbar_init(q_free, 1);
+    for (int k = 0; k < AT_PIECES; ++k) {
+      mbar_init(piece_full(k), 1);
+      mbar_init(piece_free(k), AT_SOFT + 3);  // one arrival per warp that reads it
+    }
     mbar_init(tail_bar, 1);
     mbar_init(mma_done, 1);
-    abort_sh = 0;
+    sh.abort = 0;
     mbar_fence_init();
   }
   if (warp == AT_MMA) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_sh)));
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   pdl_wait();
   pdl_trigger();
   long long u0, u1, per;
-  Segment g;
-  plan<AT_R, AT_BK, AT_THREADS>(a, reinterpret_cast<PlanShared*>(smem + S::OFF_KV), blockIdx.x, gridDim.x, &u0, &u1, &per, &g.c);
-  g.left = u1 - u0;
+  Cursor c;
+  plan<AT_R, AT_BK, AT_THREADS>(a, reinterpret_cast<PlanShared*>(smem + S::OFF_KV), blockIdx.x, gridDim.x, &u0, &u1, &per, &c);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the plan's accesses before TMA's to the same memory
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = tmem_sh;
-  if (tid == 0) a.cut[2 * blockIdx.x].x = -1;
-  volatile int* abort_flag = &abort_sh;
+  const uint32_t tbase = sh.tmem;
+  volatile int* abort_flag = &sh.abort;
   auto fail = [&]() {
     atomicExch(a.pg.err, (int)MT_ERR_TIMEOUT);
     *abort_flag = 1;
   };
-  // a warp's bounded wait, one answer for all its lanes
-  auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-    const bool ok = mbar_wait_bounded(bar, parity);
-    if (__all_sync(0xffffffffu, ok) && !__any_sync(0xffffffffu, *abort_flag)) return true;
-    fail();
-    return false;
+  // This thread's bounded wait; false after an abort, or if it expires.
+  auto wait1 = [&](uint32_t bar, uint32_t parity) -> bool {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (;;) {
+#pragma unroll 1
+      for (int i = 0; i < 32; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+      if (*abort_flag) return false;
+      if (clock64() - t0 > (1ll << 31)) {
+        fail();
+        return false;
+      }
+    }
   };
+  // a warp's, one answer for all its lanes
+  auto wait = [&](uint32_t bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait1(bar, parity)); };
 
-  // a softmax thread holds a row of S, the other warps need few registers:
-  // 2 x 128 x 208 + 128 x 80 of the launch's 384 x 168
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    if (u0 >= u1) {
+  // a softmax thread holds half a row of S, the other warps need fewer
+  // registers: 512 x 104 + 128 x 64 of the launch's 640 x 96
+  if (warp >= AT_SOFT) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == AT_WALK) {
+      // ---- the stretch's pieces
+      if (lane == 0) {
+        const int tps = a.tile_tokens >> 1;
+        a.cut[2 * blockIdx.x].x = -1;
+        long long left = u1 - u0;
+        for (int k = 0;; ++k) {
+          if (k >= AT_PIECES && !wait1(piece_free(k), ((k / AT_PIECES) + 1) & 1)) break;
+          Piece& p = sh.piece[k % AT_PIECES];
+          p.stop = left <= 0;
+          if (left > 0) {
+            const int n = (int)min((long long)(c.t.n - c.i), left);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              const int first = c.r.i0 + s * tps, last = min(first + tps - 1, c.r.i1);
+              const int end = (max(c.s.kv - c.s.n + last + 1, 0) + AT_BK - 1) / AT_BK;
+              const int all = min(c.t.sink, end) + max(0, end - c.t.win);  // of the tile's blocks, those up to the last token
+              p.n[s] = first > c.r.i1 ? 0 : min(max(all - c.i, 0), n);
+            }
+            p.first = c.i;
+            p.sink = c.t.sink;
+            p.win = c.t.win;
+            p.key_end = c.t.key_end;
+            p.win_lo = c.t.win_lo;
+            p.kv = c.s.kv;
+            p.base = c.s.kv - c.s.n;
+            p.b = c.b;
+            p.h = c.h;
+            p.row0 = c.s.row0;
+            p.i0 = c.r.i0;
+            p.i1 = c.r.i1;
+            p.p0 = c.r.p0;
+            p.whole = n == c.t.n;
+            if (c.i == 0 && n < c.t.n) put_cut(a, blockIdx.x, (int)((u1 - left + c.t.n - 1) / per), c);
+            left -= n;
+          }
+          const bool stop = p.stop;
+          mbar_arrive(piece_full(k));
+          if (stop) break;
+          if (left > 0) {
+            c.i = c.t.n - 1;
+            cursor_next<AT_R, AT_BK>(a, c);
+          }
+        }
+      }
     } else if (warp == AT_TMA) {
       // ---- K and V blocks
       const int boxes = AT_BK / box_rows;
-      int st = 0;             // blocks asked for (K and V each count)
+      int st = 0;  // blocks asked for (K and V each count)
       uint32_t tails = 0;
       bool ok = true;
-      do {
-        const int n = max(seg_blocks(a, g, 0), seg_blocks(a, g, 1));
-        for (int j = 0; ok && j < n; ++j) {
-          const int blk = span_block(g.c.t, g.c.i + j);
-          // this lane's box
-          int page = a.pg.num_pages, row = 0;
-          if (lane < boxes) {
-            const int k0 = blk * AT_BK + lane * box_rows, k1 = k0 + box_rows;
-            if (k0 < g.c.t.key_end && (k1 > g.c.t.win_lo || k0 < a.sinks)) {
-              const int e = k0 / a.pg.page_size, p = paged_entry(a.pg, g.c.b, e);
-              if (p >= 0) page = p;
-              row = k0 - e * a.pg.page_size;
-            }
+      for (int k = 0; ok; ++k) {
+        ok = wait(piece_full(k), (k / AT_PIECES) & 1);
+        const Piece& p = sh.piece[k % AT_PIECES];
+        if (!ok || p.stop) break;
+        const int n = max(p.n[0], p.n[1]), h = p.h;
+        // this lane's box of block j: the table's entry and the row in the page; false if no row sees it
+        auto box = [&](int j, int& page, int& row) -> bool {
+          page = a.pg.num_pages;
+          row = 0;
+          const int i = p.first + j, k0 = (i < p.sink ? i : i - p.sink + p.win) * AT_BK + lane * box_rows;
+          if (j < n && lane < boxes && k0 < p.key_end && (k0 + box_rows > p.win_lo || k0 < a.sinks)) {
+            const int e = k0 / a.pg.page_size;
+            page = __ldg(a.pg.pages + (int64_t)p.b * a.pg.pages_ld + e);
+            row = k0 - e * a.pg.page_size;
+            return true;
           }
+          return false;
+        };
+        int page_next, row_next;
+        bool seen_next = box(0, page_next, row_next);
+        for (int j = 0; ok && j < n; ++j) {
+          int page = page_next;
+          const int row = row_next;
+          if (seen_next && (unsigned)page >= (unsigned)a.pg.num_pages) {
+            atomicExch(a.pg.err, (int)MT_ERR_PAGE);
+            page = a.pg.num_pages;  // zeros, as for a box that no row sees
+          }
+          seen_next = box(j + 1, page_next, row_next);  // its load returns while this block is asked for
+          const int i = p.first + j, k0 = (i < p.sink ? i : i - p.sink + p.win) * AT_BK;
           // rows of the block beyond the sequence's end that a box still reads
-          const int tail0 = g.c.s.kv - blk * AT_BK, tail1 = min((tail0 + box_rows - 1) / box_rows * box_rows, AT_BK);
+          const int tail0 = p.kv - k0, tail1 = min((tail0 + box_rows - 1) / box_rows * box_rows, AT_BK);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
-            const int i = st % NS;
-            if (st >= NS) ok = wait(kv_free(i), ((st / NS) + 1) & 1);
+            const int q = st % NS;
+            if (st >= NS) ok = wait(kv_free(q), ((st / NS) + 1) & 1);
             if (!ok) break;
             const bool patch = kv == 1 && tail0 < AT_BK && tail0 > 0 && tail1 > tail0;
-            const uint32_t bar = patch ? tail_bar : kv_full(i), dst = stage(i);
+            const uint32_t bar = patch ? tail_bar : kv_full(q), dst = stage(q);
             if (lane == 0) mbar_arrive_expect_tx(bar, S::TILE);
             __syncwarp();
             if (lane < boxes) {
 #pragma unroll
               for (int c = 0; c < S::CH; ++c)
-                tma_load_4d(dst + c * S::HALF + lane * box_rows * 128, kv ? &vmap : &kmap, 64 * c, row, g.c.h, page, bar);
+                tma_load_4d(dst + c * S::HALF + lane * box_rows * 128, kv ? &vmap : &kmap, 64 * c, row, h, page, bar);
             }
             ++st;
             if (patch) {
               ok = wait(tail_bar, tails & 1);
               ++tails;
-              unsigned char* v = smem + S::OFF_KV + (size_t)i * S::TILE;
+              unsigned char* v = smem + S::OFF_KV + (size_t)q * S::TILE;
               for (int x = lane; x < (tail1 - tail0) * 8 * S::CH; x += 32) {
-                const int c = x & 7, r = (x >> 3) % (tail1 - tail0), h = (x >> 3) / (tail1 - tail0);
-                *reinterpret_cast<uint4*>(v + h * S::HALF + (tail0 + r) * 128 + 16 * c) = make_uint4(0, 0, 0, 0);
+                const int c = x & 7, r = (x >> 3) % (tail1 - tail0), hh = (x >> 3) / (tail1 - tail0);
+                *reinterpret_cast<uint4*>(v + hh * S::HALF + (tail0 + r) * 128 + 16 * c) = make_uint4(0, 0, 0, 0);
               }
               asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
               __syncwarp();
-              if (lane == 0) mbar_arrive(kv_full(i));
+              if (lane == 0) mbar_arrive(kv_full(q));
               if (!ok) break;
             }
           }
         }
-      } while (ok && seg_next(a, g));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(piece_free(k));
+      }
       // copies still in flight (only after an abort) land before the CTA ends
-      for (int k = max(0, st - NS); !ok && k < st; ++k) (void)mbar_wait_bounded(kv_full(k % NS), (k / NS) & 1);
+      for (int i = max(0, st - NS); !ok && i < st; ++i) (void)mbar_wait_bounded(kv_full(i % NS), (i / NS) & 1);
     } else if (warp == AT_Q) {
       // ---- Q tiles, once the last piece's S products are done with them
-      int k = 0;
-      bool ok = true;
-      do {
-        const int n0 = seg_blocks(a, g, 0), n1 = seg_blocks(a, g, 1);
-        if (n0 == 0 && n1 == 0) continue;
-        if (k > 0) ok = wait(q_free, (k + 1) & 1);
-        if (!ok) break;
-        if (lane == 0) {
-          const int tps = a.tile_tokens >> 1;
-          const uint32_t bytes = (uint32_t)(S::CH * 128 * a.group * tps);
-          mbar_arrive_expect_tx(q_full, bytes * ((n0 > 0) + (n1 > 0)));
-          for (int s = 0; s < 2; ++s)
-            if ((s ? n1 : n0) > 0)
-              for (int c = 0; c < S::CH; ++c)
-                tma_load_3d(q_tile(s) + c * S::HALF, &qmap, 64 * c, g.c.h * a.group, g.c.s.row0 + g.c.r.i0 + s * tps, q_full);
+      if (lane == 0) {
+        const int tps = a.tile_tokens >> 1;
+        uint32_t asked[2] = {0, 0};
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+          ok = wait1(piece_full(k), (k / AT_PIECES) & 1);
+          const Piece& p = sh.piece[k % AT_PIECES];
+          if (!ok || p.stop) break;
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (!ok || p.n[s] == 0) continue;
+            if (asked[s] > 0) ok = wait1(q_free(s), (asked[s] + 1) & 1);
+            if (!ok) continue;
+            mbar_arrive_expect_tx(q_full(s), (uint32_t)(S::CH * 128 * a.group * tps));
+            for (int c = 0; c < S::CH; ++c)
+              tma_load_3d(q_tile(s) + c * S::HALF, &qmap, 64 * c, p.h * a.group, p.row0 + p.i0 + s * tps, q_full(s));
+            ++asked[s];
+          }
+          mbar_arrive(piece_free(k));
         }
-        __syncwarp();
-        ++k;
-      } while (seg_next(a, g));
-      if (!ok && k > 0) (void)mbar_wait_bounded(q_full, (k - 1) & 1);
-    } else if (warp == AT_MMA) {
-      // ---- the products; the whole warp walks, one elected lane issues
-      int st = 0, k = 0;
-      uint32_t pp[2] = {0, 0};  // p_full phases passed
-      bool ok = true;
-      auto qk = [&](int s, int i) {  // S_s = Q_s K^T, K in stage i
-        if (elect_one()) {
+        for (int s = 0; s < 2; ++s)
+          if (!ok && asked[s] > 0) (void)mbar_wait_bounded(q_full(s), (asked[s] - 1) & 1);
+      }
+    } else {
+      // ---- the products, all issued by one lane
+      if (elect_one()) {
+        int st = 0;
+        uint32_t pp[2] = {0, 0}, qq[2] = {0, 0};  // p_full and q_full phases passed
+        auto qk = [&](int s, int i) {  // S_s = Q_s K^T, K in stage i
 #pragma unroll
           for (int ks = 0; ks < DP / 16; ++ks) {
             const uint32_t o = (uint32_t)((ks >> 2) * S::HALF + (ks & 3) * 32);
             at_mma_ss(tbase + 128 * s, pf_desc_sw128(q_tile(s) + o), pf_desc_sw128(stage(i) + o), at_idesc(128, false), ks > 0);
           }
           tc_commit(s_full(s));
-        }
-        __syncwarp();
-      };
-      auto commit = [&](uint32_t bar) {
-        if (elect_one()) tc_commit(bar);
-        __syncwarp();
-      };
-      do {
-        const int n[2] = {seg_blocks(a, g, 0), seg_blocks(a, g, 1)};
-        const int nb = max(n[0], n[1]);
-        if (nb == 0) continue;
-        ok = wait(q_full, k & 1) && wait(kv_full(st % NS), (st / NS) & 1);
-        ++k;
-        if (!ok) break;
-        tc_fence_after();
-        for (int s = 0; s < 2; ++s)
-          if (n[s] > 0) qk(s, st % NS);
-        commit(kv_free(st % NS));
-        if (nb == 1) commit(q_free);
-        ++st;
-        for (int j = 0; ok && j < nb; ++j) {
-          const int iv = st % NS, ik = (st + 1) % NS;
-          ok = wait(kv_full(iv), (st / NS) & 1);
-          bool have_k = false;
-          for (int s = 0; ok && s < 2; ++s) {
-            if (j >= n[s]) continue;
-            ok = wait(p_full(s), pp[s] & 1);
-            ++pp[s];
-            if (!ok) break;
+        };
+        auto products = [&](int n0, int n1) -> bool {  // one piece's
+          const int nb = max(n0, n1);
+          if (!wait1(kv_full(st % NS), (st / NS) & 1)) return false;
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const int n = s ? n1 : n0;
+            if (n == 0) continue;
+            if (!wait1(q_full(s), qq[s] & 1)) return false;
+            ++qq[s];
             tc_fence_after();
-            if (elect_one()) {
+            qk(s, st % NS);
+            if (n == 1) tc_commit(q_free(s));
+          }
+          tc_commit(kv_free(st % NS));
+          ++st;
+          for (int j = 0; j < nb; ++j) {
+            const int iv = st % NS, ik = (st + 1) % NS;
+            if (!wait1(kv_full(iv), (st / NS) & 1)) return false;
+            bool have_k = false;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              const int n = s ? n1 : n0;
+              if (j >= n) continue;
+              if (!wait1(p_full(s), pp[s] & 1)) return false;
+              ++pp[s];
+              tc_fence_after();
 #pragma unroll
               for (int ks = 0; ks < AT_BK / 16; ++ks)
                 at_mma_ts(tbase + 256 + DP * s, tbase + 128 * s + 8 * ks, at_desc_mn(stage(iv) + ks * 2048, S::HALF),
                           at_idesc(DP, true), j > 0 || ks > 0);
-              if (j + 1 == n[s]) tc_commit(o_full(s));
+              if (j + 1 == n) {
+                tc_commit(o_full(s));
+              } else {
+                if (!have_k && !wait1(kv_full(ik), ((st + 1) / NS) & 1)) return false;
+                have_k = true;
+                tc_fence_after();
+                qk(s, ik);
+                if (j + 2 == n) tc_commit(q_free(s));
+              }
             }
-            __syncwarp();
-            if (j + 1 < n[s]) {
-              if (!have_k) ok = wait(kv_full(ik), ((st + 1) / NS) & 1);
-              have_k = true;
-              if (!ok) break;
-              tc_fence_after();
-              qk(s, ik);
-            }
-          }
-          if (!ok) break;
-          commit(kv_free(iv));
-          ++st;
-          if (j + 1 < nb) {
-            commit(kv_free(ik));
+            tc_commit(kv_free(iv));
             ++st;
-            if (j + 2 == nb) commit(q_free);
+            if (j + 1 < nb) {
+              tc_commit(kv_free(ik));
+              ++st;
+            }
           }
+          return true;
+        };
+        for (int k = 0;; ++k) {
+          if (!wait1(piece_full(k), (k / AT_PIECES) & 1)) break;
+          const Piece& p = sh.piece[k % AT_PIECES];
+          if (p.stop) break;
+          const int n0 = p.n[0], n1 = p.n[1];
+          mbar_arrive(piece_free(k));
+          if ((n0 > 0 || n1 > 0) && !products(n0, n1)) break;
         }
-      } while (ok && seg_next(a, g));
-      commit(mma_done);  // completes when every MMA issued above has
+        tc_commit(mma_done);  // completes when every MMA issued above has
+      }
+      __syncwarp();
       (void)mbar_wait_bounded(mma_done, 0);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    if (u0 < u1) {
-      // ---- softmax of tile s, row r
-      const int s = warp >> 2, r = tid & 127, G = a.group, tps = a.tile_tokens >> 1;
-      const uint32_t lanes = tbase + ((uint32_t)((warp & 3) * 32) << 16);
-      const uint32_t t_s = lanes + 128 * s, t_o = lanes + 256 + DP * s;
-      const float c = a.scale_log2;
-      const uint64_t c2 = pair(c, c);
-      uint32_t sp = 0, op = 0;  // s_full and o_full phases passed
-      bool ok = true;
-      const Segment& sg = seg_sh[s];
-      if (r == 0) seg_sh[s] = g;
-      auto wg_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + s) : "memory"); };
-      // the next piece, for the whole warpgroup; false at the end (or after an abort of any of its warps)
-      auto advance = [&]() -> bool {
-        wg_sync();
-        if (r == 0) more_sh[s] = !*abort_flag && seg_next(a, seg_sh[s]);
-        wg_sync();
-        return more_sh[s] != 0;
-      };
-      wg_sync();
-      do {
-        if (!ok) continue;
-        const int n = seg_blocks(a, sg, s);
-        const int tok0 = sg.c.r.i0 + s * tps;
-        if (tok0 > sg.c.r.i1) continue;  // no rows of this tile
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    // ---- softmax of tile s, row r, keys [64 hf, 64 hf + 64) of each block
+    const int s = warp >> 3, hf = (warp >> 2) & 1, r = tid & 127, G = a.group, tps = a.tile_tokens >> 1;
+    const uint32_t lanes = tbase + ((uint32_t)((warp & 3) * 32) << 16);
+    // this half's scores, its weights, and its columns of O
+    const uint32_t t_s = lanes + 128 * s + 64 * hf, t_p = lanes + 128 * s + 32 * hf, t_o = lanes + 256 + DP * s + (DP / 2) * hf;
+    const float cl = a.scale_log2;
+    uint32_t sp = 0, op = 0;  // s_full and o_full phases passed
+    // a barrier of the tile's two warpgroups, with one answer for all of them:
+    // whether every warp's waits succeeded (after an abort no warp may leave
+    // the others at a barrier)
+    auto all_ok = [&](bool fine) -> bool {
+      uint32_t bad;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.eq.b32 p, %1, 0;\n\t"
+          "barrier.red.or.pred q, %2, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+          : "=r"(bad)
+          : "r"((uint32_t)fine), "r"(1 + s)
+          : "memory");
+      return bad == 0;
+    };
+    for (int k = 0;; ++k) {
+      if (!all_ok(wait1(piece_full(k), (k / AT_PIECES) & 1))) break;
+      const Piece& p = sh.piece[k % AT_PIECES];
+      if (p.stop) break;
+      const int tok0 = p.i0 + s * tps, n = p.n[s];
+      if (tok0 <= p.i1) {  // the tile has rows
         const int tok = tok0 + r / G;
-        const bool row = r < tps * G && tok <= sg.c.r.i1;
-        const int base = sg.c.s.kv - sg.c.s.n;  // position of the sequence's first new token
-        const int pos = row ? base + tok : -1;
-        const int pos_first = base + tok0, pos_last = base + min(tok0 + tps - 1, sg.c.r.i1);
+        const bool row = r < tps * G && tok <= p.i1;
+        const int pos = row ? p.base + tok : -1;
+        const int pos_first = p.base + tok0, pos_last = p.base + min(tok0 + tps - 1, p.i1);
         float m = -INFINITY;  // reference maximum, in units of scores
         float l = 0.f;
+        bool ok = true;
         for (int j = 0; j < n; ++j) {
-          const int k0 = span_block(sg.c.t, sg.c.i + j) * AT_BK;
-          ok = wait(s_full(s), sp & 1);
+          const int i0 = p.first + j, k0 = (i0 < p.sink ? i0 : i0 - p.sink + p.win) * AT_BK;
+          const bool there = wait1(s_full(s), sp & 1);
           ++sp;
-          if (!ok) break;
           tc_fence_after();
           __syncwarp();
-          uint32_t x[128];
+          // after an abort the values mean nothing: the barrier below ends the loop
+          uint32_t x[64];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) at_ld32(t_s + 32 * q, x + 32 * q);
+          for (int q = 0; q < 2; ++q) at_ld32(t_s + 32 * q, x + 32 * q);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) at_ld_done32(x + 32 * q);
+          for (int q = 0; q < 2; ++q) at_ld_done32(x + 32 * q);
           // every row sees the whole block, unless it reaches past the first row or out of the last row's window
           const bool clear = k0 + AT_BK - 1 <= pos_first && (a.window == 0 || k0 > pos_last - a.window || k0 + AT_BK <= a.sinks);
           if (!clear) {
@@ -481,9 +562,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             // The empty statement keeps the selects inside the branch (without it
             // every block paid for them: 2200 of a block's 5800 cycles)
             asm volatile("");
-            const int hi = pos - k0 + 1, lo = a.window ? hi - a.window : 0, sk = min(a.sinks - k0, hi);
+            const int kb = k0 + 64 * hf, hi = pos - kb + 1, lo = a.window ? hi - a.window : 0, sk = min(a.sinks - kb, hi);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
               const uint32_t w = (low_bits(hi - 32 * q) & ~low_bits(lo - 32 * q)) | low_bits(sk - 32 * q);
 #pragma unroll
               for (int i = 0; i < 32; ++i)
@@ -494,35 +575,39 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
 #pragma unroll
           for (int q = 0; q < 4; ++q) mx[q] = __uint_as_float(x[q]);
 #pragma unroll
-          for (int i = 4; i < 124; i += 8)
+          for (int i = 4; i < 60; i += 8)
 #pragma unroll
             for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], __uint_as_float(x[i + q]), __uint_as_float(x[i + 4 + q]));
 #pragma unroll
-          for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], __uint_as_float(x[124 + q]));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], __uint_as_float(x[60 + q]));
+          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          sh.half[s][hf][r] = top;
+          ok = all_ok(there);
+          if (!ok) break;
+          top = fmaxf(top, sh.half[s][hf ^ 1][r]);
           if (j == 0) {
             m = top;
-          } else if (__any_sync(0xffffffffu, (top - m) * c > 8.f)) {
+          } else if (__any_sync(0xffffffffu, (top - m) * cl > 8.f)) {
             const float mn = fmaxf(m, top);
-            const float f = mn == -INFINITY ? 1.f : ex2((m - mn) * c);
+            const float f = mn == -INFINITY ? 1.f : ex2((m - mn) * cl);
             m = mn;
             l *= f;
 #pragma unroll
             for (int q = 0; q < DP / 32; ++q) {
-              uint32_t o[32];
-              at_ld32(t_o + 32 * q, o);
-              at_ld_done32(o);
+              float v[16];
+              uint32_t o[16];
+              tc_ld16_wait(t_o + 16 * q, v);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              at_st32(t_o + 32 * q, o);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(v[i] * f);
+              at_st16(t_o + 16 * q, o);
             }
           }
-          const float b = m == -INFINITY ? 0.f : -m * c;
-          const uint64_t b2 = pair(b, b);
+          const float b = m == -INFINITY ? 0.f : -m * cl;
+          const uint64_t b2 = pair(b, b), c2 = pair(cl, cl);
           uint64_t sum[2] = {0, 0};
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t p[16];
+          for (int q = 0; q < 2; ++q) {
+            uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               float u, v;
@@ -530,34 +615,39 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
               u = ex2(u);
               v = ex2(v);
               sum[i & 1] = add2(sum[i & 1], pair(u, v));
-              p[i] = bf16x2(u, v);
+              w[i] = bf16x2(u, v);
             }
-            at_st16(t_s + 16 * q, p);
+            at_st16(t_p + 16 * q, w);
           }
-          float u0_, u1_;
-          unpair(add2(sum[0], sum[1]), u0_, u1_);
-          l += u0_ + u1_;
           at_st_done();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(p_full(s));
+          float u, v;
+          unpair(add2(sum[0], sum[1]), u, v);
+          l += u + v;
         }
-        if (!ok) continue;
+        if (!ok) break;
         // ---- the piece's rows
-        const bool whole = sg.c.i == 0 && sg.left >= sg.c.t.n;
+        bool there = true;
         if (n > 0) {
-          ok = wait(o_full(s), op & 1);
+          there = wait1(o_full(s), op & 1);
           ++op;
-          if (!ok) continue;
           tc_fence_after();
         }
+        if (!all_ok(there)) break;  // and every maximum of sh.half has been read
+        sh.half[s][hf][r] = l;
+        if (!all_ok(true)) break;
+        l = sh.half[s][0][r] + sh.half[s][1][r];
+        const bool whole = p.whole;
         const float f = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
-        const int D = a.pg.head_dim, h = sg.c.h * G + r % G;
-        const int64_t t = sg.c.s.row0 + tok;
-        const int64_t slot = (2 * (int64_t)blockIdx.x + (sg.c.i == 0 ? 1 : 0)) * AT_R + s * tps * G + r;
+        const int D = a.pg.head_dim, h = p.h * G + r % G;
+        const int64_t t = p.row0 + tok;
+        const int64_t slot = (2 * (int64_t)blockIdx.x + (p.first == 0 ? 1 : 0)) * AT_R + s * tps * G + r;
 #pragma unroll
-        for (int q = 0; q < DP / 32; ++q) {
+        for (int q = 0; q < DP / 64; ++q) {
           uint32_t o[32];
+          const int col = (DP / 2) * hf + 32 * q;  // first of the 32 columns
           __syncwarp();
           if (n > 0) {
             at_ld32(t_o + 32 * q, o);
@@ -567,14 +657,14 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             for (int i = 0; i < 32; ++i) o[i] = 0;
           }
           if (row && !whole) {
-            uint4* dst = reinterpret_cast<uint4*>(a.part_o + slot * DP + 32 * q);
+            uint4* dst = reinterpret_cast<uint4*>(a.part_o + slot * DP + col);
 #pragma unroll
             for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           } else if (row) {
-            uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + t * a.out_stride + (int64_t)h * D + 32 * q;
+            uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + t * a.out_stride + (int64_t)h * D + col;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              if (32 * q + 8 * i < D) {
+              if (col + 8 * i < D) {
                 float y[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(o[8 * i + e]) * f;
@@ -583,15 +673,16 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             }
           }
         }
-        if (row) {
-          const float ml = m == -INFINITY ? m : m * c;
+        if (row && hf == 0) {
+          const float ml = m == -INFINITY ? m : m * cl;
           if (!whole) a.part_ml[slot] = make_float2(ml, l);
           else if (a.lse) a.lse[t * a.q_heads + h] = l > 0.f || l != l ? ((m == -INFINITY ? 0.f : ml) + log2f(l)) * 0.6931471805599453f : -INFINITY;
         }
-        if (!whole && sg.c.i == 0 && tid == 0) put_cut(a, blockIdx.x, (int)((u1 - sg.left + sg.c.t.n - 1) / per), sg.c);
-        // the reads of O above come before the next piece's products, which this warpgroup's P allows
+        // the reads of O above come before the next piece's products, which this tile's P allows
         tc_fence_before();
-      } while (advance());
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(piece_free(k));
     }
   }
   tc_fence_before();
@@ -615,13 +706,12 @@ int at_box(int page_size) { return std::min(page_size & -page_size, AT_BK); }
 
 template <int DP>
 mt_status run_tile(AttnArgs a, void* ws, const Launch& l, const DeviceInfo* di) {
-  using S = AtShape<DP>;
   static std::atomic<bool> set[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e);
   if (dev >= 0 && dev < 64 && !set[dev].load()) {
-    e = cudaFuncSetAttribute(attn_tile_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM);
+    e = cudaFuncSetAttribute(attn_tile_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)at_smem<DP>());
     if (e != cudaSuccess) return cuda_fail(e);
     set[dev].store(true);
   }
@@ -652,7 +742,7 @@ mt_status run_tile(AttnArgs a, void* ws, const Launch& l, const DeviceInfo* di) 
   a.part_ml = reinterpret_cast<float2*>(w);
   w += (size_t)ctas * 2 * AT_R * sizeof(float2);
   a.part_o = reinterpret_cast<float*>(w);
-  if (const mt_status st = launch(attn_tile_kernel<DP>, dim3(ctas), dim3(AT_THREADS), S::SMEM, l, qmap, kmap, vmap, a, box)) return st;
+  if (const mt_status st = launch(attn_tile_kernel<DP>, dim3(ctas), dim3(AT_THREADS), at_smem<DP>(), l, qmap, kmap, vmap, a, box)) return st;
   return launch(attn_join_kernel<AT_R, DP>, dim3(ctas, 32), dim3(128), 0, l, a);
 }
 
