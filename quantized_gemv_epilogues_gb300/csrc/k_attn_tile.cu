@@ -20,11 +20,10 @@
 //    which TMA fills with zeros.  Rows beyond the sequence's end in its last
 //    page may hold anything: the producer zeroes V's before handing it on (a
 //    weight of zero times NaN is NaN).
-//  * Two softmax warpgroups per tile, one row per thread and half of a block's
-//    keys each; the halves of a row exchange their maxima through shared
-//    memory.  (With one warpgroup a tile's chain of S, softmax, P V, S ... is
-//    the bound: 1860 of 3520 cycles a block were softmax latency, against 2048
-//    of MMA for both tiles.)  The row's reference maximum moves only when a
+//  * One softmax warpgroup per tile, one row per thread, so that maxima and
+//    sums need no exchange and no warp waits for another.  (Two warpgroups a
+//    tile, half a row per thread, cost more in the exchange than the shorter
+//    rows gained: 521 against XXX us for a prompt of 8000.)  The row's reference maximum moves only when a
 //    score exceeds it by more than 2^8 (8 in log2 units): fp32 sums and bf16
 //    weights lose nothing by weights up to 2^8, and O is rescaled in tensor
 //    memory only then - once or twice a row, typically.  When S of block j is
@@ -49,9 +48,9 @@ namespace mt {
 
 namespace {
 
-constexpr int AT_BK = 128, AT_R = 256, AT_THREADS = 640;
-constexpr int AT_SOFT = 16;  // warps 0-15: softmax; tile warp / 8, columns' half (warp / 4) % 2, rows 32 (warp % 4) on
-constexpr int AT_TMA = 16, AT_MMA = 17, AT_Q = 18, AT_WALK = 19;
+constexpr int AT_BK = 128, AT_R = 256, AT_THREADS = 384;
+constexpr int AT_SOFT = 8;  // warps 0-7: softmax; tile warp / 4, rows 32 (warp % 4) on
+constexpr int AT_TMA = 8, AT_MMA = 9, AT_Q = 10, AT_WALK = 11;
 
 template <int DP>
 struct AtShape {
@@ -172,6 +171,26 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return r;
 }
 
+// Eight 16-byte chunks in each of eight neighbouring lanes, transposed: chunk
+// i of lane k moves to chunk k of lane i.
+__device__ __forceinline__ void lane_transpose8(uint32_t* v, int lane) {
+#pragma unroll
+  for (int b = 1; b < 8; b <<= 1) {
+    const bool up = lane & b;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      if (c & b) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t &lo = v[4 * c + e], &hi = v[4 * (c | b) + e];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, b);
+        if (up) lo = got;
+        else hi = got;
+      }
+    }
+  }
+}
+
 // Bits [0, n), n clamped to 0 .. 32.
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
 
@@ -198,7 +217,6 @@ struct AtShared {
   uint32_t tmem;
   int abort;
   Piece piece[AT_PIECES];
-  float half[2][2][128];  // a tile's two halves' row maxima (or sums)
 };
 template <int DP>
 constexpr size_t at_smem() {
@@ -236,7 +254,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(s_full(s), 1);
-      mbar_init(p_full(s), 8);  // one arrival per softmax warp
+      mbar_init(p_full(s), 4);  // one arrival per softmax warp
       mbar_init(o_full(s), 1);
       mbar_init(q_full(s), 1);
       mbar_init(q_free(s), 1);
@@ -287,10 +305,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   // a warp's, one answer for all its lanes
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait1(bar, parity)); };
 
-  // a softmax thread holds half a row of S, the other warps need fewer
-  // registers: 512 x 104 + 128 x 64 of the launch's 640 x 96
+  // a softmax thread holds a row of S, the other warps need fewer registers:
+  // 256 x 216 + 128 x 72 of the launch's 384 x 168
   if (warp >= AT_SOFT) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == AT_WALK) {
       // ---- the stretch's pieces
       if (lane == 0) {
@@ -509,29 +527,15 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       (void)mbar_wait_bounded(mma_done, 0);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-    // ---- softmax of tile s, row r, keys [64 hf, 64 hf + 64) of each block
-    const int s = warp >> 3, hf = (warp >> 2) & 1, r = tid & 127, G = a.group, tps = a.tile_tokens >> 1;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    // ---- softmax of tile s, row r
+    const int s = warp >> 2, r = tid & 127, G = a.group, tps = a.tile_tokens >> 1;
     const uint32_t lanes = tbase + ((uint32_t)((warp & 3) * 32) << 16);
-    // this half's scores, its weights, and its columns of O
-    const uint32_t t_s = lanes + 128 * s + 64 * hf, t_p = lanes + 128 * s + 32 * hf, t_o = lanes + 256 + DP * s + (DP / 2) * hf;
+    const uint32_t t_s = lanes + 128 * s, t_o = lanes + 256 + DP * s;
     const float cl = a.scale_log2;
     uint32_t sp = 0, op = 0;  // s_full and o_full phases passed
-    // a barrier of the tile's two warpgroups, with one answer for all of them:
-    // whether every warp's waits succeeded (after an abort no warp may leave
-    // the others at a barrier)
-    auto all_ok = [&](bool fine) -> bool {
-      uint32_t bad;
-      asm volatile(
-          "{\n\t.reg .pred p, q;\n\tsetp.eq.b32 p, %1, 0;\n\t"
-          "barrier.red.or.pred q, %2, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-          : "=r"(bad)
-          : "r"((uint32_t)fine), "r"(1 + s)
-          : "memory");
-      return bad == 0;
-    };
     for (int k = 0;; ++k) {
-      if (!all_ok(wait1(piece_full(k), (k / AT_PIECES) & 1))) break;
+      if (!wait(piece_full(k), (k / AT_PIECES) & 1)) break;
       const Piece& p = sh.piece[k % AT_PIECES];
       if (p.stop) break;
       const int tok0 = p.i0 + s * tps, n = p.n[s];
@@ -545,16 +549,15 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         bool ok = true;
         for (int j = 0; j < n; ++j) {
           const int i0 = p.first + j, k0 = (i0 < p.sink ? i0 : i0 - p.sink + p.win) * AT_BK;
-          const bool there = wait1(s_full(s), sp & 1);
+          ok = wait(s_full(s), sp & 1);
           ++sp;
+          if (!ok) break;
           tc_fence_after();
-          __syncwarp();
-          // after an abort the values mean nothing: the barrier below ends the loop
-          uint32_t x[64];
+          uint32_t x[128];
 #pragma unroll
-          for (int q = 0; q < 2; ++q) at_ld32(t_s + 32 * q, x + 32 * q);
+          for (int q = 0; q < 4; ++q) at_ld32(t_s + 32 * q, x + 32 * q);
 #pragma unroll
-          for (int q = 0; q < 2; ++q) at_ld_done32(x + 32 * q);
+          for (int q = 0; q < 4; ++q) at_ld_done32(x + 32 * q);
           // every row sees the whole block, unless it reaches past the first row or out of the last row's window
           const bool clear = k0 + AT_BK - 1 <= pos_first && (a.window == 0 || k0 > pos_last - a.window || k0 + AT_BK <= a.sinks);
           if (!clear) {
@@ -562,9 +565,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             // The empty statement keeps the selects inside the branch (without it
             // every block paid for them: 2200 of a block's 5800 cycles)
             asm volatile("");
-            const int kb = k0 + 64 * hf, hi = pos - kb + 1, lo = a.window ? hi - a.window : 0, sk = min(a.sinks - kb, hi);
+            const int hi = pos - k0 + 1, lo = a.window ? hi - a.window : 0, sk = min(a.sinks - k0, hi);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
+            for (int q = 0; q < 4; ++q) {
               const uint32_t w = (low_bits(hi - 32 * q) & ~low_bits(lo - 32 * q)) | low_bits(sk - 32 * q);
 #pragma unroll
               for (int i = 0; i < 32; ++i)
@@ -575,16 +578,12 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
 #pragma unroll
           for (int q = 0; q < 4; ++q) mx[q] = __uint_as_float(x[q]);
 #pragma unroll
-          for (int i = 4; i < 60; i += 8)
+          for (int i = 4; i < 124; i += 8)
 #pragma unroll
             for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], __uint_as_float(x[i + q]), __uint_as_float(x[i + 4 + q]));
 #pragma unroll
-          for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], __uint_as_float(x[60 + q]));
-          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          sh.half[s][hf][r] = top;
-          ok = all_ok(there);
-          if (!ok) break;
-          top = fmaxf(top, sh.half[s][hf ^ 1][r]);
+          for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], __uint_as_float(x[124 + q]));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           if (j == 0) {
             m = top;
           } else if (__any_sync(0xffffffffu, (top - m) * cl > 8.f)) {
@@ -593,7 +592,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             m = mn;
             l *= f;
 #pragma unroll
-            for (int q = 0; q < DP / 32; ++q) {
+            for (int q = 0; q < DP / 16; ++q) {
               float v[16];
               uint32_t o[16];
               tc_ld16_wait(t_o + 16 * q, v);
@@ -606,7 +605,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           const uint64_t b2 = pair(b, b), c2 = pair(cl, cl);
           uint64_t sum[2] = {0, 0};
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
+          for (int q = 0; q < 4; ++q) {
             uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -617,7 +616,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
               sum[i & 1] = add2(sum[i & 1], pair(u, v));
               w[i] = bf16x2(u, v);
             }
-            at_st16(t_p + 16 * q, w);
+            at_st16(t_s + 16 * q, w);
           }
           at_st_done();
           tc_fence_before();
@@ -629,51 +628,68 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         }
         if (!ok) break;
         // ---- the piece's rows
-        bool there = true;
         if (n > 0) {
-          there = wait1(o_full(s), op & 1);
+          ok = wait(o_full(s), op & 1);
           ++op;
+          if (!ok) break;
           tc_fence_after();
         }
-        if (!all_ok(there)) break;  // and every maximum of sh.half has been read
-        sh.half[s][hf][r] = l;
-        if (!all_ok(true)) break;
-        l = sh.half[s][0][r] + sh.half[s][1][r];
         const bool whole = p.whole;
         const float f = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
         const int D = a.pg.head_dim, h = p.h * G + r % G;
         const int64_t t = p.row0 + tok;
         const int64_t slot = (2 * (int64_t)blockIdx.x + (p.first == 0 ? 1 : 0)) * AT_R + s * tps * G + r;
+        // A row's columns lie in one thread, and a store of 16 bytes by each of
+        // 32 rows is 32 requests to L2: chunks of 16 bytes are transposed between
+        // lanes, so that 8 lanes write one row's 128 contiguous bytes.
+        const unsigned rows_here = __ballot_sync(0xffffffffu, row);
+        uint32_t o[32];
 #pragma unroll
-        for (int q = 0; q < DP / 64; ++q) {
-          uint32_t o[32];
-          const int col = (DP / 2) * hf + 32 * q;  // first of the 32 columns
-          __syncwarp();
-          if (n > 0) {
-            at_ld32(t_o + 32 * q, o);
-            at_ld_done32(o);
+        for (int c0 = 0; c0 < DP; c0 += 64) {
+          if (whole) {  // 64 columns as bf16, 128 bytes
+            uint32_t w[32];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              if (n > 0) {
+                at_ld32(t_o + c0 + 32 * q, o);
+                at_ld_done32(o);
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                w[16 * q + i] = n > 0 ? bf16x2(__uint_as_float(o[2 * i]) * f, __uint_as_float(o[2 * i + 1]) * f) : 0u;
+            }
+            lane_transpose8(w, lane);
+            const int64_t at = t * a.out_stride + (int64_t)h * D;
+            const int col = c0 + 8 * (lane & 7);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int src = (lane & ~7) + i;
+              const int64_t to = __shfl_sync(0xffffffffu, at, src);
+              if (((rows_here >> src) & 1u) && col < D)
+                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + to + col) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            }
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0;
-          }
-          if (row && !whole) {
-            uint4* dst = reinterpret_cast<uint4*>(a.part_o + slot * DP + col);
+            for (int q = 0; q < 2; ++q) {  // 32 columns as fp32, 128 bytes
+              if (n > 0) {
+                at_ld32(t_o + c0 + 32 * q, o);
+                at_ld_done32(o);
+              } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          } else if (row) {
-            uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + t * a.out_stride + (int64_t)h * D + col;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (col + 8 * i < D) {
-                float y[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(o[8 * i + e]) * f;
-                *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(bf16x2(y[0], y[1]), bf16x2(y[2], y[3]), bf16x2(y[4], y[5]), bf16x2(y[6], y[7]));
+                for (int i = 0; i < 32; ++i) o[i] = 0;
               }
+              lane_transpose8(o, lane);
+              const int64_t base = slot - (lane & 7);  // the part's row of the lane group's first lane
+              const int col = c0 + 32 * q + 4 * (lane & 7);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if ((rows_here >> ((lane & ~7) + i)) & 1u)
+                  *reinterpret_cast<uint4*>(a.part_o + (base + i) * DP + col) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
             }
           }
+          __syncwarp();
         }
-        if (row && hf == 0) {
+        if (row) {
           const float ml = m == -INFINITY ? m : m * cl;
           if (!whole) a.part_ml[slot] = make_float2(ml, l);
           else if (a.lse) a.lse[t * a.q_heads + h] = l > 0.f || l != l ? ((m == -INFINITY ? 0.f : ml) + log2f(l)) * 0.6931471805599453f : -INFINITY;
