@@ -17,6 +17,9 @@
 // this balances every mixture to one block.  A tile that a stretch boundary
 // cuts leaves parts in the workspace (at most two per CTA), which a second
 // kernel joins in key order; the sum's order depends only on the lengths.
+// A tile also has EXTRA units before its blocks, which stand for the time that
+// its start and its output take: a stretch that begins or ends among them
+// begins or ends at the tile's first block.
 #pragma once
 #include <float.h>
 
@@ -127,9 +130,10 @@ struct PlanShared {
 };
 
 // Units of every sequence, their running sums, and the start of this CTA's
-// stretch: [u0, u1) of all units, `per` to a CTA.  Every thread of the block
+// stretch: [u0, u1) of all units, `per` to a CTA; cur->i counts the tile's
+// units, the EXTRA ones first.  Every thread of the block
 // (NT of them) calls it and gets the same answers; ends with a barrier.
-template <int R, int BK, int NT>
+template <int R, int BK, int NT, int EXTRA>
 __device__ void plan(const AttnArgs& a, PlanShared* sh, int cta, int ctas, long long* u0, long long* u1, long long* per,
                      Cursor* cur) {
   const PagedArgs& pg = a.pg;
@@ -144,7 +148,7 @@ __device__ void plan(const AttnArgs& a, PlanShared* sh, int cta, int ctas, long 
     if (tiles <= 4) {
       for (int rt = 0; rt < tiles; ++rt) {
         const TileRows r = tile_rows<R>(a, s, rt);
-        n += tile_span<BK>(s, r.i0, r.i1, a.window, a.sinks).n;
+        n += tile_span<BK>(s, r.i0, r.i1, a.window, a.sinks).n + EXTRA;
       }
     } else {
       sh->big[atomicAdd(&sh->n_big, 1)] = b;
@@ -159,7 +163,7 @@ __device__ void plan(const AttnArgs& a, PlanShared* sh, int cta, int ctas, long 
     long long n = 0;
     for (int rt = tid; rt < tiles; rt += NT) {
       const TileRows r = tile_rows<R>(a, s, rt);
-      n += tile_span<BK>(s, r.i0, r.i1, a.window, a.sinks).n;
+      n += tile_span<BK>(s, r.i0, r.i1, a.window, a.sinks).n + EXTRA;
     }
     atomicAdd(reinterpret_cast<unsigned long long*>(&sh->pre[b + 1]), (unsigned long long)(n * pg.kv_heads));
   }
@@ -208,7 +212,7 @@ __device__ void plan(const AttnArgs& a, PlanShared* sh, int cta, int ctas, long 
       long long n = 0;
       if (rt < c.tiles) {
         const TileRows r = tile_rows<R>(a, c.s, rt);
-        n = tile_span<BK>(c.s, r.i0, r.i1, a.window, a.sinks).n;
+        n = tile_span<BK>(c.s, r.i0, r.i1, a.window, a.sinks).n + EXTRA;
       }
       long long in = n;
 #pragma unroll

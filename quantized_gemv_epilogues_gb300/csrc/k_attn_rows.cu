@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(AR_THREADS, ArShape<DP>::PER_SM) attn_rows_ker
   pdl_trigger();
   long long u0, u1, per;
   Cursor ld;  // of the block whose page indices are fetched next
-  plan<AR_R, AR_BK, AR_THREADS>(a, reinterpret_cast<PlanShared*>(ring), cta, ctas, &u0, &u1, &per, &ld);
+  plan<AR_R, AR_BK, AR_THREADS, 0>(a, reinterpret_cast<PlanShared*>(ring), cta, ctas, &u0, &u1, &per, &ld);
   if (tid == 0) a.cut[2 * cta].x = -1;
   if (u0 >= u1) return;
   const int units = (int)(u1 - u0);

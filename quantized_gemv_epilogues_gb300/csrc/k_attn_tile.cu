@@ -49,6 +49,7 @@ namespace mt {
 namespace {
 
 constexpr int AT_BK = 128, AT_R = 256, AT_THREADS = 384;
+constexpr int AT_EXTRA = 3;  // units of a tile beside its blocks: the blocks that its start and output take as long as
 constexpr int AT_SOFT = 8;  // warps 0-7: softmax; tile warp / 4, rows 32 (warp % 4) on
 constexpr int AT_TMA = 8, AT_MMA = 9, AT_Q = 10, AT_WALK = 11;
 
@@ -57,8 +58,9 @@ struct AtShape {
   static constexpr int CH = DP / 64;                 // 64-element column halves (one 128-byte swizzle row each)
   static constexpr int HALF = 128 * 128;             // 128 rows of 128 bytes
   static constexpr int TILE = CH * HALF;             // a Q tile, or a K or V block
-  static constexpr int NS = DP == 128 ? 5 : 10;      // ring stages
+  static constexpr int NS = DP == 128 ? 4 : 8;       // ring stages
   static constexpr size_t OFF_KV = 2 * (size_t)TILE;
+  static constexpr size_t OFF_OUT = OFF_KV + (size_t)NS * TILE;  // 128 bytes of each softmax thread's row, on their way out
   static_assert((size_t)NS * TILE >= sizeof(PlanShared), "the plan uses the ring's memory");
 };
 
@@ -171,25 +173,30 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return r;
 }
 
-// Eight 16-byte chunks in each of eight neighbouring lanes, transposed: chunk
-// i of lane k moves to chunk k of lane i.
-__device__ __forceinline__ void lane_transpose8(uint32_t* v, int lane) {
+// Eight 16-byte chunks rotated by the lane: chunk i becomes chunk (i + lane) % 8.
+__device__ __forceinline__ void rotate8(uint32_t* v, int lane) {
 #pragma unroll
   for (int b = 1; b < 8; b <<= 1) {
-    const bool up = lane & b;
+    const bool on = lane & b;
+    uint32_t w[32];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      if (c & b) continue;
+    for (int i = 0; i < 32; ++i) w[i] = on ? v[(i + 4 * b) & 31] : v[i];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint32_t &lo = v[4 * c + e], &hi = v[4 * (c | b) + e];
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, b);
-        if (up) lo = got;
-        else hi = got;
-      }
-    }
+    for (int i = 0; i < 32; ++i) v[i] = w[i];
   }
 }
+__device__ __forceinline__ void st_shared16(uint32_t p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// One thread's bulk copy shared -> global (16-byte aligned, a multiple of 16
+// bytes), the wait until its copies have read their sources, and until they
+// are done.
+__device__ __forceinline__ void bulk_s2g(void* dst, uint32_t src, int bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_reads_done() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Bits [0, n), n clamped to 0 .. 32.
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
@@ -213,14 +220,14 @@ constexpr int AT_PIECES = 4;
 // What follows the tiles in shared memory (all of it is dynamic, so that the
 // tiles start where it starts, on a 1024-byte boundary).
 struct AtShared {
-  uint64_t bars[2 * 10 + 6 + 4 + 2 + 2 * AT_PIECES];
+  uint64_t bars[2 * 10 + 6 + 4 + 2 + 2 * AT_PIECES + 2];
   uint32_t tmem;
   int abort;
   Piece piece[AT_PIECES];
 };
 template <int DP>
 constexpr size_t at_smem() {
-  return AtShape<DP>::OFF_KV + (size_t)AtShape<DP>::NS * AtShape<DP>::TILE + sizeof(AtShared);
+  return AtShape<DP>::OFF_OUT + 256 * 128 + sizeof(AtShared);
 }
 static_assert(at_smem<128>() <= 227 * 1024 && at_smem<64>() <= 227 * 1024, "shared memory plan");
 
@@ -231,7 +238,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   using S = AtShape<DP>;
   constexpr int NS = S::NS;
   extern __shared__ __align__(1024) unsigned char smem[];
-  AtShared& sh = *reinterpret_cast<AtShared*>(smem + S::OFF_KV + (size_t)NS * S::TILE);
+  AtShared& sh = *reinterpret_cast<AtShared*>(smem + S::OFF_OUT + 256 * 128);
   uint64_t* bars = sh.bars;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto kv_full = [&](int i) { return smem_u32(&bars[i]); };
@@ -239,6 +246,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   auto s_full = [&](int s) { return smem_u32(&bars[2 * NS + s]); };      // S of a block is in tensor memory
   auto p_full = [&](int s) { return smem_u32(&bars[2 * NS + 2 + s]); };  // P is (and O rescaled)
   auto o_full = [&](int s) { return smem_u32(&bars[2 * NS + 4 + s]); };  // O of the piece is complete
+  auto p_half = [&](int s) { return smem_u32(&bars[2 * NS + 12 + 2 * AT_PIECES + s]); };  // P of the block's first 64 keys is
   auto q_full = [&](int s) { return smem_u32(&bars[2 * NS + 6 + s]); };
   auto q_free = [&](int s) { return smem_u32(&bars[2 * NS + 8 + s]); };
   const uint32_t tail_bar = smem_u32(&bars[2 * NS + 10]), mma_done = smem_u32(&bars[2 * NS + 11]);
@@ -254,7 +262,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(s_full(s), 1);
-      mbar_init(p_full(s), 4);  // one arrival per softmax warp
+      mbar_init(p_half(s), 4);  // one arrival per softmax warp
+      mbar_init(p_full(s), 4);
       mbar_init(o_full(s), 1);
       mbar_init(q_full(s), 1);
       mbar_init(q_free(s), 1);
@@ -276,7 +285,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   pdl_trigger();
   long long u0, u1, per;
   Cursor c;
-  plan<AT_R, AT_BK, AT_THREADS>(a, reinterpret_cast<PlanShared*>(smem + S::OFF_KV), blockIdx.x, gridDim.x, &u0, &u1, &per, &c);
+  plan<AT_R, AT_BK, AT_THREADS, AT_EXTRA>(a, reinterpret_cast<PlanShared*>(smem + S::OFF_KV), blockIdx.x, gridDim.x, &u0, &u1, &per, &c);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the plan's accesses before TMA's to the same memory
   tc_fence_before();
   __syncthreads();
@@ -314,21 +323,24 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       if (lane == 0) {
         const int tps = a.tile_tokens >> 1;
         a.cut[2 * blockIdx.x].x = -1;
-        long long left = u1 - u0;
+        long long left = u1 - u0;  // units of the stretch from unit c.i of the tile on
         for (int k = 0;; ++k) {
           if (k >= AT_PIECES && !wait1(piece_free(k), ((k / AT_PIECES) + 1) & 1)) break;
           Piece& p = sh.piece[k % AT_PIECES];
-          p.stop = left <= 0;
-          if (left > 0) {
-            const int n = (int)min((long long)(c.t.n - c.i), left);
+          // blocks [i0, i1) of the tile
+          const int all_units = c.t.n + AT_EXTRA, end = (int)min((long long)all_units, c.i + left);
+          const int i0 = max(c.i - AT_EXTRA, 0), i1 = end - AT_EXTRA;
+          const bool stop = left <= 0 || i1 <= 0;  // (a stretch that ends among the extra units leaves the tile to the next)
+          p.stop = stop;
+          if (!stop) {
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
               const int first = c.r.i0 + s * tps, last = min(first + tps - 1, c.r.i1);
-              const int end = (max(c.s.kv - c.s.n + last + 1, 0) + AT_BK - 1) / AT_BK;
-              const int all = min(c.t.sink, end) + max(0, end - c.t.win);  // of the tile's blocks, those up to the last token
-              p.n[s] = first > c.r.i1 ? 0 : min(max(all - c.i, 0), n);
+              const int to = (max(c.s.kv - c.s.n + last + 1, 0) + AT_BK - 1) / AT_BK;
+              const int all = min(c.t.sink, to) + max(0, to - c.t.win);  // of the tile's blocks, those up to the last token
+              p.n[s] = first > c.r.i1 ? 0 : min(max(all - i0, 0), i1 - i0);
             }
-            p.first = c.i;
+            p.first = i0;
             p.sink = c.t.sink;
             p.win = c.t.win;
             p.key_end = c.t.key_end;
@@ -341,13 +353,12 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             p.i0 = c.r.i0;
             p.i1 = c.r.i1;
             p.p0 = c.r.p0;
-            p.whole = n == c.t.n;
-            if (c.i == 0 && n < c.t.n) put_cut(a, blockIdx.x, (int)((u1 - left + c.t.n - 1) / per), c);
-            left -= n;
+            p.whole = i0 == 0 && i1 == c.t.n;
+            if (i0 == 0 && i1 < c.t.n) put_cut(a, blockIdx.x, (int)((u1 - left + all_units - c.i - 1) / per), c);
           }
-          const bool stop = p.stop;
           mbar_arrive(piece_full(k));
           if (stop) break;
+          left -= end - c.i;
           if (left > 0) {
             c.i = c.t.n - 1;
             cursor_next<AT_R, AT_BK>(a, c);
@@ -487,13 +498,16 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             for (int s = 0; s < 2; ++s) {
               const int n = s ? n1 : n0;
               if (j >= n) continue;
-              if (!wait1(p_full(s), pp[s] & 1)) return false;
-              ++pp[s];
-              tc_fence_after();
 #pragma unroll
-              for (int ks = 0; ks < AT_BK / 16; ++ks)
+              for (int ks = 0; ks < AT_BK / 16; ++ks) {
+                if (ks == 0 || ks == AT_BK / 32) {
+                  if (!wait1(ks ? p_full(s) : p_half(s), pp[s] & 1)) return false;
+                  tc_fence_after();
+                }
                 at_mma_ts(tbase + 256 + DP * s, tbase + 128 * s + 8 * ks, at_desc_mn(stage(iv) + ks * 2048, S::HALF),
                           at_idesc(DP, true), j > 0 || ks > 0);
+              }
+              ++pp[s];
               if (j + 1 == n) {
                 tc_commit(o_full(s));
               } else {
@@ -533,6 +547,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     const uint32_t lanes = tbase + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t t_s = lanes + 128 * s, t_o = lanes + 256 + DP * s;
     const float cl = a.scale_log2;
+    const int r_tok = r / G, r_head = r - r_tok * G;
     uint32_t sp = 0, op = 0;  // s_full and o_full phases passed
     for (int k = 0;; ++k) {
       if (!wait(piece_full(k), (k / AT_PIECES) & 1)) break;
@@ -540,7 +555,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       if (p.stop) break;
       const int tok0 = p.i0 + s * tps, n = p.n[s];
       if (tok0 <= p.i1) {  // the tile has rows
-        const int tok = tok0 + r / G;
+        const int tok = tok0 + r_tok;
         const bool row = r < tps * G && tok <= p.i1;
         const int pos = row ? p.base + tok : -1;
         const int pos_first = p.base + tok0, pos_last = p.base + min(tok0 + tps - 1, p.i1);
@@ -591,7 +606,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             const float f = mn == -INFINITY ? 1.f : ex2((m - mn) * cl);
             m = mn;
             l *= f;
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < DP / 16; ++q) {
               float v[16];
               uint32_t o[16];
@@ -617,6 +632,12 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
               w[i] = bf16x2(u, v);
             }
             at_st16(t_s + 16 * q, w);
+            if (q == 1) {  // half of the second product can start
+              at_st_done();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(p_half(s));
+            }
           }
           at_st_done();
           tc_fence_before();
@@ -636,56 +657,45 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         }
         const bool whole = p.whole;
         const float f = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
-        const int D = a.pg.head_dim, h = p.h * G + r % G;
+        const int D = a.pg.head_dim, h = p.h * G + r_head;
         const int64_t t = p.row0 + tok;
         const int64_t slot = (2 * (int64_t)blockIdx.x + (p.first == 0 ? 1 : 0)) * AT_R + s * tps * G + r;
-        // A row's columns lie in one thread, and a store of 16 bytes by each of
-        // 32 rows is 32 requests to L2: chunks of 16 bytes are transposed between
-        // lanes, so that 8 lanes write one row's 128 contiguous bytes.
-        const unsigned rows_here = __ballot_sync(0xffffffffu, row);
-        uint32_t o[32];
+        // A row's columns lie in one thread; written from there, 16 bytes of 32
+        // rows a store, they cost the warps 7000 cycles a piece.  Instead each
+        // thread puts 128 bytes of its row into shared memory and has them
+        // copied out in bulk, while it goes on.
+        const int64_t at = whole ? (t * a.out_stride + (int64_t)h * D) * 2 : slot * DP * 4;  // this row's first byte
+        char* const dst = (whole ? reinterpret_cast<char*>(a.out) : reinterpret_cast<char*>(a.part_o)) + at;
+        auto send = [&](uint32_t* v, int col_bytes) {  // v: 128 bytes; only those within the row are copied
+          rotate8(v, lane);
+          bulk_reads_done();  // the row's last 128 bytes have left
+          const uint32_t buf = smem_u32(smem + S::OFF_OUT + tid * 128);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)  // chunk (i + lane) % 8: eight neighbouring rows write to different banks
+            st_shared16(buf + (((i + lane) & 7) << 4), v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          if (row) bulk_s2g(dst + col_bytes, buf, whole ? min(128, 2 * D - col_bytes) : 128);
+        };
 #pragma unroll
         for (int c0 = 0; c0 < DP; c0 += 64) {
-          if (whole) {  // 64 columns as bf16, 128 bytes
-            uint32_t w[32];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              if (n > 0) {
-                at_ld32(t_o + c0 + 32 * q, o);
-                at_ld_done32(o);
-              }
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                w[16 * q + i] = n > 0 ? bf16x2(__uint_as_float(o[2 * i]) * f, __uint_as_float(o[2 * i + 1]) * f) : 0u;
-            }
-            lane_transpose8(w, lane);
-            const int64_t at = t * a.out_stride + (int64_t)h * D;
-            const int col = c0 + 8 * (lane & 7);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int src = (lane & ~7) + i;
-              const int64_t to = __shfl_sync(0xffffffffu, at, src);
-              if (((rows_here >> src) & 1u) && col < D)
-                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + to + col) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-            }
+          uint32_t o[64];
+          if (n > 0) {
+            at_ld32(t_o + c0, o);
+            at_ld32(t_o + c0 + 32, o + 32);
+            at_ld_done32(o);
+            at_ld_done32(o + 32);
           } else {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {  // 32 columns as fp32, 128 bytes
-              if (n > 0) {
-                at_ld32(t_o + c0 + 32 * q, o);
-                at_ld_done32(o);
-              } else {
+            for (int i = 0; i < 64; ++i) o[i] = 0;
+          }
+          if (whole) {
+            uint32_t w[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = 0;
-              }
-              lane_transpose8(o, lane);
-              const int64_t base = slot - (lane & 7);  // the part's row of the lane group's first lane
-              const int col = c0 + 32 * q + 4 * (lane & 7);
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if ((rows_here >> ((lane & ~7) + i)) & 1u)
-                  *reinterpret_cast<uint4*>(a.part_o + (base + i) * DP + col) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-            }
+            for (int i = 0; i < 32; ++i) w[i] = bf16x2(__uint_as_float(o[2 * i]) * f, __uint_as_float(o[2 * i + 1]) * f);
+            send(w, 2 * c0);
+          } else {
+            send(o, 4 * c0);
+            send(o + 32, 4 * c0 + 128);
           }
           __syncwarp();
         }
@@ -700,6 +710,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(piece_free(k));
     }
+    bulk_done();
   }
   tc_fence_before();
   __syncthreads();
