@@ -40,7 +40,7 @@ struct AttnArgs {
   int window, sinks;
   int tile_tokens;  // tokens of a tile, 0: tiles of packed rows that may start within a token
   int min_units;    // fewest blocks of a CTA's stretch
-  float* part_o;    // [2 * CTAs][R][DP]
+  float* part_o;    // [2 * CTAs][R][DP], or as part_at() says
   float2* part_ml;  // [2 * CTAs][R]
   int4* cut;        // [CTAs][2]: the tile that begins in CTA c's stretch and ends in a later one
 };
@@ -244,6 +244,15 @@ __device__ __forceinline__ void put_cut(const AttnArgs& a, int cta, int last, co
 
 __device__ __forceinline__ float exp2_(float x) { return exp2f(x); }
 
+// Where column d of row r of a part lies, in floats.  The kernel for chunks
+// (R = 256) writes 32 columns of 32 rows at a time, as 128-byte rows whose
+// 16-byte chunks are swizzled, and its second tile's rows from 128 on.
+template <int R, int DP>
+__device__ __forceinline__ int64_t part_at(int64_t slot, int r, int d) {
+  if (R == 16) return (slot * R + r) * DP + d;
+  return (slot * (DP / 32) + d / 32) * (R * 32) + r * 32 + ((((d >> 2) & 7) ^ (r & 7)) << 2) + (d & 3);
+}
+
 // Joins the tile cut at the end of CTA x's stretch.  A warp takes a row: the
 // parts one after the other, their loads in flight together.  Where a tile has
 // more than eight parts the block's four warps share them out, and add up in
@@ -266,17 +275,18 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
   const int per = share ? (parts + 3) / 4 : parts, p0 = share ? min(parts, warp * per) : 0, p1 = min(parts, p0 + per);
   const int step = share ? gridDim.y : 4 * gridDim.y;
   for (int r = share ? blockIdx.y : blockIdx.y * 4 + warp; r < rows; r += step) {
+    // the row's place in the parts
+    const int half = a.tile_tokens / 2 * a.group, pr_part = R != 16 && r >= half ? r - half + R / 2 : r;
     float m = -INFINITY, l = 0.f, o[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = 0.f;
 #pragma unroll 4
     for (int p = p0; p < p1; ++p) {
       const int64_t slot = 2 * (int64_t)(c0 + p) + (p == 0 ? 1 : 0);
-      const float2 ml = a.part_ml[slot * R + r];
-      const float* src = a.part_o + (slot * R + r) * DP + lane * 2;
+      const float2 ml = a.part_ml[slot * R + pr_part];
       float2 v[V / 2];
 #pragma unroll
-      for (int i = 0; i < V / 2; ++i) v[i] = *reinterpret_cast<const float2*>(src + 64 * i);
+      for (int i = 0; i < V / 2; ++i) v[i] = *reinterpret_cast<const float2*>(a.part_o + part_at<R, DP>(slot, pr_part, 64 * i + 2 * lane));
       const float mn = fmaxf(m, ml.x), ms = mn == -INFINITY ? 0.f : mn;
       const float f0 = exp2_(m - ms), f1 = exp2_(ml.x - ms);
       l = l * f0 + ml.y * f1;

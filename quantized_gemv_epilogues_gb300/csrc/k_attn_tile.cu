@@ -173,26 +173,17 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return r;
 }
 
-// Eight 16-byte chunks rotated by the lane: chunk i becomes chunk (i + lane) % 8.
-__device__ __forceinline__ void rotate8(uint32_t* v, int lane) {
-#pragma unroll
-  for (int b = 1; b < 8; b <<= 1) {
-    const bool on = lane & b;
-    uint32_t w[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) w[i] = on ? v[(i + 4 * b) & 31] : v[i];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = w[i];
-  }
-}
-__device__ __forceinline__ void st_shared16(uint32_t p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
 // One thread's bulk copy shared -> global (16-byte aligned, a multiple of 16
 // bytes), the wait until its copies have read their sources, and until they
 // are done.
 __device__ __forceinline__ void bulk_s2g(void* dst, uint32_t src, int bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int x, int y, int z, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x), "r"(y), "r"(z),
+               "r"(src)
+               : "memory");
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 __device__ __forceinline__ void bulk_reads_done() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
@@ -234,7 +225,8 @@ static_assert(at_smem<128>() <= 227 * 1024 && at_smem<64>() <= 227 * 1024, "shar
 template <int DP>
 __global__ void __launch_bounds__(AT_THREADS, 1)
     attn_tile_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                     const __grid_constant__ CUtensorMap vmap, const AttnArgs a, const int box_rows) {
+                     const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap, const AttnArgs a,
+                     const int box_rows) {
   using S = AtShape<DP>;
   constexpr int NS = S::NS;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -659,22 +651,40 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         const float f = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
         const int D = a.pg.head_dim, h = p.h * G + r_head;
         const int64_t t = p.row0 + tok;
-        const int64_t slot = (2 * (int64_t)blockIdx.x + (p.first == 0 ? 1 : 0)) * AT_R + s * tps * G + r;
-        // A row's columns lie in one thread; written from there, 16 bytes of 32
-        // rows a store, they cost the warps 7000 cycles a piece.  Instead each
-        // thread puts 128 bytes of its row into shared memory and has them
-        // copied out in bulk, while it goes on.
-        const int64_t at = whole ? (t * a.out_stride + (int64_t)h * D) * 2 : slot * DP * 4;  // this row's first byte
-        char* const dst = (whole ? reinterpret_cast<char*>(a.out) : reinterpret_cast<char*>(a.part_o)) + at;
-        auto send = [&](uint32_t* v, int col_bytes) {  // v: 128 bytes; only those within the row are copied
-          rotate8(v, lane);
-          bulk_reads_done();  // the row's last 128 bytes have left
-          const uint32_t buf = smem_u32(smem + S::OFF_OUT + tid * 128);
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (p.first == 0 ? 1 : 0);
+        // A row's columns lie in one thread; stored from there, 16 bytes of 32
+        // rows at a time, they cost the warps 7000 cycles a piece.  A warp's 32
+        // rows go through shared memory, 128 bytes of each at a time, as the
+        // 128-byte swizzle lays them out (no bank conflicts), and leave in one
+        // piece: parts as 4 KB in one bulk copy (the joining kernel undoes the
+        // swizzle), full rows of 32 / G whole tokens as one TMA store, others
+        // as 16 bytes a lane, 8 lanes a row.
+        const int w_tok = tok0 + (warp & 3) * (32 / G);  // the warp's first token, where 32 % G == 0
+        const bool tma = whole && 32 % G == 0 && w_tok + 32 / G - 1 <= p.i1;
+        unsigned char* const buf = smem + S::OFF_OUT + warp * 4096;
+        const int64_t at = t * a.out_stride + (int64_t)h * D;
+        const unsigned rows_here = __ballot_sync(0xffffffffu, row);
+        auto send = [&](const uint32_t* v, int c0) {  // v: the row's 128 bytes from column c0 on
+          if (lane == 0) bulk_reads_done();            // the last ones have left
+          __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 8; ++i)  // chunk (i + lane) % 8: eight neighbouring rows write to different banks
-            st_shared16(buf + (((i + lane) & 7) << 4), v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4*>(buf + lane * 128 + ((i ^ (lane & 7)) << 4)) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          if (row) bulk_s2g(dst + col_bytes, buf, whole ? min(128, 2 * D - col_bytes) : 128);
+          __syncwarp();
+          if (!whole) {
+            if (lane == 0) bulk_s2g(a.part_o + (slot * (DP / 32) + c0 / 32) * (AT_R * 32) + warp * (32 * 32), smem_u32(buf), 4096);
+          } else if (tma) {
+            if (lane == 0) tma_store_3d(&omap, c0, p.h * G, p.row0 + w_tok, smem_u32(buf));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int src = 4 * i + (lane >> 3), col = c0 + 8 * (lane & 7);
+              const int64_t to = __shfl_sync(0xffffffffu, at, src) + col;
+              if (((rows_here >> src) & 1u) && col < D)
+                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + to) = *reinterpret_cast<const uint4*>(buf + src * 128 + (((lane & 7) ^ (src & 7)) << 4));
+            }
+          }
         };
 #pragma unroll
         for (int c0 = 0; c0 < DP; c0 += 64) {
@@ -692,16 +702,16 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             uint32_t w[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) w[i] = bf16x2(__uint_as_float(o[2 * i]) * f, __uint_as_float(o[2 * i + 1]) * f);
-            send(w, 2 * c0);
+            send(w, c0);
           } else {
-            send(o, 4 * c0);
-            send(o + 32, 4 * c0 + 128);
+            send(o, c0);
+            send(o + 32, c0 + 32);
           }
           __syncwarp();
         }
         if (row) {
           const float ml = m == -INFINITY ? m : m * cl;
-          if (!whole) a.part_ml[slot] = make_float2(ml, l);
+          if (!whole) a.part_ml[slot * AT_R + 128 * s + r] = make_float2(ml, l);
           else if (a.lse) a.lse[t * a.q_heads + h] = l > 0.f || l != l ? ((m == -INFINITY ? 0.f : ml) + log2f(l)) * 0.6931471805599453f : -INFINITY;
         }
         // the reads of O above come before the next piece's products, which this tile's P allows
@@ -746,13 +756,17 @@ mt_status run_tile(AttnArgs a, void* ws, const Launch& l, const DeviceInfo* di) 
   const int tps = 128 / a.group, box = at_box(pg.page_size);
   a.tile_tokens = 2 * tps;
   a.min_units = 1;
-  CUtensorMap qmap, kmap, vmap;
+  CUtensorMap qmap, kmap, vmap, omap;
   const cuuint64_t row = (cuuint64_t)pg.head_dim * 2;
   {
     const cuuint64_t dims[3] = {(cuuint64_t)pg.head_dim, (cuuint64_t)a.q_heads, (cuuint64_t)pg.T};
     const cuuint64_t st[2] = {row, (cuuint64_t)a.q_stride * 2};
     const cuuint32_t bx[3] = {64, (cuuint32_t)a.group, (cuuint32_t)tps};
     if (!at_map(&qmap, a.q, 3, dims, st, bx)) return cuda_fail(cudaErrorInvalidValue);
+    // a warp's 32 rows of the output (used where they are whole tokens)
+    const cuuint64_t so[2] = {row, (cuuint64_t)a.out_stride * 2};
+    const cuuint32_t bo[3] = {64, (cuuint32_t)a.group, (cuuint32_t)std::max(1, 32 / a.group)};
+    if (!at_map(&omap, a.out, 3, dims, so, bo)) return cuda_fail(cudaErrorInvalidValue);
   }
   {
     const cuuint64_t dims[4] = {(cuuint64_t)pg.head_dim, (cuuint64_t)pg.page_size, (cuuint64_t)pg.kv_heads, (cuuint64_t)pg.num_pages};
@@ -769,7 +783,7 @@ mt_status run_tile(AttnArgs a, void* ws, const Launch& l, const DeviceInfo* di) 
   a.part_ml = reinterpret_cast<float2*>(w);
   w += (size_t)ctas * 2 * AT_R * sizeof(float2);
   a.part_o = reinterpret_cast<float*>(w);
-  if (const mt_status st = launch(attn_tile_kernel<DP>, dim3(ctas), dim3(AT_THREADS), at_smem<DP>(), l, qmap, kmap, vmap, a, box)) return st;
+  if (const mt_status st = launch(attn_tile_kernel<DP>, dim3(ctas), dim3(AT_THREADS), at_smem<DP>(), l, qmap, kmap, vmap, omap, a, box)) return st;
   return launch(attn_join_kernel<AT_R, DP>, dim3(ctas, 32), dim3(128), 0, l, a);
 }
 
