@@ -31,7 +31,9 @@
 //    and they complete in order), so the softmax warps may rescale O without
 //    another barrier.
 //  * While one tile's softmax runs, the tensor cores work on the other tile:
-//    PV0(j) S0(j+1) PV1(j) S1(j+1) is the issue order.
+//    PV0(j) S0(j+1) PV1(j) S1(j+1) is the issue order.  A piece with rows in
+//    one tile only (single tokens beside a chunk) uses both buffers of S in
+//    turn, and S runs a block ahead.
 // Weights are rounded to bf16 (2^-8 of each) because the MMA takes one type
 // for both operands and V is bf16; the sum l is of the unrounded weights.
 // Every mbarrier wait is bounded (~1 s): on expiry the error word gets
@@ -459,15 +461,56 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       if (elect_one()) {
         int st = 0;
         uint32_t pp[2] = {0, 0}, qq[2] = {0, 0};  // p_full and q_full phases passed
-        auto qk = [&](int s, int i) {  // S_s = Q_s K^T, K in stage i
+        auto qk = [&](int s, int i, int buf) {  // S = Q_s K^T into buffer buf, K in stage i
 #pragma unroll
           for (int ks = 0; ks < DP / 16; ++ks) {
             const uint32_t o = (uint32_t)((ks >> 2) * S::HALF + (ks & 3) * 32);
-            at_mma_ss(tbase + 128 * s, pf_desc_sw128(q_tile(s) + o), pf_desc_sw128(stage(i) + o), at_idesc(128, false), ks > 0);
+            at_mma_ss(tbase + 128 * buf, pf_desc_sw128(q_tile(s) + o), pf_desc_sw128(stage(i) + o), at_idesc(128, false), ks > 0);
           }
-          tc_commit(s_full(s));
+          tc_commit(s_full(buf));
+        };
+        // O_s (+)= P V, P in buffer buf, V in stage i; the first 64 keys as soon as their weights are there
+        auto pv = [&](int s, int i, int buf, bool add) -> bool {
+#pragma unroll
+          for (int ks = 0; ks < AT_BK / 16; ++ks) {
+            if (ks == 0 || ks == AT_BK / 32) {
+              if (!wait1(ks ? p_full(buf) : p_half(buf), pp[buf] & 1)) return false;
+              tc_fence_after();
+            }
+            at_mma_ts(tbase + 256 + DP * s, tbase + 128 * buf + 8 * ks, at_desc_mn(stage(i) + ks * 2048, S::HALF), at_idesc(DP, true),
+                      add || ks > 0);
+          }
+          ++pp[buf];
+          return true;
+        };
+        // a piece with rows in one tile only: S of the next block goes into the
+        // other tile's buffer (and uses its barriers), so that the softmax has
+        // it when it has finished a block
+        auto single = [&](int n) -> bool {
+          if (!wait1(q_full(0), qq[0] & 1)) return false;
+          ++qq[0];
+          for (int j = -1; j < n; ++j) {
+            if (j + 1 < n) {
+              const int k = st + 2 * (j + 1);
+              if (!wait1(kv_full(k % NS), (k / NS) & 1)) return false;
+              tc_fence_after();
+              qk(0, k % NS, (j + 1) & 1);
+              tc_commit(kv_free(k % NS));
+              if (j + 2 == n) tc_commit(q_free(0));
+            }
+            if (j < 0) continue;
+            const int v = st + 2 * j + 1;
+            if (!wait1(kv_full(v % NS), (v / NS) & 1)) return false;
+            tc_fence_after();
+            if (!((j & 1) ? pv(0, v % NS, 1, j > 0) : pv(0, v % NS, 0, j > 0))) return false;
+            tc_commit(j + 1 == n ? o_full(0) : o_full(1));
+            tc_commit(kv_free(v % NS));
+          }
+          st += 2 * n;
+          return true;
         };
         auto products = [&](int n0, int n1) -> bool {  // one piece's
+          if (n1 == 0) return single(n0);
           const int nb = max(n0, n1);
           if (!wait1(kv_full(st % NS), (st / NS) & 1)) return false;
 #pragma unroll
@@ -477,7 +520,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             if (!wait1(q_full(s), qq[s] & 1)) return false;
             ++qq[s];
             tc_fence_after();
-            qk(s, st % NS);
+            qk(s, st % NS, s);
             if (n == 1) tc_commit(q_free(s));
           }
           tc_commit(kv_free(st % NS));
@@ -490,23 +533,14 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             for (int s = 0; s < 2; ++s) {
               const int n = s ? n1 : n0;
               if (j >= n) continue;
-#pragma unroll
-              for (int ks = 0; ks < AT_BK / 16; ++ks) {
-                if (ks == 0 || ks == AT_BK / 32) {
-                  if (!wait1(ks ? p_full(s) : p_half(s), pp[s] & 1)) return false;
-                  tc_fence_after();
-                }
-                at_mma_ts(tbase + 256 + DP * s, tbase + 128 * s + 8 * ks, at_desc_mn(stage(iv) + ks * 2048, S::HALF),
-                          at_idesc(DP, true), j > 0 || ks > 0);
-              }
-              ++pp[s];
+              if (!pv(s, iv, s, j > 0)) return false;
               if (j + 1 == n) {
                 tc_commit(o_full(s));
               } else {
                 if (!have_k && !wait1(kv_full(ik), ((st + 1) / NS) & 1)) return false;
                 have_k = true;
                 tc_fence_after();
-                qk(s, ik);
+                qk(s, ik, s);
                 if (j + 2 == n) tc_commit(q_free(s));
               }
             }
@@ -537,15 +571,17 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     // ---- softmax of tile s, row r
     const int s = warp >> 2, r = tid & 127, G = a.group, tps = a.tile_tokens >> 1;
     const uint32_t lanes = tbase + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t t_s = lanes + 128 * s, t_o = lanes + 256 + DP * s;
+    const uint32_t t_o = lanes + 256 + DP * s;
     const float cl = a.scale_log2;
     const int r_tok = r / G, r_head = r - r_tok * G;
-    uint32_t sp = 0, op = 0;  // s_full and o_full phases passed
+    uint32_t sp0 = 0, sp1 = 0, op0 = 0, op1 = 0;  // phases of s_full and o_full that have been (here, or by the other tile's warps)
     for (int k = 0;; ++k) {
       if (!wait(piece_full(k), (k / AT_PIECES) & 1)) break;
       const Piece& p = sh.piece[k % AT_PIECES];
       if (p.stop) break;
       const int tok0 = p.i0 + s * tps, n = p.n[s];
+      const int n_first = p.n[0], n_second = p.n[1];
+      const bool single = n_second == 0;  // the first tile's blocks alternate between both tiles' buffers of S
       if (tok0 <= p.i1) {  // the tile has rows
         const int tok = tok0 + r_tok;
         const bool row = r < tps * G && tok <= p.i1;
@@ -556,8 +592,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         bool ok = true;
         for (int j = 0; j < n; ++j) {
           const int i0 = p.first + j, k0 = (i0 < p.sink ? i0 : i0 - p.sink + p.win) * AT_BK;
-          ok = wait(s_full(s), sp & 1);
-          ++sp;
+          const int buf = single ? j & 1 : s;
+          const uint32_t t_s = lanes + 128 * buf;
+          ok = wait(s_full(buf), ((buf ? sp1 : sp0) + (single ? j >> 1 : j)) & 1);
           if (!ok) break;
           tc_fence_after();
           uint32_t x[128];
@@ -598,6 +635,12 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             const float f = mn == -INFINITY ? 1.f : ex2((m - mn) * cl);
             m = mn;
             l *= f;
+            // O is complete up to the last block: with S, unless S runs ahead
+            if (single) {
+              ok = wait(o_full(1), (op1 + j - 1) & 1);
+              if (!ok) break;
+              tc_fence_after();
+            }
 #pragma unroll 1
             for (int q = 0; q < DP / 16; ++q) {
               float v[16];
@@ -628,13 +671,13 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
               at_st_done();
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(p_half(s));
+              if (lane == 0) mbar_arrive(p_half(buf));
             }
           }
           at_st_done();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(p_full(s));
+          if (lane == 0) mbar_arrive(p_full(buf));
           float u, v;
           unpair(add2(sum[0], sum[1]), u, v);
           l += u + v;
@@ -642,8 +685,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         if (!ok) break;
         // ---- the piece's rows
         if (n > 0) {
-          ok = wait(o_full(s), op & 1);
-          ++op;
+          ok = wait(o_full(s), (s ? op1 : op0) & 1);
           if (!ok) break;
           tc_fence_after();
         }
@@ -717,6 +759,15 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         // the reads of O above come before the next piece's products, which this tile's P allows
         tc_fence_before();
       }
+      // The second tile's warps keep to the first one's pieces: a parity only
+      // tells a phase from its neighbours, and theirs have passed here too.
+      // (The first tile's warps are kept by S of a piece's first block, which
+      // completes after everything before it.)
+      if (s == 1 && single && n_first > 0 && !wait(o_full(0), op0 & 1)) break;
+      sp0 += single ? (n_first + 1) >> 1 : n_first;
+      sp1 += single ? n_first >> 1 : n_second;
+      op0 += n_first > 0;
+      op1 += single ? max(n_first - 1, 0) : 1;
       __syncwarp();
       if (lane == 0) mbar_arrive(piece_free(k));
     }

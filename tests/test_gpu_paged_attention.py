@@ -149,6 +149,25 @@ def test_two_calls_give_the_same_bits(mt, lens):
     assert torch.equal(a, b) and torch.equal(la, lb)
 
 
+@pytest.mark.parametrize("heads", [(8, 2, 128), (14, 2, 64), (16, 1, 128), (3, 3, 96)], ids=lambda h: "x".join(map(str, h)))
+def test_chunks_and_single_tokens_in_every_order(mt, heads):
+    # tiles with rows in one half and in both follow one another, with growing
+    # scores so that reference maxima move
+    g = heads[0] // heads[1]
+    full = 256 // g  # tokens of a whole tile
+    for lens in ([(full, 700), (1, 900), (full + 3, 400), (1, 1), (2, 650), (full, full), (1, 129)],
+                 [(1, 513), (2 * full, 2 * full), (1, 256), (full // 2 + 1, 300), (0, 50), (1, 2000)]):
+        p = Paged(lens, *heads, page=16, seed=19, q_scale=4.0)
+        for kb in p.keys:
+            kb *= torch.linspace(0.2, 2.0, len(kb))[:, None, None].to(torch.bfloat16)
+        for b, (_, kv) in enumerate(lens):
+            for i in range(-(-kv // 16)):
+                n = min(16, kv - i * 16)
+                p.k[p.pages[b, i], :n] = p.keys[b][i * 16:i * 16 + n]
+        compare(mt, p)
+        compare(mt, p, window=200, sinks=3)
+
+
 def test_many_sequences(mt):
     lens = [(1 if b % 7 else 0, (b * 37) % 200 + 1) for b in range(1024)]
     compare(mt, Paged(lens, 4, 2, 64, page=16, seed=15))
