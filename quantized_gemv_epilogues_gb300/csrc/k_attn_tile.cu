@@ -53,7 +53,7 @@ namespace {
 constexpr int AT_BK = 128, AT_R = 256, AT_THREADS = 384;
 constexpr int AT_EXTRA = 3;  // units of a tile beside its blocks: the blocks that its start and output take as long as
 constexpr int AT_SOFT = 8;  // warps 0-7: softmax; tile warp / 4, rows 32 (warp % 4) on
-constexpr int AT_TMA = 8, AT_MMA = 9, AT_Q = 10, AT_WALK = 11;
+constexpr int AT_MMA = 8, AT_WALK = 9, AT_LOAD = 10;  // AT_LOAD: Q and K, and the next warp V
 
 template <int DP>
 struct AtShape {
@@ -359,88 +359,52 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           }
         }
       }
-    } else if (warp == AT_TMA) {
-      // ---- K and V blocks
+    } else if (warp >= AT_LOAD) {
+      // ---- K blocks (stages 0, 2, ... of the ring) and V blocks (1, 3, ...),
+      // a warp each: a lane's copy takes its warp some 70 cycles to ask for, and
+      // pages of 16 tokens make 16 copies a block.  (Four warps in place of two
+      // cost the softmax 5 %.)  The K warp also fetches Q at a piece's start,
+      // once the last piece's S products are done with it.
+      const int kv = warp - AT_LOAD;
+      const CUtensorMap* map = kv ? &vmap : &kmap;
       const int boxes = AT_BK / box_rows;
-      int st = 0;  // blocks asked for (K and V each count)
-      uint32_t tails = 0;
+      int st = kv;  // the next block's stage
+      uint32_t tails = 0, asked[2] = {0, 0};
       bool ok = true;
       for (int k = 0; ok; ++k) {
         ok = wait(piece_full(k), (k / AT_PIECES) & 1);
         const Piece& p = sh.piece[k % AT_PIECES];
         if (!ok || p.stop) break;
         const int n = max(p.n[0], p.n[1]), h = p.h;
-        // this lane's box of block j: the table's entry and the row in the page; false if no row sees it
-        auto box = [&](int j, int& page, int& row) -> bool {
-          page = a.pg.num_pages;
-          row = 0;
-          const int i = p.first + j, k0 = (i < p.sink ? i : i - p.sink + p.win) * AT_BK + lane * box_rows;
-          if (j < n && lane < boxes && k0 < p.key_end && (k0 + box_rows > p.win_lo || k0 < a.sinks)) {
-            const int e = k0 / a.pg.page_size;
-            page = __ldg(a.pg.pages + (int64_t)p.b * a.pg.pages_ld + e);
-            row = k0 - e * a.pg.page_size;
-            return true;
-          }
-          return false;
+        struct Box {
+          bool mine;         // the lane has a box of the block
+          int page, row;     // the table's entry, the row in the page
+          bool seen;         // by some row of the tile
+          int tail0, tail1;  // V rows of the block beyond the sequence's end that a box still reads
         };
-        int page_next, row_next;
-        bool seen_next = box(0, page_next, row_next);
-        for (int j = 0; ok && j < n; ++j) {
-          int page = page_next;
-          const int row = row_next;
-          if (seen_next && (unsigned)page >= (unsigned)a.pg.num_pages) {
-            atomicExch(a.pg.err, (int)MT_ERR_PAGE);
-            page = a.pg.num_pages;  // zeros, as for a box that no row sees
+        auto box = [&](int j) -> Box {  // this lane's of block j
+          Box b = {false, a.pg.num_pages, 0, false, 0, 0};
+          if (j >= n) return b;
+          const int i = p.first + j, blk0 = (i < p.sink ? i : i - p.sink + p.win) * AT_BK;
+          const int t0 = p.kv - blk0, t1 = min((t0 + box_rows - 1) / box_rows * box_rows, AT_BK);
+          if (kv && t0 > 0 && t0 < AT_BK && t1 > t0) {
+            b.tail0 = t0;
+            b.tail1 = t1;
           }
-          seen_next = box(j + 1, page_next, row_next);  // its load returns while this block is asked for
-          const int i = p.first + j, k0 = (i < p.sink ? i : i - p.sink + p.win) * AT_BK;
-          // rows of the block beyond the sequence's end that a box still reads
-          const int tail0 = p.kv - k0, tail1 = min((tail0 + box_rows - 1) / box_rows * box_rows, AT_BK);
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            const int q = st % NS;
-            if (st >= NS) ok = wait(kv_free(q), ((st / NS) + 1) & 1);
-            if (!ok) break;
-            const bool patch = kv == 1 && tail0 < AT_BK && tail0 > 0 && tail1 > tail0;
-            const uint32_t bar = patch ? tail_bar : kv_full(q), dst = stage(q);
-            if (lane == 0) mbar_arrive_expect_tx(bar, S::TILE);
-            __syncwarp();
-            if (lane < boxes) {
-#pragma unroll
-              for (int c = 0; c < S::CH; ++c)
-                tma_load_4d(dst + c * S::HALF + lane * box_rows * 128, kv ? &vmap : &kmap, 64 * c, row, h, page, bar);
-            }
-            ++st;
-            if (patch) {
-              ok = wait(tail_bar, tails & 1);
-              ++tails;
-              unsigned char* v = smem + S::OFF_KV + (size_t)q * S::TILE;
-              for (int x = lane; x < (tail1 - tail0) * 8 * S::CH; x += 32) {
-                const int c = x & 7, r = (x >> 3) % (tail1 - tail0), hh = (x >> 3) / (tail1 - tail0);
-                *reinterpret_cast<uint4*>(v + hh * S::HALF + (tail0 + r) * 128 + 16 * c) = make_uint4(0, 0, 0, 0);
-              }
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-              __syncwarp();
-              if (lane == 0) mbar_arrive(kv_full(q));
-              if (!ok) break;
-            }
+          if (lane >= boxes) return b;
+          b.mine = true;
+          const int k0 = blk0 + lane * box_rows;
+          if (k0 < p.key_end && (k0 + box_rows > p.win_lo || k0 < a.sinks)) {
+            const int e = k0 / a.pg.page_size;
+            b.page = __ldg(a.pg.pages + (int64_t)p.b * a.pg.pages_ld + e);
+            b.row = k0 - e * a.pg.page_size;
+            b.seen = true;
           }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(piece_free(k));
-      }
-      // copies still in flight (only after an abort) land before the CTA ends
-      for (int i = max(0, st - NS); !ok && i < st; ++i) (void)mbar_wait_bounded(kv_full(i % NS), (i / NS) & 1);
-    } else if (warp == AT_Q) {
-      // ---- Q tiles, once the last piece's S products are done with them
-      if (lane == 0) {
-        const int tps = a.tile_tokens >> 1;
-        uint32_t asked[2] = {0, 0};
-        bool ok = true;
-        for (int k = 0; ok; ++k) {
-          ok = wait1(piece_full(k), (k / AT_PIECES) & 1);
-          const Piece& p = sh.piece[k % AT_PIECES];
-          if (!ok || p.stop) break;
+          return b;
+        };
+        Box next = box(0);
+        if (kv == 0 && lane == 0) {
+          const int tps = a.tile_tokens >> 1;
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
             if (!ok || p.n[s] == 0) continue;
@@ -448,15 +412,51 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             if (!ok) continue;
             mbar_arrive_expect_tx(q_full(s), (uint32_t)(S::CH * 128 * a.group * tps));
             for (int c = 0; c < S::CH; ++c)
-              tma_load_3d(q_tile(s) + c * S::HALF, &qmap, 64 * c, p.h * a.group, p.row0 + p.i0 + s * tps, q_full(s));
+              tma_load_3d(q_tile(s) + c * S::HALF, &qmap, 64 * c, h * a.group, p.row0 + p.i0 + s * tps, q_full(s));
             ++asked[s];
           }
-          mbar_arrive(piece_free(k));
         }
-        for (int s = 0; s < 2; ++s)
-          if (!ok && asked[s] > 0) (void)mbar_wait_bounded(q_full(s), (asked[s] - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        for (int j = 0; ok && j < n; ++j) {
+          Box b = next;
+          if (b.seen && (unsigned)b.page >= (unsigned)a.pg.num_pages) {
+            atomicExch(a.pg.err, (int)MT_ERR_PAGE);
+            b.page = a.pg.num_pages;  // zeros, as for a box that no row sees
+          }
+          next = box(j + 1);  // its load returns while this block is asked for
+          const int q = st % NS;
+          if (st >= NS) ok = wait(kv_free(q), ((st / NS) + 1) & 1);
+          if (!ok) break;
+          const uint32_t bar = b.tail1 ? tail_bar : kv_full(q), dst = stage(q);
+          if (lane == 0) mbar_arrive_expect_tx(bar, S::TILE);
+          __syncwarp();
+          if (b.mine) {
+#pragma unroll
+            for (int c = 0; c < S::CH; ++c)
+              tma_load_4d(dst + c * S::HALF + lane * box_rows * 128, map, 64 * c, b.row, h, b.page, bar);
+          }
+          st += 2;
+          if (b.tail1) {
+            ok = wait(tail_bar, tails & 1);
+            ++tails;
+            unsigned char* v = smem + S::OFF_KV + (size_t)q * S::TILE;
+            for (int x = lane; x < (b.tail1 - b.tail0) * 8 * S::CH; x += 32) {
+              const int c = x & 7, r = (x >> 3) % (b.tail1 - b.tail0), hh = (x >> 3) / (b.tail1 - b.tail0);
+              *reinterpret_cast<uint4*>(v + hh * S::HALF + (b.tail0 + r) * 128 + 16 * c) = make_uint4(0, 0, 0, 0);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(kv_full(q));
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(piece_free(k));
       }
-    } else {
+      // copies still in flight (only after an abort) land before the CTA ends
+      for (int i = max(kv, st - NS); !ok && i < st; i += 2) (void)mbar_wait_bounded(kv_full(i % NS), (i / NS) & 1);
+      for (int s = 0; s < 2; ++s)
+        if (!ok && lane == 0 && asked[s] > 0) (void)mbar_wait_bounded(q_full(s), (asked[s] - 1) & 1);
+    } else if (warp == AT_MMA) {
       // ---- the products, all issued by one lane
       if (elect_one()) {
         int st = 0;
