@@ -71,7 +71,8 @@ mt_status mt_paged_attention(const void* q, int64_t q_stride, int q_heads, const
   a.window = window;
   a.sinks = sinks;
   const Launch l{(cudaStream_t)stream, mt_get_option(MT_OPT_PDL) != 0};
-  if ((int64_t)batch->max_q * a.group > 16 && attn_tile_takes(a)) return launch_attn_tile(a, workspace, l, di);
+  a.max_q = batch->max_q;
+  if (attn_tile_takes(a)) return launch_attn_tile(a, workspace, l, di);
   return launch_attn_rows(a, workspace, l, di);
 }
 

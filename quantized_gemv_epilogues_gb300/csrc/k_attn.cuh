@@ -39,6 +39,7 @@ struct AttnArgs {
   float scale_log2;  // scale * log2 e
   int window, sinks;
   int tile_tokens;  // tokens of a tile, 0: tiles of packed rows that may start within a token
+  int max_q;        // the host's hint
   int min_units;    // fewest blocks of a CTA's stretch
   float* part_o;    // [2 * CTAs][R][DP], or as part_at() says
   float2* part_ml;  // [2 * CTAs][R]
@@ -253,90 +254,133 @@ __device__ __forceinline__ int64_t part_at(int64_t slot, int r, int d) {
   return (slot * (DP / 32) + d / 32) * (R * 32) + r * 32 + ((((d >> 2) & 7) ^ (r & 7)) << 2) + (d & 3);
 }
 
-// Joins the tile cut at the end of CTA x's stretch.  A warp takes a row: the
-// parts one after the other, their loads in flight together.  Where a tile has
-// more than eight parts the block's four warps share them out, and add up in
-// order.
+// Joins the tile cut at the end of CTA x's stretch.  A warp takes two rows at a
+// time, V columns a lane: the loads of both rows' parts are in flight
+// together.  Where a tile has more than eight parts, the block's eight warps
+// share out those of one row, and add up in order.
+constexpr int JOIN_WARPS = 8;
 template <int R, int DP>
-__global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(32 * JOIN_WARPS) attn_join_kernel(const AttnArgs a) {
+  constexpr int V = DP / 32;
+  __shared__ float o_sh[JOIN_WARPS][DP];
+  __shared__ float2 ml_sh[JOIN_WARPS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, D = a.pg.head_dim, c0 = blockIdx.x;
   pdl_wait();
   pdl_trigger();
-  const int c0 = blockIdx.x;
   const int4 k0 = a.cut[2 * c0];
+  const int rows = a.cut[2 * c0 + 1].x;
   const int c1 = k0.x;
   if (c1 <= c0) return;
-  const int rows = a.cut[2 * c0 + 1].x;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, D = a.pg.head_dim;
-  constexpr int V = DP / 32;  // columns a lane, in pairs 64 apart
-  __shared__ float o_sh[4][DP];
-  __shared__ float2 ml_sh[4];
   const int parts = c1 - c0 + 1;
-  const bool share = parts > 8;
-  const int per = share ? (parts + 3) / 4 : parts, p0 = share ? min(parts, warp * per) : 0, p1 = min(parts, p0 + per);
-  const int step = share ? gridDim.y : 4 * gridDim.y;
-  for (int r = share ? blockIdx.y : blockIdx.y * 4 + warp; r < rows; r += step) {
-    // the row's place in the parts
-    const int half = a.tile_tokens / 2 * a.group, pr_part = R != 16 && r >= half ? r - half + R / 2 : r;
-    float m = -INFINITY, l = 0.f, o[V];
+  const int half = a.tile_tokens / 2 * a.group;
+  struct Row {
+    float m, l, o[V];
+  };
+  auto clear = [&](Row& x) {
+    x.m = -INFINITY;
+    x.l = 0.f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = 0.f;
-#pragma unroll 4
-    for (int p = p0; p < p1; ++p) {
-      const int64_t slot = 2 * (int64_t)(c0 + p) + (p == 0 ? 1 : 0);
-      const float2 ml = a.part_ml[slot * R + pr_part];
-      float2 v[V / 2];
+    for (int i = 0; i < V; ++i) x.o[i] = 0.f;
+  };
+  auto load = [&](int p, int r, float2& ml, float (&v)[V]) {
+    const int64_t slot = 2 * (int64_t)(c0 + p) + (p == 0 ? 1 : 0);
+    const int at = R != 16 && r >= half ? r - half + R / 2 : r;  // the row's place in the parts
+    ml = a.part_ml[slot * R + at];
 #pragma unroll
-      for (int i = 0; i < V / 2; ++i) v[i] = *reinterpret_cast<const float2*>(a.part_o + part_at<R, DP>(slot, pr_part, 64 * i + 2 * lane));
-      const float mn = fmaxf(m, ml.x), ms = mn == -INFINITY ? 0.f : mn;
-      const float f0 = exp2_(m - ms), f1 = exp2_(ml.x - ms);
-      l = l * f0 + ml.y * f1;
-#pragma unroll
-      for (int i = 0; i < V / 2; ++i) {
-        o[2 * i] = o[2 * i] * f0 + v[i].x * f1;
-        o[2 * i + 1] = o[2 * i + 1] * f0 + v[i].y * f1;
-      }
-      m = mn;
-    }
-    if (share) {
-      __syncthreads();
-      if (lane == 0) ml_sh[warp] = make_float2(m, l);
-#pragma unroll
-      for (int i = 0; i < V / 2; ++i) *reinterpret_cast<float2*>(&o_sh[warp][64 * i + 2 * lane]) = make_float2(o[2 * i], o[2 * i + 1]);
-      __syncthreads();
-      if (warp) continue;
-      m = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) m = fmaxf(m, ml_sh[w].x);
-      l = 0.f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) o[i] = 0.f;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float f = exp2_(ml_sh[w].x - (m == -INFINITY ? 0.f : m));
-        l += ml_sh[w].y * f;
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-          const float2 y = *reinterpret_cast<const float2*>(&o_sh[w][64 * i + 2 * lane]);
-          o[2 * i] += y.x * f;
-          o[2 * i + 1] += y.y * f;
-        }
+    for (int i = 0; i < V; i += 4) {
+      const float* src = a.part_o + part_at<R, DP>(slot, at, V * lane + i);
+      if (V == 2) {
+        *reinterpret_cast<float2*>(&v[0]) = *reinterpret_cast<const float2*>(src);
+      } else {
+        const float4 q = *reinterpret_cast<const float4*>(src);
+        v[i] = q.x;
+        v[i + 1] = q.y;
+        v[(i + 2) % V] = q.z;
+        v[(i + 3) % V] = q.w;
       }
     }
-    const bool any = l > 0.f || l != l;
-    const float inv = any ? 1.f / l : 0.f;
+  };
+  auto add = [&](Row& x, const float2 ml, const float (&v)[V]) {
+    const float mn = fmaxf(x.m, ml.x), ms = mn == -INFINITY ? 0.f : mn;
+    const float f0 = exp2_(x.m - ms), f1 = exp2_(ml.x - ms);
+    x.l = x.l * f0 + ml.y * f1;
+#pragma unroll
+    for (int i = 0; i < V; ++i) x.o[i] = x.o[i] * f0 + v[i] * f1;
+    x.m = mn;
+  };
+  auto write = [&](int r, const Row& x) {
+    const bool any = x.l > 0.f || x.l != x.l;
+    const float inv = any ? 1.f / x.l : 0.f;
     const int pr = k0.w + r, t = k0.y + pr / a.group, h = k0.z * a.group + pr % a.group;
     const int64_t at = (int64_t)t * a.out_stride + (int64_t)h * D;
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-      const int d = 64 * i + 2 * lane;  // D is even
+    for (int i = 0; i < V; i += 2) {
+      const int d = V * lane + i;  // D is even
       if (d < D) {
-        const float x = o[2 * i] * inv, y = o[2 * i + 1] * inv;
-        if (a.out_f32) *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out) + at + d) = make_float2(x, y);
-        else *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.out) + at + d) = (uint32_t)f2bf(x) | ((uint32_t)f2bf(y) << 16);
+        const float y0 = x.o[i] * inv, y1 = x.o[i + 1] * inv;
+        if (a.out_f32) *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out) + at + d) = make_float2(y0, y1);
+        else *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.out) + at + d) = (uint32_t)f2bf(y0) | ((uint32_t)f2bf(y1) << 16);
       }
     }
-    if (lane == 0 && a.lse) a.lse[(int64_t)t * a.q_heads + h] = any ? ((m == -INFINITY ? 0.f : m) + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    if (lane == 0 && a.lse) a.lse[(int64_t)t * a.q_heads + h] = any ? ((x.m == -INFINITY ? 0.f : x.m) + log2f(x.l)) * 0.6931471805599453f : -INFINITY;
+  };
+  if (parts <= 8) {
+    const int step = JOIN_WARPS * gridDim.y;
+    for (int r = blockIdx.y * JOIN_WARPS + warp; r < rows; r += 2 * step) {
+      const bool two = r + step < rows;
+      const int r2 = two ? r + step : r;
+      Row x, y;
+      clear(x);
+      clear(y);
+#pragma unroll 2
+      for (int p = 0; p < parts; ++p) {
+        float2 ma, mb;
+        float va[V], vb[V];
+        load(p, r, ma, va);
+        load(p, r2, mb, vb);
+        add(x, ma, va);
+        add(y, mb, vb);
+      }
+      write(r, x);
+      if (two) write(r2, y);
+    }
+    return;
   }
+  const int per = (parts + JOIN_WARPS - 1) / JOIN_WARPS, p0 = min(parts, warp * per), p1 = min(parts, p0 + per);
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    Row x;
+    clear(x);
+#pragma unroll 8
+    for (int p = p0; p < p1; ++p) {
+      float2 ml;
+      float v[V];
+      load(p, r, ml, v);
+      add(x, ml, v);
+    }
+    __syncthreads();
+    if (lane == 0) ml_sh[warp] = make_float2(x.m, x.l);
+#pragma unroll
+    for (int i = 0; i < V; ++i) o_sh[warp][V * lane + i] = x.o[i];
+    __syncthreads();
+    if (warp) continue;
+    clear(x);
+#pragma unroll
+    for (int w = 0; w < JOIN_WARPS; ++w) {
+      float v[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = o_sh[w][V * lane + i];
+      add(x, ml_sh[w], v);
+    }
+    write(r, x);
+  }
+}
+
+// Blocks of the joining kernel for each cut: as many as a tile has rows, as far
+// as the host knows (each block strides over them), but at most 8: blocks that
+// find nothing to join still cost their launch.
+inline int join_blocks(const AttnArgs& a) {
+  const int64_t rows = (int64_t)(a.max_q > 0 ? a.max_q : 1) * a.group;
+  return (int)(rows < 8 ? rows : 8);
 }
 
 // Launchers (k_attn_rows.cu, k_attn_tile.cu): the main kernel and the join.

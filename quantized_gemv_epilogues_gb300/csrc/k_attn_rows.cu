@@ -359,7 +359,7 @@ mt_status run_rows(AttnArgs a, void* ws, const Launch& l, const DeviceInfo* di) 
   w += (size_t)ctas * 2 * AR_R * sizeof(float2);
   a.part_o = reinterpret_cast<float*>(w);
   if (const mt_status st = launch(attn_rows_kernel<DP>, dim3(ctas), dim3(AR_THREADS), S::SMEM, l, a)) return st;
-  return launch(attn_join_kernel<AR_R, DP>, dim3(ctas, AR_R), dim3(128), 0, l, a);
+  return launch(attn_join_kernel<AR_R, DP>, dim3(ctas, join_blocks(a)), dim3(32 * JOIN_WARPS), 0, l, a);
 }
 
 }  // namespace
