@@ -4,17 +4,20 @@
 //   x = logit + bias;  seen: x > 0 ? x / r : x * r;
 //   generated n > 0 times: x - f n - p;  not allowed: -inf
 //
-// Bound: memory, each logit read and written once (and one mask bit).  A block
-// takes CH consecutive logits of one sequence and issues all of its loads at
-// once; while they are on their way it counts its sequence's tokens.  Counting
-// needs no clearing of CH words: a first walk over the history marks each of
-// the block's tokens in a bitmap and zeroes its word, a second walk (the ids
-// are in L1 then) adds, and the pass over the logits looks at words only
-// where the bitmap has a bit: one byte of shared memory per eight logits
-// otherwise.  Every block of a sequence reads its whole history, which L2
-// serves: 4 bytes a token against 2 CH (bf16) or 4 CH bytes of logits.
-// Counts are integers and a repeated bias entry is resolved by its index, so
-// no result depends on the order of the atomics.
+// Bound: memory, each logit read and written once (and one mask bit); a
+// sequence's history touches a few thousand of its 10^5 logits.  Two kernels:
+//  * mask_kernel passes all logits to the output under the mask, 16 bytes a
+//    load, NV of them in flight a thread.  In place and without a mask there is
+//    nothing to do, and it is not launched.
+//  * token_kernel, a block per sequence, counts the tokens in a hash table in
+//    shared memory, then does their logits, reading each from the input.  It
+//    counts while mask_kernel still runs, and waits for it (programmatic
+//    dependent launch) before it writes.
+// (One kernel, whose blocks each took a chunk of the vocabulary and counted
+// the tokens that fell there, read every history 16 times and spent its time
+// on those loads' latency: 50 us where this takes XX for 200 texts.)
+// Counts are integers and a repeated bias entry is resolved by its index, so no
+// result depends on the order of the atomics.
 #include <math.h>
 
 #include <atomic>
@@ -25,7 +28,8 @@ namespace mt {
 
 namespace {
 
-constexpr int LG_THREADS = 256;
+constexpr int LM_THREADS = 256;  // mask_kernel
+constexpr int LT_THREADS = 512;  // token_kernel
 
 struct LogitArgs {
   const char* in;
@@ -45,15 +49,15 @@ struct LogitArgs {
   int n_bias;
   const uint32_t* allowed;
   int64_t allowed_ld;
+  int slots;   // of token_kernel's table, a power of two
+  bool in_order;  // token_kernel follows mask_kernel
 };
 
-// NV 16-byte vectors of logits a thread; CH = logits a block.
-template <bool F32, int NV>
-struct LogitShape {
-  static constexpr int VE = F32 ? 4 : 8;
-  static constexpr int CH = NV * LG_THREADS * VE;
-  static constexpr int CAP = CH + 32;  // the first block also takes up to VE - 1 logits before the aligned ones
-};
+// A token's word: the times it was generated, and
+constexpr uint32_t LG_PROMPT = 1u << 31;  // it is in the prompt
+constexpr uint32_t LG_BIASED = 1u << 30;  // it has a bias
+constexpr uint32_t LG_TIMES = LG_BIASED - 1;
+constexpr uint32_t LG_EMPTY = 0xFFFFFFFFu;  // a slot's key without a token
 
 template <bool F32>
 __device__ __forceinline__ float logit_get(const char* p, int i) {
@@ -66,152 +70,215 @@ __device__ __forceinline__ void logit_put(char* p, int i, float x) {
 }
 
 template <bool F32, int NV>
-__global__ void __launch_bounds__(LG_THREADS) logit_penalties_kernel(const LogitArgs a) {
-  using S = LogitShape<F32, NV>;
-  constexpr int VE = S::VE, CH = S::CH, ES = F32 ? 4 : 2;
-  extern __shared__ __align__(16) uint32_t lg_smem[];
-  uint32_t* marked = lg_smem;                   // bit per logit: seen
-  uint32_t* biased = marked + S::CAP / 32;      // bit per logit: has a bias
-  uint32_t* count = biased + S::CAP / 32;       // times generated, where marked
-  uint32_t* slot = count + S::CAP;              // 1 + index of the bias entry, where biased (only with biases)
+__global__ void __launch_bounds__(LM_THREADS) mask_kernel(const LogitArgs a) {
+  constexpr int VE = F32 ? 4 : 8, CH = NV * LM_THREADS * VE, ES = F32 ? 4 : 2;
   const int tid = threadIdx.x, b = blockIdx.y, V = a.V;
   pdl_wait();
-  pdl_trigger();
+  pdl_trigger();  // after the wait: what token_kernel reads before its own is complete
   const char* in = a.in + (int64_t)b * a.in_ld * ES;
   char* out = a.out + (int64_t)b * a.out_ld * ES;
+  const uint32_t* allowed = a.allowed ? a.allowed + (int64_t)b * a.allowed_ld : nullptr;
+  auto one = [&](int t) {
+    float x = logit_get<F32>(in, t);
+    if (!allowed || ((__ldg(allowed + (t >> 5)) >> (t & 31)) & 1u)) {
+      if (F32) reinterpret_cast<uint32_t*>(out)[t] = reinterpret_cast<const uint32_t*>(in)[t];  // as it is, NaN or not
+      else reinterpret_cast<uint16_t*>(out)[t] = reinterpret_cast<const uint16_t*>(in)[t];
+    } else {
+      x = -INFINITY;
+      logit_put<F32>(out, t, x);
+    }
+  };
   // logits before the row's first 16-byte boundary; vectors need it to be the
   // output's too
   const int e0 = min(V, (int)((16u - ((uint32_t)(uintptr_t)in & 15u)) & 15u) / ES);
-  const bool vec = (((uintptr_t)in ^ (uintptr_t)out) & 15u) == 0;
-  const int c0 = e0 + blockIdx.x * CH;         // first aligned logit
-  const int lo = blockIdx.x ? c0 : 0;          // first logit of the block
-  const int hi = min(V, c0 + CH);
-  if (lo >= hi) return;
-
+  const int c0 = e0 + blockIdx.x * CH;
+  if ((((uintptr_t)in ^ (uintptr_t)out) & 15u) != 0) {
+#pragma unroll 1
+    for (int t = (blockIdx.x ? c0 : 0) + tid; t < min(V, c0 + CH); t += LM_THREADS) one(t);
+    return;
+  }
   uint4 raw[NV];
+  uint32_t ok[NV];  // the mask's VE bits from each vector's first logit on
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int t = c0 + (v * LG_THREADS + tid) * VE;
-    if (vec && t + VE <= V) raw[v] = *reinterpret_cast<const uint4*>(in + (int64_t)t * ES);
+    const int t = c0 + (v * LM_THREADS + tid) * VE;
+    if (t + VE <= V) {
+      raw[v] = *reinterpret_cast<const uint4*>(in + (int64_t)t * ES);
+      ok[v] = allowed ? __funnelshift_r(__ldg(allowed + (t >> 5)), __ldg(allowed + ((t + VE - 1) >> 5)), t & 31) : 0xFFFFFFFFu;
+    }
   }
-  for (int i = tid; i < 2 * (S::CAP / 32); i += LG_THREADS) marked[i] = 0;
-  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int t = c0 + (v * LM_THREADS + tid) * VE;
+    if (t + VE > V) {
+#pragma unroll 1
+      for (int i = t; i < V; ++i) one(i);  // the row's last logits
+      continue;
+    }
+    uint32_t* w = reinterpret_cast<uint32_t*>(&raw[v]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (F32) {
+        w[i] = (ok[v] >> i) & 1u ? w[i] : 0xFF800000u;
+      } else {
+        const uint32_t keep = ((ok[v] >> (2 * i)) & 1u ? 0x0000FFFFu : 0u) | ((ok[v] >> (2 * i)) & 2u ? 0xFFFF0000u : 0u);
+        w[i] = (w[i] & keep) | (0xFF80FF80u & ~keep);
+      }
+    }
+    *reinterpret_cast<uint4*>(out + (int64_t)t * ES) = raw[v];
+  }
+  if (blockIdx.x == 0 && tid < e0) one(tid);
+}
 
-  const int span = hi - lo;
-  int h0 = 0, h1 = 0, hp = 0;
+// Table of `slots` entries: key, word, and with biases 1 + the bias entry's
+// index.  A sequence whose history and biases could fill it by more than three
+// quarters is done in passes over ranges of `slots` tokens instead, the word at
+// a token's place in the range.
+template <bool F32>
+__global__ void __launch_bounds__(LT_THREADS) token_kernel(const LogitArgs a) {
+  constexpr int ES = F32 ? 4 : 2, N = 8;
+  extern __shared__ __align__(16) uint32_t lt_smem[];
+  const int tid = threadIdx.x, b = blockIdx.x, V = a.V, slots = a.slots;
+  uint32_t* key = lt_smem;
+  uint32_t* word = key + slots;
+  uint32_t* slot = word + slots;
+  // alone, the kernel waits for what comes before it now; after mask_kernel it
+  // waits for that later
+  if (!a.in_order) pdl_wait();
+  int h0 = 0, h1 = 0, hp = 0, b0 = 0, b1 = 0;
   if (a.history) {
     h0 = min(max(__ldg(a.history_start + b), 0), a.n_history);
     h1 = min(max(__ldg(a.history_start + b + 1), h0), a.n_history);
-    hp = a.prompt_len ? min(max(__ldg(a.prompt_len + b), 0), h1 - h0) : 0;  // prompt tokens
-    hp += h0;
-#pragma unroll 4
-    for (int i = h0 + tid; i < h1; i += LG_THREADS) {
-      const int id = __ldg(a.history + i);
-      const unsigned at = (unsigned)(id - lo);
-      if (id >= 0 && at < (unsigned)span) {
-        count[at] = 0;
-        atomicOr(&marked[at >> 5], 1u << (at & 31));
-      }
-    }
+    hp = h0 + (a.prompt_len ? min(max(__ldg(a.prompt_len + b), 0), h1 - h0) : 0);  // the end of the prompt
   }
-  int b0 = 0, b1 = 0;
   if (a.bias_ids) {
     b0 = min(max(__ldg(a.bias_start + b), 0), a.n_bias);
     b1 = min(max(__ldg(a.bias_start + b + 1), b0), a.n_bias);
-    for (int i = b0 + tid; i < b1; i += LG_THREADS) {
-      const int id = __ldg(a.bias_ids + i);
-      const unsigned at = (unsigned)(id - lo);
-      if (id >= 0 && at < (unsigned)span) {
-        slot[at] = 0;
-        atomicOr(&biased[at >> 5], 1u << (at & 31));
-      }
-    }
   }
-  __syncthreads();
-#pragma unroll 4
-  for (int i = hp + tid; i < h1; i += LG_THREADS) {
-    const int id = __ldg(a.history + i);
-    const unsigned at = (unsigned)(id - lo);
-    if (id >= 0 && at < (unsigned)span) atomicAdd(&count[at], 1u);
-  }
-  for (int i = b0 + tid; i < b1; i += LG_THREADS) {
-    const int id = __ldg(a.bias_ids + i);
-    const unsigned at = (unsigned)(id - lo);
-    if (id >= 0 && at < (unsigned)span) atomicMax(&slot[at], (uint32_t)(i - b0 + 1));
-  }
-  __syncthreads();
-
-  const float rep = a.repetition ? __ldg(a.repetition + b) : 1.f;
-  const float pres = a.presence ? __ldg(a.presence + b) : 0.f;
-  const float freq = a.frequency ? __ldg(a.frequency + b) : 0.f;
+  const float rep = a.repetition ? __ldg(a.repetition + b) : 1.f, rep_inv = 1.f / rep;
+  const float freq = a.frequency ? __ldg(a.frequency + b) : 0.f, pres = a.presence ? __ldg(a.presence + b) : 0.f;
+  const char* in = a.in + (int64_t)b * a.in_ld * ES;
+  char* out = a.out + (int64_t)b * a.out_ld * ES;
   const uint32_t* allowed = a.allowed ? a.allowed + (int64_t)b * a.allowed_ld : nullptr;
-  auto touched = [&](float x, unsigned at) -> float {  // a logit with a bias or in the history
-    if ((biased[at >> 5] >> (at & 31)) & 1u) x += __ldg(a.bias_values + b0 + (int)slot[at] - 1);
-    if ((marked[at >> 5] >> (at & 31)) & 1u) {
-      x = x > 0.f ? x / rep : x * rep;
-      const uint32_t n = count[at];
-      if (n) x = x - freq * (float)n - pres;
+  const bool hashed = (int64_t)(h1 - h0) + (b1 - b0) <= slots / 4 * 3;
+  const int passes = hashed ? 1 : (V + slots - 1) / slots;
+  int shift = 32;  // the hash's upper bits: a slot's index
+  for (int n = slots; n > 1; n >>= 1) --shift;
+
+  for (int p = 0; p < passes; ++p) {
+    const int base = hashed ? 0 : p * slots, top = hashed ? V : min(V, base + slots);
+    // (slots is a multiple of 4 * LT_THREADS)
+    for (int i = tid; i < slots / 4; i += LT_THREADS) {
+      if (hashed) reinterpret_cast<uint4*>(key)[i] = make_uint4(LG_EMPTY, LG_EMPTY, LG_EMPTY, LG_EMPTY);
+      reinterpret_cast<uint4*>(word)[i] = make_uint4(0, 0, 0, 0);
+      if (a.bias_ids) reinterpret_cast<uint4*>(slot)[i] = make_uint4(0, 0, 0, 0);
     }
-    return x;
-  };
-  auto single = [&](int t) {
-    float x = touched(logit_get<F32>(in, t), (unsigned)(t - lo));
-    if (allowed && !((__ldg(allowed + (t >> 5)) >> (t & 31)) & 1u)) x = -INFINITY;
-    logit_put<F32>(out, t, x);
-  };
-  if (!vec) {  // rows of input and output that are not aligned alike
-    for (int t = lo + tid; t < hi; t += LG_THREADS) single(t);
-    return;
-  }
-  if (lo + tid < c0) single(lo + tid);
+    __syncthreads();
+    auto place = [&](int t) -> int {  // of token t in the table, which has room
+      if (!hashed) return t - base;
+      uint32_t at = (uint32_t)t * 2654435761u >> shift;
+      for (;;) {
+        uint32_t k = *const_cast<volatile uint32_t*>(&key[at]);
+        if (k == LG_EMPTY) k = atomicCAS(&key[at], LG_EMPTY, (uint32_t)t);
+        if (k == LG_EMPTY || k == (uint32_t)t) return (int)at;
+        at = (at + 1) & (slots - 1);
+      }
+    };
+    for (int i0 = h0; i0 < h1; i0 += N * LT_THREADS) {
+      int id[N];
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int t = c0 + (v * LG_THREADS + tid) * VE;
-    if (t + VE > V) {
-      for (int i = t; i < V; ++i) single(i);
-      continue;
-    }
-    const unsigned at = (unsigned)(t - lo);
-    // the VE bits from bit t (at) on, of the mask (the bitmaps)
-    uint32_t ok = 0xFFFFFFFFu;
-    if (allowed) ok = __funnelshift_r(__ldg(allowed + (t >> 5)), __ldg(allowed + ((t + VE - 1) >> 5)), t & 31);
-    const unsigned w0 = at >> 5, w1 = (at + VE - 1) >> 5;
-    const uint32_t hit = __funnelshift_r(marked[w0] | biased[w0], marked[w1] | biased[w1], at & 31) & ((1u << VE) - 1);
-    uint4 r = raw[v];
-    uint32_t* w = reinterpret_cast<uint32_t*>(&r);
-    if (hit || (~ok & ((1u << VE) - 1))) {
+      for (int q = 0; q < N; ++q) {
+        const int i = i0 + q * LT_THREADS + tid;
+        id[q] = i < h1 ? __ldg(a.history + i) : -1;
+      }
+#pragma unroll 1
+      for (int q = 0; q < N; ++q) {
+        int t = id[0];
 #pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        float x = F32 ? __uint_as_float(w[F32 ? i : 0]) : ((i & 1) ? bf16hi(w[i >> 1]) : bf16lo(w[i >> 1]));
-        if ((hit >> i) & 1u) x = touched(x, at + i);
-        if (!((ok >> i) & 1u)) x = -INFINITY;
-        if (F32) w[F32 ? i : 0] = __float_as_uint(x);
-        else if (((hit | ~ok) >> i) & 1u)
-          w[i >> 1] = (i & 1) ? (w[i >> 1] & 0x0000FFFFu) | ((uint32_t)f2bf(x) << 16)
-                              : (w[i >> 1] & 0xFFFF0000u) | (uint32_t)f2bf(x);
+        for (int s = 0; s + 1 < N; ++s) id[s] = id[s + 1];
+        if (t < base || t >= top) continue;
+        uint32_t* w = &word[place(t)];
+        // (a prompt's token is marked once: frequent ones would queue up at their word)
+        if (i0 + q * LT_THREADS + tid >= hp) atomicAdd(w, 1u);
+        else if (!(*const_cast<volatile uint32_t*>(w) & LG_PROMPT)) atomicOr(w, LG_PROMPT);
       }
     }
-    *reinterpret_cast<uint4*>(out + (int64_t)t * ES) = r;
+    for (int i = b0 + tid; i < b1; i += LT_THREADS) {
+      const int t = __ldg(a.bias_ids + i);
+      if (t < base || t >= top) continue;
+      const int at = place(t);
+      atomicOr(&word[at], LG_BIASED);
+      atomicMax(&slot[at], (uint32_t)(i - b0 + 1));
+    }
+    if (p == 0 && a.in_order) pdl_wait();
+    __syncthreads();
+    if (p == 0) pdl_trigger();
+    // N entries of a thread's at a time, so that their loads are in flight
+    // together.  In place, a logit that was not masked still is what it was,
+    // and a masked one is masked again.
+    for (int i0 = tid; i0 < slots; i0 += N * LT_THREADS) {
+      uint32_t w[N], m[N];
+      int t[N];
+      float x[N], add[N];
+#pragma unroll
+      for (int q = 0; q < N; ++q) {
+        const int i = i0 + q * LT_THREADS;
+        w[q] = i < slots ? word[i] : 0;
+        t[q] = w[q] ? (hashed ? (int)key[i] : base + i) : 0;
+        add[q] = 0.f;
+        if (w[q]) {
+          x[q] = logit_get<F32>(in, t[q]);
+          m[q] = allowed ? __ldg(allowed + (t[q] >> 5)) : 0xFFFFFFFFu;
+          if (w[q] & LG_BIASED) add[q] = __ldg(a.bias_values + b0 + (int)slot[i] - 1);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < N; ++q)
+        if (w[q]) {
+          float y = x[q];
+          if (w[q] & LG_BIASED) y += add[q];
+          if (w[q] & (LG_PROMPT | LG_TIMES)) y *= y > 0.f ? rep_inv : rep;
+          if (w[q] & LG_TIMES) y = y - freq * (float)(w[q] & LG_TIMES) - pres;
+          if (!((m[q] >> (t[q] & 31)) & 1u)) y = -INFINITY;
+          logit_put<F32>(out, t[q], y);
+        }
+    }
+    __syncthreads();  // the next pass's table is this one
   }
 }
 
-template <bool F32, int NV>
-mt_status logit_launch(const LogitArgs& a, int B, const Launch& l) {
-  using S = LogitShape<F32, NV>;
-  const size_t smem = (size_t)(2 * (S::CAP / 32) + S::CAP * (a.bias_ids ? 2 : 1)) * 4;
+template <bool F32>
+mt_status logit_launch(LogitArgs a, int B, const Launch& l, int sms) {
+  const bool tokens = (a.history && a.n_history) || (a.bias_ids && a.n_bias);
+  const bool masks = a.in != a.out || a.allowed;
+  if (masks) {
+    constexpr int VE = F32 ? 4 : 8;
+    // few logits: one vector a thread, so that they spread over the GPU
+    const bool few = (long)B * a.V < 4L * 4 * LM_THREADS * VE * sms;
+    const int ch = (few ? 1 : 4) * LM_THREADS * VE;
+    const dim3 grid((a.V + ch - 1) / ch, B);
+    const mt_status st = few ? launch(mask_kernel<F32, 1>, grid, dim3(LM_THREADS), 0, l, a)
+                             : launch(mask_kernel<F32, 4>, grid, dim3(LM_THREADS), 0, l, a);
+    if (st) return st;
+  }
+  if (!tokens) return MT_OK;
+  a.in_order = masks;
+  // four slots for a sequence's average token, so that its table is at most
+  // half full unless it is twice the average
+  const int words = a.bias_ids ? 3 : 2;
+  const long want = 4 * (((long)a.n_history + a.n_bias) / B + 1);
+  a.slots = 4 * LT_THREADS;
+  while (a.slots < want && a.slots < 16384) a.slots *= 2;
   static std::atomic<bool> set[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e);
   if (dev >= 0 && dev < 64 && !set[dev].load()) {
-    e = cudaFuncSetAttribute(logit_penalties_kernel<F32, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)((2 * (S::CAP / 32) + S::CAP * 2) * 4));
+    e = cudaFuncSetAttribute(token_kernel<F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, 16384 * 3 * 4);
     if (e != cudaSuccess) return cuda_fail(e);
     set[dev].store(true);
   }
-  // one block more where a row's unaligned first logits push its last ones over
-  const int blocks = (a.V + S::CH - 1) / S::CH;
-  return launch(logit_penalties_kernel<F32, NV>, dim3(blocks, B), dim3(LG_THREADS), smem, l, a);
+  return launch(token_kernel<F32>, dim3(B), dim3(LT_THREADS), (size_t)a.slots * words * 4, l, a);
 }
 
 }  // namespace
@@ -274,9 +341,5 @@ extern "C" mt_status mt_logit_penalties(const void* logits, int64_t logits_ld, v
   a.allowed = allowed;
   a.allowed_ld = allowed_ld;
   const Launch l{(cudaStream_t)stream, mt_get_option(MT_OPT_PDL) != 0};
-  // few sequences: 2048 logits a block, so that a vocabulary fills the GPU;
-  // many: 8192, which read the history a quarter as often
-  if (dtype == MT_F32)
-    return (long)B * V < 4L * 8192 * di->sm_count ? logit_launch<true, 2>(a, B, l) : logit_launch<true, 8>(a, B, l);
-  return (long)B * V < 4L * 8192 * di->sm_count ? logit_launch<false, 1>(a, B, l) : logit_launch<false, 4>(a, B, l);
+  return dtype == MT_F32 ? logit_launch<true>(a, B, l, di->sm_count) : logit_launch<false>(a, B, l, di->sm_count);
 }
