@@ -9,7 +9,7 @@
 //  * mask_kernel passes all logits to the output under the mask, 16 bytes a
 //    load, NV of them in flight a thread.  In place and without a mask there is
 //    nothing to do, and it is not launched.
-//  * token_kernel, a block per sequence, counts the tokens in a hash table in
+//  * token_kernel, a block per sequence (several, for few), counts the tokens in a hash table in
 //    shared memory, then does their logits, reading each from the input.  It
 //    counts while mask_kernel still runs, and waits for it (programmatic
 //    dependent launch) before it writes.
@@ -20,6 +20,7 @@
 // result depends on the order of the atomics.
 #include <math.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "k_paged.cuh"
@@ -29,7 +30,7 @@ namespace mt {
 namespace {
 
 constexpr int LM_THREADS = 256;  // mask_kernel
-constexpr int LT_THREADS = 512;  // token_kernel
+constexpr int LT_THREADS = 1024;  // token_kernel
 
 struct LogitArgs {
   const char* in;
@@ -130,18 +131,21 @@ __global__ void __launch_bounds__(LM_THREADS) mask_kernel(const LogitArgs a) {
   if (blockIdx.x == 0 && tid < e0) one(tid);
 }
 
-// Table of `slots` entries: key, word, and with biases 1 + the bias entry's
-// index.  A sequence whose history and biases could fill it by more than three
+// Table of `slots` entries: key, word, with biases 1 + the bias entry's index;
+// and a list of the entries in use.  A sequence whose history and biases could fill it by more than three
 // quarters is done in passes over ranges of `slots` tokens instead, the word at
 // a token's place in the range.
 template <bool F32>
 __global__ void __launch_bounds__(LT_THREADS) token_kernel(const LogitArgs a) {
   constexpr int ES = F32 ? 4 : 2, N = 8;
   extern __shared__ __align__(16) uint32_t lt_smem[];
-  const int tid = threadIdx.x, b = blockIdx.x, V = a.V, slots = a.slots;
+  const int tid = threadIdx.x, b = blockIdx.y, V = a.V, slots = a.slots;
+  const int share = blockIdx.x, shares = gridDim.x;  // of the sequence's tokens
   uint32_t* key = lt_smem;
   uint32_t* word = key + slots;
   uint32_t* slot = word + slots;
+  uint16_t* list = reinterpret_cast<uint16_t*>(slot + (a.bias_ids ? slots : 0));
+  __shared__ int used;
   // alone, the kernel waits for what comes before it now; after mask_kernel it
   // waits for that later
   if (!a.in_order) pdl_wait();
@@ -165,15 +169,17 @@ __global__ void __launch_bounds__(LT_THREADS) token_kernel(const LogitArgs a) {
   int shift = 32;  // the hash's upper bits: a slot's index
   for (int n = slots; n > 1; n >>= 1) --shift;
 
-  for (int p = 0; p < passes; ++p) {
+  bool first_pass = true;
+  for (int p = hashed ? 0 : share; p < passes; p += shares) {
     const int base = hashed ? 0 : p * slots, top = hashed ? V : min(V, base + slots);
-    // (slots is a multiple of 4 * LT_THREADS)
+    if (tid == 0) used = 0;
     for (int i = tid; i < slots / 4; i += LT_THREADS) {
       if (hashed) reinterpret_cast<uint4*>(key)[i] = make_uint4(LG_EMPTY, LG_EMPTY, LG_EMPTY, LG_EMPTY);
       reinterpret_cast<uint4*>(word)[i] = make_uint4(0, 0, 0, 0);
       if (a.bias_ids) reinterpret_cast<uint4*>(slot)[i] = make_uint4(0, 0, 0, 0);
     }
     __syncthreads();
+    auto mine = [&](int t) -> bool { return hashed ? t >= 0 && t < V && t % shares == share : t >= base && t < top; };
     auto place = [&](int t) -> int {  // of token t in the table, which has room
       if (!hashed) return t - base;
       uint32_t at = (uint32_t)t * 2654435761u >> shift;
@@ -184,6 +190,15 @@ __global__ void __launch_bounds__(LT_THREADS) token_kernel(const LogitArgs a) {
         at = (at + 1) & (slots - 1);
       }
     };
+    // by whole warps: the entries that some lanes are the first to touch join the list
+    auto enlist = [&](bool first, int at) {
+      const unsigned who = __ballot_sync(0xffffffffu, first);
+      if (!who) return;
+      int n = 0;
+      if ((tid & 31) == 0) n = atomicAdd(&used, __popc(who));
+      n = __shfl_sync(0xffffffffu, n, 0);
+      if (first) list[n + __popc(who & ((1u << (tid & 31)) - 1u))] = (uint16_t)at;
+    };
     for (int i0 = h0; i0 < h1; i0 += N * LT_THREADS) {
       int id[N];
 #pragma unroll
@@ -191,60 +206,69 @@ __global__ void __launch_bounds__(LT_THREADS) token_kernel(const LogitArgs a) {
         const int i = i0 + q * LT_THREADS + tid;
         id[q] = i < h1 ? __ldg(a.history + i) : -1;
       }
-#pragma unroll 1
-      for (int q = 0; q < N; ++q) {
-        int t = id[0];
 #pragma unroll
-        for (int s = 0; s + 1 < N; ++s) id[s] = id[s + 1];
-        if (t < base || t >= top) continue;
-        uint32_t* w = &word[place(t)];
-        // (a prompt's token is marked once: frequent ones would queue up at their word)
-        if (i0 + q * LT_THREADS + tid >= hp) atomicAdd(w, 1u);
-        else if (!(*const_cast<volatile uint32_t*>(w) & LG_PROMPT)) atomicOr(w, LG_PROMPT);
+      for (int q = 0; q < N; ++q) {
+        if (i0 + q * LT_THREADS >= h1) break;
+        const int t = id[q];
+        bool first = false;
+        int at = 0;
+        if (mine(t)) {
+          at = place(t);
+          // (a prompt's token is marked once: frequent ones would queue up at their word)
+          if (i0 + q * LT_THREADS + tid >= hp) first = atomicAdd(&word[at], 1u) == 0;
+          else if (!(*const_cast<volatile uint32_t*>(&word[at]) & LG_PROMPT)) first = atomicOr(&word[at], LG_PROMPT) == 0;
+        }
+        enlist(first, at);
       }
     }
-    for (int i = b0 + tid; i < b1; i += LT_THREADS) {
-      const int t = __ldg(a.bias_ids + i);
-      if (t < base || t >= top) continue;
-      const int at = place(t);
-      atomicOr(&word[at], LG_BIASED);
-      atomicMax(&slot[at], (uint32_t)(i - b0 + 1));
+    for (int i0 = b0; i0 < b1; i0 += LT_THREADS) {
+      const int i = i0 + tid, t = i < b1 ? __ldg(a.bias_ids + i) : -1;
+      bool first = false;
+      int at = 0;
+      if (mine(t)) {
+        at = place(t);
+        first = atomicOr(&word[at], LG_BIASED) == 0;
+        atomicMax(&slot[at], (uint32_t)(i - b0 + 1));
+      }
+      enlist(first, at);
     }
-    if (p == 0 && a.in_order) pdl_wait();
+    if (first_pass && a.in_order) pdl_wait();
+    first_pass = false;
     __syncthreads();
-    if (p == 0) pdl_trigger();
-    // N entries of a thread's at a time, so that their loads are in flight
+    // M entries of a thread's at a time, so that their loads are in flight
     // together.  In place, a logit that was not masked still is what it was,
     // and a masked one is masked again.
-    for (int i0 = tid; i0 < slots; i0 += N * LT_THREADS) {
-      uint32_t w[N], m[N];
-      int t[N];
-      float x[N], add[N];
+    constexpr int M = 4;
+    const int n = used;
+    for (int i0 = tid; i0 < n; i0 += M * LT_THREADS) {
+      uint32_t w[M], m[M];
+      int t[M];
+      float x[M], add[M];
 #pragma unroll
-      for (int q = 0; q < N; ++q) {
-        const int i = i0 + q * LT_THREADS;
-        w[q] = i < slots ? word[i] : 0;
-        t[q] = w[q] ? (hashed ? (int)key[i] : base + i) : 0;
-        add[q] = 0.f;
-        if (w[q]) {
-          x[q] = logit_get<F32>(in, t[q]);
-          m[q] = allowed ? __ldg(allowed + (t[q] >> 5)) : 0xFFFFFFFFu;
-          if (w[q] & LG_BIASED) add[q] = __ldg(a.bias_values + b0 + (int)slot[i] - 1);
-        }
+      for (int q = 0; q < M; ++q) {
+        const int at = list[min(i0 + q * LT_THREADS, n - 1)];  // past the end: the last one, not written
+        w[q] = word[at];
+        t[q] = hashed ? (int)key[at] : base + at;
+        x[q] = logit_get<F32>(in, t[q]);
+        m[q] = allowed ? __ldg(allowed + (t[q] >> 5)) : 0xFFFFFFFFu;
+        add[q] = w[q] & LG_BIASED ? __ldg(a.bias_values + b0 + (int)slot[at] - 1) : 0.f;
       }
 #pragma unroll
-      for (int q = 0; q < N; ++q)
-        if (w[q]) {
-          float y = x[q];
-          if (w[q] & LG_BIASED) y += add[q];
-          if (w[q] & (LG_PROMPT | LG_TIMES)) y *= y > 0.f ? rep_inv : rep;
-          if (w[q] & LG_TIMES) y = y - freq * (float)(w[q] & LG_TIMES) - pres;
-          if (!((m[q] >> (t[q] & 31)) & 1u)) y = -INFINITY;
-          logit_put<F32>(out, t[q], y);
-        }
+      for (int q = 0; q < M; ++q) {
+        float y = x[q];
+        if (w[q] & LG_BIASED) y += add[q];
+        if (w[q] & (LG_PROMPT | LG_TIMES)) y *= y > 0.f ? rep_inv : rep;
+        if (w[q] & LG_TIMES) y = y - freq * (float)(w[q] & LG_TIMES) - pres;
+        if (!((m[q] >> (t[q] & 31)) & 1u)) y = -INFINITY;
+        if (i0 + q * LT_THREADS < n) logit_put<F32>(out, t[q], y);
+      }
     }
     __syncthreads();  // the next pass's table is this one
   }
+  // a share without a pass must not end before mask_kernel either: what follows
+  // takes this kernel's end for both
+  if (first_pass && a.in_order) pdl_wait();
+  pdl_trigger();
 }
 
 template <bool F32>
@@ -265,20 +289,23 @@ mt_status logit_launch(LogitArgs a, int B, const Launch& l, int sms) {
   a.in_order = masks;
   // four slots for a sequence's average token, so that its table is at most
   // half full unless it is twice the average
-  const int words = a.bias_ids ? 3 : 2;
+  const int bytes = a.bias_ids ? 14 : 10;  // of a slot
   const long want = 4 * (((long)a.n_history + a.n_bias) / B + 1);
-  a.slots = 4 * LT_THREADS;
+  a.slots = 2048;
   while (a.slots < want && a.slots < 16384) a.slots *= 2;
   static std::atomic<bool> set[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e);
   if (dev >= 0 && dev < 64 && !set[dev].load()) {
-    e = cudaFuncSetAttribute(token_kernel<F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, 16384 * 3 * 4);
+    e = cudaFuncSetAttribute(token_kernel<F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, 16384 * 14);
     if (e != cudaSuccess) return cuda_fail(e);
     set[dev].store(true);
   }
-  return launch(token_kernel<F32>, dim3(B), dim3(LT_THREADS), (size_t)a.slots * words * 4, l, a);
+  // few sequences: several blocks each, as one SM's scattered loads and stores
+  // (some two cycles each) would be the bound
+  const int shares = std::max(1, std::min(16, 2 * sms / B));
+  return launch(token_kernel<F32>, dim3(shares, B), dim3(LT_THREADS), (size_t)a.slots * bytes, l, a);
 }
 
 }  // namespace
