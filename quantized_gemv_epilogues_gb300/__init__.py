@@ -131,9 +131,22 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_torch = None  # set by the first call that needs it
+
+
+def _get_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
 def _stream(stream):
     if stream is None:
-        import torch
+        torch = _torch or _get_torch()
+        if torch.cuda.is_initialized():
+            # the handle itself: building a Stream object takes 3 us
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -331,54 +344,58 @@ def mt_mlp_stack_run_noalloc(layers, d, f, group, fmt, eps, values, residual, ou
 
 
 def _typed(name, t, dtype, dim):
-    if t.dtype != dtype or t.dim() != dim:
+    if t.dtype is not dtype or t.dim() != dim:
         raise TypeError(f"{name}: a {dim}-dimensional {dtype} tensor is required, got {t.dim()}-dimensional {t.dtype}")
 
 
-def _flat(name, t, dtype, dim=1):
+def _flat(name, t, dtype, n=None):
+    """Address of a contiguous one-dimensional tensor (of n entries), None for None."""
     if t is None:
         return None
-    _typed(name, t, dtype, dim)
+    if t.dtype is not dtype or t.dim() != 1:
+        _typed(name, t, dtype, 1)
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name}: {n} entries are required")
     if not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous tensor is required")
     return t.data_ptr()
 
 
-def _head_rows(name, t, dtype, T, H, D):
-    """Pointer and row stride of a [T, H, D] tensor whose heads lie side by side."""
-    _typed(name, t, dtype, 3)
-    if tuple(t.shape) != (T, H, D):
-        raise ValueError(f"{name}: shape {(T, H, D)} is required, got {tuple(t.shape)}")
-    st = t.stride()
-    if (D > 1 and st[2] != 1) or (H > 1 and st[1] != D):
+def _head_rows(name, t, dtype, shape):
+    """Address and row stride of a [T, H, D] tensor whose heads lie side by side."""
+    if t.dtype is not dtype or t.shape != shape:
+        _typed(name, t, dtype, 3)
+        raise ValueError(f"{name}: shape {tuple(shape)} is required, got {tuple(t.shape)}")
+    row, head, one = t.stride()
+    T, H, D = shape
+    if (one != 1 and D > 1) or (head != D and H > 1):
         raise ValueError(f"{name}: heads must lie side by side in a row")
-    return t.data_ptr(), (st[0] if T > 1 else max(st[0], H * D))
+    return t.data_ptr(), (row if T > 1 else H * D)
 
 
 def _paged(k_cache, v_cache, pages, q_start, kv_len, T, max_q):
     """The cache and batch arguments from tensors: caches [pages, page, heads, dim]
     (any strides with contiguous dim, the same for both), pages int32 [B, n],
     q_start int32 [B + 1], kv_len int32 [B]."""
-    import torch
-    i32 = torch.int32
-    _typed("k_cache", k_cache, torch.bfloat16, 4)
-    _typed("v_cache", v_cache, torch.bfloat16, 4)
-    n, page, heads, dim = k_cache.shape
-    st = k_cache.stride()
-    if v_cache.shape != k_cache.shape or v_cache.stride() != st:
+    bf, i32 = _torch.bfloat16, _torch.int32
+    if k_cache.dtype is not bf or v_cache.dtype is not bf or k_cache.dim() != 4:
+        _typed("k_cache", k_cache, bf, 4)
+        _typed("v_cache", v_cache, bf, 4)
+    shape, st = k_cache.shape, k_cache.stride()
+    if v_cache.shape != shape or v_cache.stride() != st:
         raise ValueError("k_cache and v_cache must have the same shape and strides")
-    if dim > 1 and st[3] != 1:
+    n, page, heads, dim = shape
+    if st[3] != 1 and dim > 1:
         raise ValueError("k_cache: the last dimension must be contiguous")
-    _typed("pages", pages, i32, 2)
+    if pages.dtype is not i32 or pages.dim() != 2:
+        _typed("pages", pages, i32, 2)
     B, width = pages.shape
-    if width > 1 and pages.stride(1) != 1:
+    ld, one = pages.stride()
+    if one != 1 and width > 1:
         raise ValueError("pages: the last dimension must be contiguous")
-    ks, kl = _flat("q_start", q_start, i32), _flat("kv_len", kv_len, i32)
-    if q_start.shape[0] != B + 1 or kv_len.shape[0] != B:
-        raise ValueError(f"q_start must have {B + 1} entries and kv_len {B}")
     cache = PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1], st[2], n, page, heads, dim)
-    batch = PagedBatch(ks, kl, pages.data_ptr(), max(pages.stride(0), width) if B == 1 else pages.stride(0), B, T, width,
-                       int(max_q))
+    batch = PagedBatch(_flat("q_start", q_start, i32, B + 1), _flat("kv_len", kv_len, i32, B), pages.data_ptr(),
+                       ld if B > 1 else width, B, T, width, max_q)
     return cache, batch
 
 
@@ -388,32 +405,32 @@ def mt_rope_append(q, k, v, positions, inv_freq, q_out, k_cache, v_cache, pages,
     written to their cache positions.  q [T, q_heads, dim], k and v [T,
     kv_heads, dim] (bf16, rows at any stride); positions int32 [T] or [n_axes,
     T]; inv_freq float [rot / 2]; axis uint8 [rot / 2] or None (axis 0)."""
-    import torch
-    if q.dim() != 3:
-        raise TypeError("q: a 3-dimensional tensor is required")
-    T, H, D = q.shape
-    cache, batch = _paged(k_cache, v_cache, pages, q_start, kv_len, T, 1)
+    torch = _torch or _get_torch()
     bf = torch.bfloat16
-    qp, qs = _head_rows("q", q, bf, T, H, D)
-    kp, ks = _head_rows("k", k, bf, T, cache.kv_heads, D)
-    vp, vs = _head_rows("v", v, bf, T, cache.kv_heads, D)
-    op, os_ = _head_rows("q_out", q_out, bf, T, H, D)
+    shape = q.shape
+    if len(shape) != 3:
+        raise TypeError("q: a 3-dimensional tensor is required")
+    T, H, D = shape
+    cache, batch = _paged(k_cache, v_cache, pages, q_start, kv_len, T, 1)
     if D != cache.head_dim:
         raise ValueError(f"the cache's head size is {cache.head_dim}, q's is {D}")
-    pp = _flat("positions", positions, torch.int32, positions.dim() if positions.dim() in (1, 2) else 1)
-    axes = positions.shape[0] if positions.dim() == 2 else 1
-    if positions.shape[-1] != T:
-        raise ValueError(f"positions: {T} tokens are required")
-    fp = _flat("inv_freq", inv_freq, torch.float32)
-    half = inv_freq.shape[0]
-    ap = _flat("axis", axis, torch.uint8)
-    if axis is not None and axis.shape[0] != half:
-        raise ValueError(f"axis: {half} entries are required")
-    np_, kn = _flat("q_norm", q_norm, bf), _flat("k_norm", k_norm, bf)
-    for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
-        if w is not None and w.shape[0] != D:
-            raise ValueError(f"{name}: {D} entries are required")
-    _check(_lib.mt_rope_append(qp, qs, kp, ks, vp, vs, H, np_, kn, eps, pp, axes, fp, ap, 2 * half, pairing, op, os_,
+    kv_shape = (T, cache.kv_heads, D)
+    qp, qs = _head_rows("q", q, bf, shape)
+    kp, ks = _head_rows("k", k, bf, kv_shape)
+    vp, vs = _head_rows("v", v, bf, kv_shape)
+    op, os_ = _head_rows("q_out", q_out, bf, shape)
+    axes = 1
+    if positions.dim() == 2:
+        axes = positions.shape[0]
+    elif positions.dim() != 1:
+        _typed("positions", positions, torch.int32, 2)
+    if positions.dtype is not torch.int32 or not positions.is_contiguous() or positions.numel() != axes * T:
+        _typed("positions", positions, torch.int32, positions.dim())
+        raise ValueError(f"positions: contiguous rows of {T} tokens are required")
+    half = inv_freq.numel()
+    _check(_lib.mt_rope_append(qp, qs, kp, ks, vp, vs, H, _flat("q_norm", q_norm, bf, D), _flat("k_norm", k_norm, bf, D), eps,
+                               positions.data_ptr(), axes, _flat("inv_freq", inv_freq, torch.float32),
+                               _flat("axis", axis, torch.uint8, half), 2 * half, pairing, op, os_,
                                ctypes.byref(cache), ctypes.byref(batch), _stream(stream)), "mt_rope_append")
 
 
@@ -426,22 +443,26 @@ def mt_paged_attention(q, k_cache, v_cache, pages, q_start, kv_len, max_q, scale
     """Attention of the new tokens q [T, q_heads, dim] over the paged cache;
     out [T, q_heads, dim] (bf16 or fp32), lse float [T, q_heads] or None,
     window 0 for none.  max_q: the most new tokens of a sequence (a hint)."""
-    import torch
-    if q.dim() != 3:
+    torch = _torch or _get_torch()
+    shape = q.shape
+    if len(shape) != 3:
         raise TypeError("q: a 3-dimensional tensor is required")
-    T, H, D = q.shape
+    T, H, D = shape
     cache, batch = _paged(k_cache, v_cache, pages, q_start, kv_len, T, max_q)
     if D != cache.head_dim:
         raise ValueError(f"the cache's head size is {cache.head_dim}, q's is {D}")
-    qp, qs = _head_rows("q", q, torch.bfloat16, T, H, D)
-    f32 = out.dtype == torch.float32
-    op, os_ = _head_rows("out", out, torch.float32 if f32 else torch.bfloat16, T, H, D)
-    lp = _flat("lse", lse, torch.float32, 2)
-    if lse is not None and tuple(lse.shape) != (T, H):
-        raise ValueError(f"lse: shape {(T, H)} is required")
+    qp, qs = _head_rows("q", q, torch.bfloat16, shape)
+    f32 = out.dtype is torch.float32
+    op, os_ = _head_rows("out", out, torch.float32 if f32 else torch.bfloat16, shape)
+    lp = None
+    if lse is not None:
+        if lse.dtype is not torch.float32 or lse.shape != (T, H) or not lse.is_contiguous():
+            _typed("lse", lse, torch.float32, 2)
+            raise ValueError(f"lse: a contiguous tensor of shape {(T, H)} is required")
+        lp = lse.data_ptr()
     _check(_lib.mt_paged_attention(qp, qs, H, ctypes.byref(cache), ctypes.byref(batch), scale, window, sinks, op, os_,
-                                   MT_F32 if f32 else MT_BF16, lp, workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(), _stream(stream)), "mt_paged_attention")
+                                   MT_F32 if f32 else MT_BF16, lp, workspace.data_ptr(), workspace.nbytes,
+                                   _stream(stream)), "mt_paged_attention")
 
 
 def mt_logit_penalties(logits, out, history=None, history_start=None, prompt_len=None, repetition=None, presence=None,
@@ -450,44 +471,48 @@ def mt_logit_penalties(logits, out, history=None, history_start=None, prompt_len
     """Biases, penalties for repeated tokens and allowed-token masks on logits
     [B, V] (bf16 or fp32) into out (which may be logits); ragged int32 history
     and bias lists with [B + 1] starts, allowed int32 [B, words] bits."""
-    import torch
-    i32, f32 = torch.int32, torch.float32
-    _typed("logits", logits, f32 if logits.dtype == f32 else torch.bfloat16, 2)
-    _typed("out", out, logits.dtype, 2)
-    B, V = logits.shape
-    if out.shape != logits.shape or (V > 1 and (logits.stride(1) != 1 or out.stride(1) != 1)):
+    torch = _torch or _get_torch()
+    i32, f32, dt = torch.int32, torch.float32, logits.dtype
+    shape = logits.shape
+    if (dt is not f32 and dt is not torch.bfloat16) or len(shape) != 2 or out.dtype is not dt:
+        _typed("logits", logits, f32 if dt is f32 else torch.bfloat16, 2)
+        _typed("out", out, dt, 2)
+    B, V = shape
+    ld, one = logits.stride()
+    out_ld, out_one = out.stride()
+    if out.shape != shape or (V > 1 and (one != 1 or out_one != 1)):
         raise ValueError("logits and out must have the same shape and contiguous rows")
-    args = []
-    for name, t, dt, n in (("history", history, i32, None), ("history_start", history_start, i32, B + 1),
-                           ("prompt_len", prompt_len, i32, B), ("repetition", repetition, f32, B),
-                           ("presence", presence, f32, B), ("frequency", frequency, f32, B),
-                           ("bias_ids", bias_ids, i32, None), ("bias_values", bias_values, f32, None),
-                           ("bias_start", bias_start, i32, B + 1)):
-        args.append(_flat(name, t, dt))
-        if n is not None and t is not None and t.shape[0] != n:
-            raise ValueError(f"{name}: {n} entries are required")
-    hist, start, prompt, rep, pres, freq, ids, values, bstart = args
-    n_hist = history.shape[0] if history is not None else 0
-    n_bias = bias_ids.shape[0] if bias_ids is not None else 0
-    if bias_values is not None and bias_values.shape[0] != n_bias:
-        raise ValueError("bias_ids and bias_values must have the same length")
+    if B == 1:
+        ld = out_ld = V
+    hist = start = prompt = ids = values = bstart = ap = None
+    n_hist = n_bias = ald = 0
     # an empty tensor has no address: a list without entries is no list
-    if not n_hist:
-        hist = start = prompt = None
-    if not n_bias:
-        ids = values = bstart = None
-    ap, ald = None, 0
+    if history is not None:
+        n_hist = history.numel()
+        hist = _flat("history", history, i32) or None
+        start = _flat("history_start", history_start, i32, B + 1) if hist else None
+        prompt = _flat("prompt_len", prompt_len, i32, B) if hist else None
+    if bias_ids is not None:
+        n_bias = bias_ids.numel()
+        ids = _flat("bias_ids", bias_ids, i32) or None
+        values = _flat("bias_values", bias_values, f32, n_bias) if ids else None
+        bstart = _flat("bias_start", bias_start, i32, B + 1) if ids else None
     if allowed is not None:
-        _typed("allowed", allowed, i32, 2)
-        if allowed.shape[0] != B or (allowed.shape[1] > 1 and allowed.stride(1) != 1):
+        if allowed.dtype is not i32 or allowed.dim() != 2:
+            _typed("allowed", allowed, i32, 2)
+        rows, words = allowed.shape
+        ald, one = allowed.stride()
+        if rows != B or (words > 1 and one != 1):
             raise ValueError(f"allowed: {B} contiguous rows are required")
-        ap, ald = allowed.data_ptr(), (allowed.stride(0) if B > 1 else allowed.shape[1])
-        if allowed.shape[1] * 32 < V:
+        if words * 32 < V:
             raise ValueError(f"allowed: {(V + 31) // 32} words a row are required")
-    _check(_lib.mt_logit_penalties(logits.data_ptr(), logits.stride(0) if B > 1 else V, out.data_ptr(),
-                                   out.stride(0) if B > 1 else V, MT_F32 if logits.dtype == f32 else MT_BF16, B, V,
-                                   hist, start, prompt, n_hist, rep, pres, freq, ids, values, bstart, n_bias, ap, ald,
-                                   _stream(stream)), "mt_logit_penalties")
+        ap = allowed.data_ptr()
+        if B == 1:
+            ald = words
+    _check(_lib.mt_logit_penalties(logits.data_ptr(), ld, out.data_ptr(), out_ld, MT_F32 if dt is f32 else MT_BF16, B, V,
+                                   hist, start, prompt, n_hist, _flat("repetition", repetition, f32, B),
+                                   _flat("presence", presence, f32, B), _flat("frequency", frequency, f32, B), ids, values,
+                                   bstart, n_bias, ap, ald, _stream(stream)), "mt_logit_penalties")
 
 
 def mt_set_option(opt: int, value: int) -> None:
