@@ -122,6 +122,12 @@ __device__ __forceinline__ void cursor_next(const AttnArgs& a, Cursor& c) {
   cursor_tile<R, BK>(a, c);
 }
 
+// a / b for counts: by the 32-bit divider where both fit (a 64-bit division takes
+// about a thousand cycles, and the plan needs three of them one after the other).
+__device__ __forceinline__ long long div_count(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // The plan's shared memory: may overlap what the kernel uses after it.
 struct PlanShared {
   long long pre[PG_MAX_B + 1];  // units before each sequence
@@ -129,6 +135,87 @@ struct PlanShared {
   int big[PG_MAX_B];
   int n_big;
 };
+
+// The head, tile and unit of a sequence's unit `at`, of `each` to a head: by
+// every warp for itself, 32 tiles at a time.
+template <int R, int BK, int EXTRA>
+__device__ __forceinline__ void plan_tile(const AttnArgs& a, Cursor& c, long long each, long long at, int lane) {
+  c.tiles = tile_count<R>(a, c.s);
+  c.h = (int)div_count(at, each);
+  long long rest = at - (long long)c.h * each;
+  for (int rt0 = 0; rt0 < c.tiles; rt0 += 32) {
+    const int rt = rt0 + lane;
+    long long n = 0;
+    if (rt < c.tiles) {
+      const TileRows r = tile_rows<R>(a, c.s, rt);
+      n = tile_span<BK>(c.s, r.i0, r.i1, a.window, a.sinks).n + EXTRA;
+    }
+    long long in = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, in, o);
+      if (lane >= o) in += v;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, in > rest);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      c.rt = rt0 + l;
+      c.i = (int)(rest - __shfl_sync(0xffffffffu, in - n, l));
+      break;
+    }
+    rest -= __shfl_sync(0xffffffffu, in, 31);
+  }
+  cursor_tile<R, BK>(a, c);
+}
+
+// The plan for up to 32 sequences, a lane each, by every warp for itself: no
+// barrier and no shared memory.  (A kernel's first instructions run cold, and
+// the general plan below takes 6000 cycles, half of a short decode step.)
+template <int R, int BK, int EXTRA>
+__device__ __forceinline__ void plan_small(const AttnArgs& a, int cta, int ctas, long long* u0, long long* u1, long long* per, Cursor* cur) {
+  const PagedArgs& pg = a.pg;
+  const int lane = threadIdx.x & 31;
+  PagedSeq s = {0, 0, 0};
+  if (lane < pg.B) s = paged_seq(pg, lane);
+  const int tiles = tile_count<R>(a, s);
+  long long n = 0;  // units a head
+  if (tiles == 1) {
+    const TileRows r = tile_rows<R>(a, s, 0);
+    n = tile_span<BK>(s, r.i0, r.i1, a.window, a.sinks).n + EXTRA;
+  }
+  for (unsigned big = __ballot_sync(0xffffffffu, tiles > 1); big; big &= big - 1) {
+    const int l = __ffs(big) - 1;
+    const PagedSeq x = {__shfl_sync(0xffffffffu, s.row0, l), __shfl_sync(0xffffffffu, s.n, l), __shfl_sync(0xffffffffu, s.kv, l)};
+    const int count = __shfl_sync(0xffffffffu, tiles, l);
+    long long m = 0;
+    for (int rt = lane; rt < count; rt += 32) {
+      const TileRows r = tile_rows<R>(a, x, rt);
+      m += tile_span<BK>(x, r.i0, r.i1, a.window, a.sinks).n + EXTRA;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+    if (lane == l) n = m;
+  }
+  const long long units = n * pg.kv_heads;
+  long long inc = units;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  const long long total = __shfl_sync(0xffffffffu, inc, 31);
+  *per = max(div_count(total + ctas - 1, ctas), (long long)a.min_units);
+  *u0 = min((long long)cta * *per, total);
+  *u1 = min(*u0 + *per, total);
+  Cursor c = {};
+  if (*u0 < *u1) {
+    const int lo = __ffs(__ballot_sync(0xffffffffu, inc > *u0)) - 1;
+    c.b = lo;
+    c.s = PagedSeq{__shfl_sync(0xffffffffu, s.row0, lo), __shfl_sync(0xffffffffu, s.n, lo), __shfl_sync(0xffffffffu, s.kv, lo)};
+    plan_tile<R, BK, EXTRA>(a, c, __shfl_sync(0xffffffffu, n, lo), *u0 - __shfl_sync(0xffffffffu, inc - units, lo), lane);
+  }
+  *cur = c;
+}
 
 // Units of every sequence, their running sums, and the start of this CTA's
 // stretch: [u0, u1) of all units, `per` to a CTA; cur->i counts the tile's
@@ -138,6 +225,11 @@ template <int R, int BK, int NT, int EXTRA>
 __device__ void plan(const AttnArgs& a, PlanShared* sh, int cta, int ctas, long long* u0, long long* u1, long long* per,
                      Cursor* cur) {
   const PagedArgs& pg = a.pg;
+  if (pg.B <= 32) {
+    plan_small<R, BK, EXTRA>(a, cta, ctas, u0, u1, per, cur);
+    __syncthreads();
+    return;
+  }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) sh->n_big = 0;
   __syncthreads();
@@ -166,7 +258,10 @@ __device__ void plan(const AttnArgs& a, PlanShared* sh, int cta, int ctas, long 
       const TileRows r = tile_rows<R>(a, s, rt);
       n += tile_span<BK>(s, r.i0, r.i1, a.window, a.sinks).n + EXTRA;
     }
-    atomicAdd(reinterpret_cast<unsigned long long*>(&sh->pre[b + 1]), (unsigned long long)(n * pg.kv_heads));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    // (one per warp: a 64-bit addition to one word by every thread took 13000 cycles)
+    if (lane == 0) atomicAdd(reinterpret_cast<unsigned long long*>(&sh->pre[b + 1]), (unsigned long long)(n * pg.kv_heads));
   }
   __syncthreads();
   // running sums: a run of sequences per thread, then over the threads
@@ -182,7 +277,8 @@ __device__ void plan(const AttnArgs& a, PlanShared* sh, int cta, int ctas, long 
   if (lane == 31) sh->sum[warp] = inc;
   __syncthreads();
   long long base = inc - mine;
-  for (int w = 0; w < warp; ++w) base += sh->sum[w];
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) base += w < warp ? sh->sum[w] : 0;
   for (int b = b0; b < b1; ++b) {
     base += sh->pre[b + 1];
     sh->pre[b + 1] = base;
@@ -190,7 +286,7 @@ __device__ void plan(const AttnArgs& a, PlanShared* sh, int cta, int ctas, long 
   if (tid == 0) sh->pre[0] = 0;
   __syncthreads();
   const long long total = sh->pre[pg.B];
-  *per = max((total + ctas - 1) / ctas, (long long)a.min_units);
+  *per = max(div_count(total + ctas - 1, ctas), (long long)a.min_units);
   *u0 = min((long long)cta * *per, total);
   *u1 = min(*u0 + *per, total);
   Cursor c = {};
@@ -203,34 +299,7 @@ __device__ void plan(const AttnArgs& a, PlanShared* sh, int cta, int ctas, long 
     }
     c.b = lo;
     c.s = paged_seq(pg, lo);
-    c.tiles = tile_count<R>(a, c.s);
-    const long long each = (sh->pre[lo + 1] - sh->pre[lo]) / pg.kv_heads, at = *u0 - sh->pre[lo];
-    c.h = (int)(at / each);
-    long long rest = at - (long long)c.h * each;
-    // the tile: 32 at a time, by every warp for itself
-    for (int rt0 = 0; rt0 < c.tiles; rt0 += 32) {
-      const int rt = rt0 + lane;
-      long long n = 0;
-      if (rt < c.tiles) {
-        const TileRows r = tile_rows<R>(a, c.s, rt);
-        n = tile_span<BK>(c.s, r.i0, r.i1, a.window, a.sinks).n + EXTRA;
-      }
-      long long in = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, in, o);
-        if (lane >= o) in += v;
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, in > rest);
-      if (past) {
-        const int l = __ffs(past) - 1;
-        c.rt = rt0 + l;
-        c.i = (int)(rest - __shfl_sync(0xffffffffu, in - n, l));
-        break;
-      }
-      rest -= __shfl_sync(0xffffffffu, in, 31);
-    }
-    cursor_tile<R, BK>(a, c);
+    plan_tile<R, BK, EXTRA>(a, c, div_count(sh->pre[lo + 1] - sh->pre[lo], pg.kv_heads), *u0 - sh->pre[lo], lane);
   }
   *cur = c;
   __syncthreads();

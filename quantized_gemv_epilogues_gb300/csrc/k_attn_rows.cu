@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(AR_THREADS, ArShape<DP>::PER_SM) attn_rows_ker
               Lr > 0.f || Lr != Lr ? ((Mr == -INFINITY ? 0.f : Mr) + log2f(Lr)) * 0.6931471805599453f : -INFINITY;
       }
       if (!tile_done && i_first == 0 && tid == 0)
-        put_cut(a, cta, (int)((u0 + u + (cc.t.n - 1 - cc.i)) / per), cc);
+        put_cut(a, cta, (int)div_count(u0 + u + (cc.t.n - 1 - cc.i), per), cc);
       fresh = true;
     }
     if (u + 1 < units) cursor_next<AR_R, AR_BK>(a, cc);

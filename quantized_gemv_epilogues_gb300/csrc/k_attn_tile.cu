@@ -275,6 +275,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  if (tid < 4) {  // the maps' descriptors, on their way while the plan is made
+    const CUtensorMap* m = tid == 0 ? &qmap : tid == 1 ? &kmap : tid == 2 ? &vmap : &omap;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+  }
   pdl_wait();
   pdl_trigger();
   long long u0, u1, per;
@@ -348,7 +352,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             p.i1 = c.r.i1;
             p.p0 = c.r.p0;
             p.whole = i0 == 0 && i1 == c.t.n;
-            if (i0 == 0 && i1 < c.t.n) put_cut(a, blockIdx.x, (int)((u1 - left + all_units - c.i - 1) / per), c);
+            if (i0 == 0 && i1 < c.t.n) put_cut(a, blockIdx.x, (int)div_count(u1 - left + all_units - c.i - 1, per), c);
           }
           mbar_arrive(piece_full(k));
           if (stop) break;
@@ -402,7 +406,6 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           }
           return b;
         };
-        Box next = box(0);
         if (kv == 0 && lane == 0) {
           const int tps = a.tile_tokens >> 1;
 #pragma unroll
@@ -416,6 +419,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             ++asked[s];
           }
         }
+        Box next = box(0);
         ok = __all_sync(0xffffffffu, ok);
         for (int j = 0; ok && j < n; ++j) {
           Box b = next;
@@ -613,6 +617,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const uint32_t w = (low_bits(hi - 32 * q) & ~low_bits(lo - 32 * q)) | low_bits(sk - 32 * q);
+              if (__all_sync(0xffffffffu, w == 0xFFFFFFFFu)) continue;
+              asm volatile("");
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (!((w >> i) & 1u)) x[32 * q + i] = 0xFF800000u;
