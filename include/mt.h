@@ -477,8 +477,8 @@ typedef struct mt_paged_cache {
  * the device (4-byte aligned): lengths outside their ranges are clamped to
  * them, and an entry of `pages` that is needed but not in [0, num_pages) is
  * not followed (the call that meets one reads zeros, writes nothing, and sets
- * the device error word to MT_ERR_PAGE).  Entries of pages no token sees are
- * not read.
+ * the device error word to MT_ERR_PAGE).  Entries of pages no token sees may
+ * hold anything.
  */
 typedef struct mt_paged_batch {
   const int32_t* q_start; /* [B + 1] first row of each sequence's new tokens, not

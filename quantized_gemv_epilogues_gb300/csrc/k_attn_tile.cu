@@ -380,32 +380,12 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         const Piece& p = sh.piece[k % AT_PIECES];
         if (!ok || p.stop) break;
         const int n = max(p.n[0], p.n[1]), h = p.h;
-        struct Box {
-          bool mine;         // the lane has a box of the block
-          int page, row;     // the table's entry, the row in the page
-          bool seen;         // by some row of the tile
-          int tail0, tail1;  // V rows of the block beyond the sequence's end that a box still reads
-        };
-        auto box = [&](int j) -> Box {  // this lane's of block j
-          Box b = {false, a.pg.num_pages, 0, false, 0, 0};
-          if (j >= n) return b;
-          const int i = p.first + j, blk0 = (i < p.sink ? i : i - p.sink + p.win) * AT_BK;
-          const int t0 = p.kv - blk0, t1 = min((t0 + box_rows - 1) / box_rows * box_rows, AT_BK);
-          if (kv && t0 > 0 && t0 < AT_BK && t1 > t0) {
-            b.tail0 = t0;
-            b.tail1 = t1;
-          }
-          if (lane >= boxes) return b;
-          b.mine = true;
-          const int k0 = blk0 + lane * box_rows;
-          if (k0 < p.key_end && (k0 + box_rows > p.win_lo || k0 < a.sinks)) {
-            const int e = k0 / a.pg.page_size;
-            b.page = __ldg(a.pg.pages + (int64_t)p.b * a.pg.pages_ld + e);
-            b.row = k0 - e * a.pg.page_size;
-            b.seen = true;
-          }
-          return b;
-        };
+        // Entries of the sequence's row of the table: the lane's own of the 32
+        // from e0 on and of the next 32.  (A load per block, even one block
+        // ahead, held the warp to a block in 1300 cycles.)
+        const int32_t* const table = a.pg.pages + (int64_t)p.b * a.pg.pages_ld;
+        auto entries = [&](int e) -> int { return e + lane < a.pg.max_pages ? __ldg(table + e + lane) : -1; };
+        int e0 = -(1 << 30), here = -1, there = -1;
         if (kv == 0 && lane == 0) {
           const int tps = a.tile_tokens >> 1;
 #pragma unroll
@@ -419,34 +399,51 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             ++asked[s];
           }
         }
-        Box next = box(0);
         ok = __all_sync(0xffffffffu, ok);
         for (int j = 0; ok && j < n; ++j) {
-          Box b = next;
-          if (b.seen && (unsigned)b.page >= (unsigned)a.pg.num_pages) {
-            atomicExch(a.pg.err, (int)MT_ERR_PAGE);
-            b.page = a.pg.num_pages;  // zeros, as for a box that no row sees
+          const int i = p.first + j, blk0 = (i < p.sink ? i : i - p.sink + p.win) * AT_BK;
+          // rows of the block beyond the sequence's end that a box still reads (V's are zeroed below)
+          const int tail0 = p.kv - blk0, tail1 = min((tail0 + box_rows - 1) & -box_rows, AT_BK);
+          const bool patch = kv && tail0 > 0 && tail0 < AT_BK && tail1 > tail0;
+          // this lane's box: the table's entry and the row in the page
+          const int k0 = blk0 + lane * box_rows, e = k0 / a.pg.page_size;
+          const int first = __shfl_sync(0xffffffffu, e, 0), last = __shfl_sync(0xffffffffu, e, boxes - 1);
+          if (first < e0 || last >= e0 + 64) {
+            e0 = first;
+            here = entries(e0);
+            there = entries(e0 + 32);
+          } else if (first >= e0 + 32) {
+            e0 += 32;
+            here = there;
+            there = entries(e0 + 32);
           }
-          next = box(j + 1);  // its load returns while this block is asked for
+          const int p_here = __shfl_sync(0xffffffffu, here, (e - e0) & 31), p_there = __shfl_sync(0xffffffffu, there, (e - e0) & 31);
+          int page = a.pg.num_pages, row = 0;  // beyond the cache: zeros, for a box that no row sees
+          if (lane < boxes && k0 < p.key_end && (k0 + box_rows > p.win_lo || k0 < a.sinks)) {
+            const int x = e - e0 < 32 ? p_here : p_there;
+            row = k0 - e * a.pg.page_size;
+            if ((unsigned)x < (unsigned)a.pg.num_pages) page = x;
+            else atomicExch(a.pg.err, (int)MT_ERR_PAGE);
+          }
           const int q = st % NS;
           if (st >= NS) ok = wait(kv_free(q), ((st / NS) + 1) & 1);
           if (!ok) break;
-          const uint32_t bar = b.tail1 ? tail_bar : kv_full(q), dst = stage(q);
+          const uint32_t bar = patch ? tail_bar : kv_full(q), dst = stage(q);
           if (lane == 0) mbar_arrive_expect_tx(bar, S::TILE);
           __syncwarp();
-          if (b.mine) {
+          if (lane < boxes) {
 #pragma unroll
             for (int c = 0; c < S::CH; ++c)
-              tma_load_4d(dst + c * S::HALF + lane * box_rows * 128, map, 64 * c, b.row, h, b.page, bar);
+              tma_load_4d(dst + c * S::HALF + lane * box_rows * 128, map, 64 * c, row, h, page, bar);
           }
           st += 2;
-          if (b.tail1) {
+          if (patch) {
             ok = wait(tail_bar, tails & 1);
             ++tails;
             unsigned char* v = smem + S::OFF_KV + (size_t)q * S::TILE;
-            for (int x = lane; x < (b.tail1 - b.tail0) * 8 * S::CH; x += 32) {
-              const int c = x & 7, r = (x >> 3) % (b.tail1 - b.tail0), hh = (x >> 3) / (b.tail1 - b.tail0);
-              *reinterpret_cast<uint4*>(v + hh * S::HALF + (b.tail0 + r) * 128 + 16 * c) = make_uint4(0, 0, 0, 0);
+            for (int x = lane; x < (tail1 - tail0) * 8 * S::CH; x += 32) {
+              const int c = x & 7, r = (x >> 3) % (tail1 - tail0), hh = (x >> 3) / (tail1 - tail0);
+              *reinterpret_cast<uint4*>(v + hh * S::HALF + (tail0 + r) * 128 + 16 * c) = make_uint4(0, 0, 0, 0);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
