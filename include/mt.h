@@ -554,15 +554,20 @@ mt_status mt_rope_append(const void* q, int64_t q_stride, const void* k, int64_t
  *   workspace: at least mt_paged_attention_workspace_bytes(...) bytes, 16-byte
  *              aligned, contents of no account: partial results where one
  *              sequence's keys are shared out over several SMs (joined in key
- *              order by a second kernel, so results do not vary between runs)
+ *              order by a second kernel, so results do not vary between runs).
+ *              Calls that may overlap in time need one each.
  * Rows that belong to no sequence are neither read nor written; T = 0 does
  * nothing (the row pointers may then be NULL).
- * Products are bf16 with fp32 accumulation, softmax statistics fp32.  The
- * weights exp(s_j - max) enter the product with V as bf16 (one rounding of
- * 2^-8 each) in the kernel for long chunks, and as a sum of two bf16 (2^-16)
- * in the kernel for few rows, which serves all fp32 outputs.
- * A non-finite V of a key that is beyond kv_len, or that no new token of the
- * row's tile sees, does not reach the output.
+ * Products are bf16 with fp32 accumulation, softmax statistics fp32.  bf16
+ * outputs with 64 <= head_dim <= 128 and page_size a multiple of 8 run on the
+ * tcgen05 tensor cores, where the weights exp(s_j - max) enter the product
+ * with V as bf16 (one rounding of at most 2^-8 each); all others, fp32 outputs
+ * among them, on a kernel that takes the weights as a sum of two bf16 (2^-16).
+ * What lies in the cache at keys that no new token of a row's tile sees (a
+ * tile holds at most 256 rows: query heads of one key/value head times
+ * neighbouring tokens) does not reach the output, NaN or not: a single new
+ * token is not touched by what it does not see.  A non-finite V that some of
+ * the tile's tokens see may reach the others.
  * Limits: 1 <= q_heads <= 1024, q_heads % kv_heads == 0, q_heads / kv_heads <=
  *         128; scale > 0 and finite; window >= 0; sinks >= 0; strides
  *         multiples of 8; pointers 16-byte aligned (lse 4).

@@ -17,13 +17,15 @@
 //    the page size (at most 128), one lane of the producer warp each, with the
 //    page's index from the table as a TMA coordinate; boxes that no row sees,
 //    or whose entry is out of range, are asked for at a page beyond the cache,
-//    which TMA fills with zeros.  Rows beyond the sequence's end in its last
-//    page may hold anything: the producer zeroes V's before handing it on (a
-//    weight of zero times NaN is NaN).
+//    which TMA fills with zeros.  Keys of a box that no row sees (beyond the
+//    sequence's end in its last page, before the window in its first) may hold
+//    anything: the producer zeroes their V before handing it on (a weight of
+//    zero times NaN is NaN).
 //  * One softmax warpgroup per tile, one row per thread, so that maxima and
 //    sums need no exchange and no warp waits for another.  (Two warpgroups a
 //    tile, half a row per thread, cost more in the exchange than the shorter
-//    rows gained: 521 against XXX us for a prompt of 8000.)  The row's reference maximum moves only when a
+//    rows gained: 521 against 426 us for a prompt of 8000, all else as it then
+//    was.)  The row's reference maximum moves only when a
 //    score exceeds it by more than 2^8 (8 in log2 units): fp32 sums and bf16
 //    weights lose nothing by weights up to 2^8, and O is rescaled in tensor
 //    memory only then - once or twice a row, typically.  When S of block j is
@@ -402,9 +404,13 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         ok = __all_sync(0xffffffffu, ok);
         for (int j = 0; ok && j < n; ++j) {
           const int i = p.first + j, blk0 = (i < p.sink ? i : i - p.sink + p.win) * AT_BK;
-          // rows of the block beyond the sequence's end that a box still reads (V's are zeroed below)
-          const int tail0 = p.kv - blk0, tail1 = min((tail0 + box_rows - 1) & -box_rows, AT_BK);
-          const bool patch = kv && tail0 > 0 && tail0 < AT_BK && tail1 > tail0;
+          // The block's keys that no row sees start at the sequence's (or the
+          // last token's) end, and lie between the sinks and the first window.
+          // Where such a border falls within a box, V's rows beyond it are
+          // zeroed below: a weight of zero times what lies there may be NaN.
+          const int end = p.key_end - blk0, gap0 = a.sinks - blk0, gap1 = p.win_lo - blk0;
+          auto within = [&](int x) -> bool { return x > 0 && x < AT_BK && (x & (box_rows - 1)); };
+          const bool patch = kv && (within(end) || (gap1 > gap0 && (within(gap1) || within(gap0))));
           // this lane's box: the table's entry and the row in the page
           const int k0 = blk0 + lane * box_rows, e = k0 / a.pg.page_size;
           const int first = __shfl_sync(0xffffffffu, e, 0), last = __shfl_sync(0xffffffffu, e, boxes - 1);
@@ -441,10 +447,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             ok = wait(tail_bar, tails & 1);
             ++tails;
             unsigned char* v = smem + S::OFF_KV + (size_t)q * S::TILE;
-            for (int x = lane; x < (tail1 - tail0) * 8 * S::CH; x += 32) {
-              const int c = x & 7, r = (x >> 3) % (tail1 - tail0), hh = (x >> 3) / (tail1 - tail0);
-              *reinterpret_cast<uint4*>(v + hh * S::HALF + (tail0 + r) * 128 + 16 * c) = make_uint4(0, 0, 0, 0);
-            }
+            for (int r = lane; r < AT_BK; r += 32)
+              if (r >= end || (r >= gap0 && r < gap1))
+                for (int c = 0; c < 8 * S::CH; ++c)  // 16 bytes each
+                  *reinterpret_cast<uint4*>(v + (c >> 3) * S::HALF + r * 128 + 16 * ((c + r) & 7)) = make_uint4(0, 0, 0, 0);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(kv_full(q));

@@ -15,7 +15,8 @@
 //    dependent launch) before it writes.
 // (One kernel, whose blocks each took a chunk of the vocabulary and counted
 // the tokens that fell there, read every history 16 times and spent its time
-// on those loads' latency: 50 us where this takes XX for 200 texts.)
+// on those loads' latency: 50 us where this takes 34 for 200
+// texts.)
 // Counts are integers and a repeated bias entry is resolved by its index, so no
 // result depends on the order of the atomics.
 #include <math.h>

@@ -61,6 +61,13 @@ def test_chunks(mt, heads, lens):
     compare(mt, Paged(lens, *heads, page=16, seed=2))
 
 
+@pytest.mark.parametrize("heads", [(128, 1, 64), (100, 1, 64), (33, 1, 128), (66, 2, 88), (7, 7, 120), (32, 1, 64), (4, 4, 104)],
+                         ids=lambda h: "x".join(map(str, h)))
+def test_other_groups_and_head_sizes(mt, heads):
+    compare(mt, Paged([(1, 300), (5, 70), (41, 200), (3, 3)], *heads, page=16, seed=20))
+    compare(mt, Paged([(1, 300), (41, 200)], *heads, page=16, seed=20), window=50, sinks=2)
+
+
 @pytest.mark.parametrize("page", [1, 3, 8, 20, 24, 48, 64, 128, 256])
 @pytest.mark.parametrize("lens", [[(1, 130), (1, 401)], [(140, 333), (2, 9)]], ids=["decode", "chunk"])
 def test_page_sizes(mt, page, lens):
@@ -124,6 +131,33 @@ def test_pages_that_no_token_sees_are_not_followed(mt):
         assert mt.mt_device_error(False) == 0
 
 
+@pytest.mark.parametrize("page", [16, 64, 128, 12])
+@pytest.mark.parametrize("window,sinks", [(37, 0), (100, 5), (130, 131), (1, 20)])
+def test_keys_that_a_token_does_not_see_may_be_nan(mt, page, window, sinks):
+    # one new token each: every key outside its window and sinks holds NaN and infinities
+    p = Paged([(1, 500), (1, 129), (1, 40), (1, 257)], 8, 2, 64, page=page, seed=23)
+    for b, (_, kv) in enumerate(p.lens):
+        for j in range(sinks, kv - window):
+            for x, bad in ((p.k, math.nan), (p.v, math.nan if j % 2 else math.inf)):
+                x[p.pages[b, j // page], j % page] = bad
+    compare(mt, p, window, sinks)
+
+
+@pytest.mark.parametrize("page", [16, 128])
+def test_tokens_after_a_tile_may_be_nan(mt, page):
+    # one head to a group: a tile is 256 tokens, and the last token of 300 is NaN
+    p = Paged([(300, 300)], 2, 2, 64, page=page, seed=24)
+    p.k[p.pages[0, 299 // page], 299 % page] = math.nan
+    p.v[p.pages[0, 299 // page], 299 % page] = math.nan
+    p.k[p.pages[0, 257 // page], 257 % page] = math.nan
+    p.v[p.pages[0, 257 // page], 257 % page] = math.inf
+    out, lse = run(mt, p, 0.125)
+    ref = attention_ref(p, 0.125)
+    tol_out, tol_lse = attention_bounds(p, ref, 2.0 ** -8, torch.bfloat16)
+    check(out[:256], ref[0][:256], tol_out[:256])
+    check(lse[:256], ref[1][:256], tol_lse[:256])
+
+
 @pytest.mark.parametrize("lens", [[(1, 100)], [(130, 200)]], ids=["decode", "chunk"])
 def test_page_out_of_range_is_reported(mt, lens):
     # the entry is checked on the device before it is followed; its keys count as zeros
@@ -172,6 +206,40 @@ def test_chunks_and_single_tokens_in_every_order(mt, heads):
 def test_many_sequences(mt):
     lens = [(1 if b % 7 else 0, (b * 37) % 200 + 1) for b in range(1024)]
     compare(mt, Paged(lens, 4, 2, 64, page=16, seed=15))
+
+
+def test_many_sequences_with_chunks(mt):
+    lens = [(200 + b, 210 + 3 * b) if b % 9 == 0 else (b % 4, 5 * b + 3) for b in range(45)]
+    compare(mt, Paged(lens, 8, 2, 64, page=16, seed=21))
+    compare(mt, Paged(lens, 8, 2, 64, page=12, seed=21), window=70, sinks=5)
+
+
+@pytest.mark.parametrize("page", [16, 12], ids=["chunk-kernel", "rows-kernel"])
+def test_offsets_beyond_32_bits(mt, page):
+    # two pages 2^31 elements apart, V after K in the same allocation
+    far = 1 << 31
+    p = Paged([(9, 2 * page)], 4, 2, 64, page=page, seed=22, spare=0)
+    store = torch.empty(far + 2 * page * 2 * 64, dtype=torch.bfloat16, device="cuda")
+    size, strides = (2, page, 2, 64), (far, 128, 64, 1)
+    k, v = store.as_strided(size, strides), store.as_strided(size, strides, page * 128)
+    k.copy_(p.k)
+    v.copy_(p.v)
+    q, _, _, pages, q_start, kv_len = p.cuda()
+    out, lse = torch.empty_like(q), torch.empty(p.T, 4, device="cuda")
+    ws = torch.empty(mt.mt_paged_attention_workspace_bytes(p.T, 1, 4, 2, 64), dtype=torch.uint8, device="cuda")
+    mt.mt_paged_attention(q, k, v, pages, q_start, kv_len, 9, 0.125, out, ws, lse=lse)
+    ref = attention_ref(p, 0.125)
+    tol_out, tol_lse = attention_bounds(p, ref, 2.0 ** -8, torch.bfloat16)
+    check(out, ref[0], tol_out)
+    check(lse, ref[1], tol_lse)
+    # and the write: the same tokens again, unturned (position 0)
+    new = torch.randn(9, 2, 64, device="cuda").to(torch.bfloat16)
+    mt.mt_rope_append(q, new, new, torch.zeros(9, dtype=torch.int32, device="cuda"), torch.ones(32, device="cuda"), out, k, v, pages,
+                      q_start, kv_len)
+    for i in range(9):
+        at = 2 * page - 9 + i
+        pg, r = int(p.pages[0, at // page]), at % page
+        assert torch.equal(k[pg, r], new[i]) and torch.equal(v[pg, r], new[i])
 
 
 def test_long_text_split_over_the_gpu(mt):
