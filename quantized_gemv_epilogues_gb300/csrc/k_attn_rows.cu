@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(AR_THREADS, ArShape<DP>::PER_SM) attn_rows_ker
       }
     }
     // offsets of block u + ST into the half that block u + ST - 2 used: its
-    // copies were issued before this round's barrier
+    // copies were issued before this step's barrier
     if (more && tid < AR_BK) off_sh[(u + ST) & 1][tid] = off_next;
 
     const bool tile_done = cc.i + 1 == cc.t.n;

@@ -737,8 +737,12 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             }
           }
         };
+        // A decode step's few rows are stored from where they are: the copies
+        // above take 1200 cycles each, four of them for a part.
+        const bool few = __popc(rows_here) <= 8;
 #pragma unroll
         for (int c0 = 0; c0 < DP; c0 += 64) {
+          if (rows_here == 0) break;
           uint32_t o[64];
           if (n > 0) {
             at_ld32(t_o + c0, o);
@@ -753,7 +757,20 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             uint32_t w[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) w[i] = bf16x2(__uint_as_float(o[2 * i]) * f, __uint_as_float(o[2 * i + 1]) * f);
-            send(w, c0);
+            if (!few) {
+              send(w, c0);
+            } else if (row) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (c0 + 8 * i < D)
+                  *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + at + c0 + 8 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            }
+          } else if (few) {
+            if (row) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                *reinterpret_cast<uint4*>(a.part_o + part_at<AT_R, DP>(slot, 128 * s + r, c0 + 4 * i)) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
           } else {
             send(o, c0);
             send(o + 32, c0 + 32);
