@@ -17,9 +17,13 @@
 // this balances every mixture to one block.  A tile that a stretch boundary
 // cuts leaves parts in the workspace (at most two per CTA), which a second
 // kernel joins in key order; the sum's order depends only on the lengths.
-// A tile also has EXTRA units before its blocks, which stand for the time that
-// its start and its output take: a stretch that begins or ends among them
-// begins or ends at the tile's first block.
+// The kernel for chunks weighs its tiles (EXTRA > 0): a tile has EXTRA units
+// before its blocks, which stand for the time that its start and its output
+// take (a stretch that begins or ends among them begins or ends at the tile's
+// first block), and a block is 3 units, or 2 where only one of the two 128-row
+// tiles has rows.  (A chunk of 384 beside 15 single tokens: 78 us, and 85 with
+// equal blocks, 94 with 3 and 4; a prompt of 8000: 338, 343 and 341 us.)  A
+// stretch border within a block leaves the block to the later stretch.
 #pragma once
 #include <float.h>
 
@@ -89,6 +93,16 @@ __device__ __forceinline__ int tile_count(const AttnArgs& a, const PagedSeq& s) 
   return (s.n * a.group + per - 1) / per;  // n <= 2^22, group <= 128: within 31 bits
 }
 
+template <int EXTRA>
+__device__ __forceinline__ int block_units(const AttnArgs& a, const TileRows& r) {
+  return EXTRA == 0 ? 1 : r.rows > a.tile_tokens / 2 * a.group ? 3 : 2;
+}
+template <int R, int BK, int EXTRA>
+__device__ __forceinline__ int tile_units(const AttnArgs& a, const PagedSeq& s, int rt) {
+  const TileRows r = tile_rows<R>(a, s, rt);
+  return EXTRA + block_units<EXTRA>(a, r) * tile_span<BK>(s, r.i0, r.i1, a.window, a.sinks).n;
+}
+
 // A position in the line of units.
 struct Cursor {
   int b, h, rt, i, tiles;
@@ -146,10 +160,7 @@ __device__ __forceinline__ void plan_tile(const AttnArgs& a, Cursor& c, long lon
   for (int rt0 = 0; rt0 < c.tiles; rt0 += 32) {
     const int rt = rt0 + lane;
     long long n = 0;
-    if (rt < c.tiles) {
-      const TileRows r = tile_rows<R>(a, c.s, rt);
-      n = tile_span<BK>(c.s, r.i0, r.i1, a.window, a.sinks).n + EXTRA;
-    }
+    if (rt < c.tiles) n = tile_units<R, BK, EXTRA>(a, c.s, rt);
     long long in = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -179,19 +190,13 @@ __device__ __forceinline__ void plan_small(const AttnArgs& a, int cta, int ctas,
   if (lane < pg.B) s = paged_seq(pg, lane);
   const int tiles = tile_count<R>(a, s);
   long long n = 0;  // units a head
-  if (tiles == 1) {
-    const TileRows r = tile_rows<R>(a, s, 0);
-    n = tile_span<BK>(s, r.i0, r.i1, a.window, a.sinks).n + EXTRA;
-  }
+  if (tiles == 1) n = tile_units<R, BK, EXTRA>(a, s, 0);
   for (unsigned big = __ballot_sync(0xffffffffu, tiles > 1); big; big &= big - 1) {
     const int l = __ffs(big) - 1;
     const PagedSeq x = {__shfl_sync(0xffffffffu, s.row0, l), __shfl_sync(0xffffffffu, s.n, l), __shfl_sync(0xffffffffu, s.kv, l)};
     const int count = __shfl_sync(0xffffffffu, tiles, l);
     long long m = 0;
-    for (int rt = lane; rt < count; rt += 32) {
-      const TileRows r = tile_rows<R>(a, x, rt);
-      m += tile_span<BK>(x, r.i0, r.i1, a.window, a.sinks).n + EXTRA;
-    }
+    for (int rt = lane; rt < count; rt += 32) m += tile_units<R, BK, EXTRA>(a, x, rt);
 #pragma unroll
     for (int o = 16; o; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
     if (lane == l) n = m;
@@ -239,10 +244,7 @@ __device__ void plan(const AttnArgs& a, PlanShared* sh, int cta, int ctas, long 
     const int tiles = tile_count<R>(a, s);
     long long n = 0;
     if (tiles <= 4) {
-      for (int rt = 0; rt < tiles; ++rt) {
-        const TileRows r = tile_rows<R>(a, s, rt);
-        n += tile_span<BK>(s, r.i0, r.i1, a.window, a.sinks).n + EXTRA;
-      }
+      for (int rt = 0; rt < tiles; ++rt) n += tile_units<R, BK, EXTRA>(a, s, rt);
     } else {
       sh->big[atomicAdd(&sh->n_big, 1)] = b;
     }
@@ -254,10 +256,7 @@ __device__ void plan(const AttnArgs& a, PlanShared* sh, int cta, int ctas, long 
     const PagedSeq s = paged_seq(pg, b);
     const int tiles = tile_count<R>(a, s);
     long long n = 0;
-    for (int rt = tid; rt < tiles; rt += NT) {
-      const TileRows r = tile_rows<R>(a, s, rt);
-      n += tile_span<BK>(s, r.i0, r.i1, a.window, a.sinks).n + EXTRA;
-    }
+    for (int rt = tid; rt < tiles; rt += NT) n += tile_units<R, BK, EXTRA>(a, s, rt);
 #pragma unroll
     for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
     // (one per warp: a 64-bit addition to one word by every thread took 13000 cycles)

@@ -53,7 +53,7 @@ namespace mt {
 namespace {
 
 constexpr int AT_BK = 128, AT_R = 256, AT_THREADS = 384;
-constexpr int AT_EXTRA = 3;  // units of a tile beside its blocks: the blocks that its start and output take as long as
+constexpr int AT_EXTRA = 6;  // units of a tile beside its blocks' 3 or 2
 constexpr int AT_SOFT = 8;  // warps 0-7: softmax; tile warp / 4, rows 32 (warp % 4) on
 constexpr int AT_MMA = 8, AT_WALK = 9, AT_LOAD = 10;  // AT_LOAD: Q and K, and the next warp V
 
@@ -328,9 +328,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           if (k >= AT_PIECES && !wait1(piece_free(k), ((k / AT_PIECES) + 1) & 1)) break;
           Piece& p = sh.piece[k % AT_PIECES];
           // blocks [i0, i1) of the tile
-          const int all_units = c.t.n + AT_EXTRA, end = (int)min((long long)all_units, c.i + left);
-          const int i0 = max(c.i - AT_EXTRA, 0), i1 = end - AT_EXTRA;
-          const bool stop = left <= 0 || i1 <= 0;  // (a stretch that ends among the extra units leaves the tile to the next)
+          const int w = block_units<AT_EXTRA>(a, c.r), all_units = AT_EXTRA + w * c.t.n;
+          const int end = (int)min((long long)all_units, c.i + left);
+          const int i0 = max(c.i - AT_EXTRA, 0) / w, i1 = (end - AT_EXTRA) / w;
+          // (a stretch that ends before a tile's first block does leaves the tile to the next)
+          const bool stop = left <= 0 || end < AT_EXTRA + w;
           p.stop = stop;
           if (!stop) {
 #pragma unroll
@@ -833,7 +835,7 @@ mt_status run_tile(AttnArgs a, void* ws, const Launch& l, const DeviceInfo* di) 
   const PagedArgs& pg = a.pg;
   const int tps = 128 / a.group, box = at_box(pg.page_size);
   a.tile_tokens = 2 * tps;
-  a.min_units = 1;
+  a.min_units = 3;  // no stretch without a block
   CUtensorMap qmap, kmap, vmap, omap;
   const cuuint64_t row = (cuuint64_t)pg.head_dim * 2;
   {
