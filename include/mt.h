@@ -492,8 +492,8 @@ typedef struct mt_paged_batch {
   int T;                  /* rows, 0 .. 2^22 */
   int max_pages;          /* entries of a row; max_pages * page_size <= 2^30 */
   int max_q;              /* the most new tokens of a sequence, as far as the
-                             host knows: it chooses between kernels, and any
-                             value gives the same results */
+                             host knows: it sizes a launch, and any value gives
+                             the same results */
 } mt_paged_batch;
 
 typedef enum mt_rope_pairing {

@@ -444,11 +444,11 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) attn_join_kernel(const AttnAr
 }
 
 // Blocks of the joining kernel for each cut: as many as a tile has rows, as far
-// as the host knows (each block strides over them), but at most 8: blocks that
+// as the host knows (each block strides over them), but at most 16: blocks that
 // find nothing to join still cost their launch.
 inline int join_blocks(const AttnArgs& a) {
   const int64_t rows = (int64_t)(a.max_q > 0 ? a.max_q : 1) * a.group;
-  return (int)(rows < 8 ? rows : 8);
+  return (int)(rows < 8 ? rows : rows < 64 ? 8 : 16);
 }
 
 // Launchers (k_attn_rows.cu, k_attn_tile.cu): the main kernel and the join.

@@ -10,7 +10,8 @@
 // most 2^-33 turns at any 31-bit position.  Its upper 32 bits go to
 // sincospif.
 //
-// Bound: memory, 4 bytes an element (bf16 in, bf16 out).  A block takes TOK
+// Bound: memory, 4 bytes an element (bf16 in, bf16 out), 5.3 TB/s on 11 000
+// tokens of 32 + 8 + 8 heads of 128.  A block takes TOK
 // tokens (one when there are few) and a range of their heads, computes each
 // token's rot/2 sines and cosines once into shared memory, and then L lanes
 // take one head's row at a time: each lane holds the 16-byte chunks of both
@@ -65,6 +66,13 @@ __device__ __forceinline__ uint64_t turn_fraction(float f) {
   return (bits >> 31) ? 0ull - r : r;
 }
 
+// Where pair i's cosine and sine lie: two neighbouring pairs together, and the
+// pairs that neighbouring lanes read at once (8, or 4, apart) side by side.
+template <bool ADJ>
+__device__ __forceinline__ int cs_at(int i) {
+  return ADJ ? (((i >> 1) & 1) * 32 + (i >> 2)) * 2 + (i & 1) : (((i >> 1) & 3) * 16 + (i >> 3)) * 2 + (i & 1);
+}
+
 struct Chunk {
   float x[8];
 };
@@ -72,21 +80,28 @@ __device__ __forceinline__ Chunk chunk_load(const uint16_t* p) {
   const uint4 v = *reinterpret_cast<const uint4*>(p);
   return Chunk{{bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y), bf16lo(v.z), bf16hi(v.z), bf16lo(v.w), bf16hi(v.w)}};
 }
-__device__ __forceinline__ uint32_t pack2(float a, float b) { return (uint32_t)f2bf(a) | ((uint32_t)f2bf(b) << 16); }
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
 __device__ __forceinline__ void chunk_store(uint16_t* p, const Chunk& c) {
   *reinterpret_cast<uint4*>(p) =
       make_uint4(pack2(c.x[0], c.x[1]), pack2(c.x[2], c.x[3]), pack2(c.x[4], c.x[5]), pack2(c.x[6], c.x[7]));
 }
 
-template <int L, bool ADJ, int TOK>
-__global__ void __launch_bounds__(RP_THREADS) rope_append_kernel(const RopeArgs a) {
-  __shared__ float2 cs[TOK][128];  // cosine and sine of each token's pairs
-  __shared__ int seq_sh[TOK];      // the token's sequence, -1 for none
-  __shared__ int place_sh[TOK];    // its position in the cache, -1 if it is not in it
+template <int L, bool ADJ, int TOK, int BLOCKS>
+__global__ void __launch_bounds__(RP_THREADS, BLOCKS) rope_append_kernel(const RopeArgs a) {
+  __shared__ __align__(16) float2 cs[TOK][128];  // cosine and sine of each token's pairs, at cs_at()
+  __shared__ int seq_sh[TOK];                    // the token's sequence, -1 for none
+  __shared__ int64_t at_sh[TOK];                 // its row's first element in the cache, -1 if it has none
   const PagedArgs& pg = a.pg;
   const int tid = threadIdx.x;
   const int t0 = blockIdx.x * TOK;
-  if (tid < TOK) seq_sh[tid] = place_sh[tid] = -1;
+  if (tid < TOK) {
+    seq_sh[tid] = -1;
+    at_sh[tid] = -1;
+  }
   pdl_wait();
   pdl_trigger();
   __syncthreads();
@@ -99,8 +114,11 @@ __global__ void __launch_bounds__(RP_THREADS) rope_append_kernel(const RopeArgs 
       const int at = t0 + i - s.row0;
       if (at >= 0 && at < s.n) {
         seq_sh[i] = b;
-        const int p = s.kv - s.n + at;
-        place_sh[i] = p >= 0 ? p : -1;
+        const int pl = s.kv - s.n + at;
+        if (pl >= 0) {
+          const int e = pl / pg.page_size, page = paged_entry(pg, b, e);
+          if (page >= 0) at_sh[i] = (int64_t)page * pg.page_stride + (int64_t)(pl - e * pg.page_size) * pg.token_stride;
+        }
       }
     }
   }
@@ -115,7 +133,7 @@ __global__ void __launch_bounds__(RP_THREADS) rope_append_kernel(const RopeArgs 
       const uint64_t turns = (uint64_t)(int64_t)__ldg(pos + t0 + k) * F;
       float s, c;
       sincospif((float)(int32_t)(turns >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
-      cs[k][i] = make_float2(c, s);
+      cs[k][cs_at<ADJ>(i)] = make_float2(c, s);
     }
   }
   __syncthreads();
@@ -143,11 +161,12 @@ __global__ void __launch_bounds__(RP_THREADS) rope_append_kernel(const RopeArgs 
   const int steps = (TOK * per + RP_THREADS / L - 1) / (RP_THREADS / L);
   for (int s = 0; s < steps; ++s) {
     const int w = s * (RP_THREADS / L) + grp;
-    const int k = min(w / per, TOK - 1), r = r_lo + w % per, t = t0 + k;
+    static_assert(TOK <= 2, "w / per");
+    const int k = TOK == 2 && w >= per ? 1 : 0, r = r_lo + w - k * per, t = t0 + k;
     const bool is_q = r < a.q_heads, is_v = r >= a.q_heads + pg.kv_heads;
     const int h = is_q ? r : (is_v ? r - a.q_heads - pg.kv_heads : r - a.q_heads);
     const int b = seq_sh[k];
-    const bool live = w < TOK * per && b >= 0 && t < pg.T && (is_q || place_sh[k] >= 0);
+    const bool live = w < TOK * per && b >= 0 && (is_q || at_sh[k] >= 0);
     uint16_t* dst = nullptr;
     Chunk A = {}, Bc = {};
     if (live) {
@@ -157,11 +176,7 @@ __global__ void __launch_bounds__(RP_THREADS) rope_append_kernel(const RopeArgs 
       if (is_q) {
         dst = a.q_out + (int64_t)t * a.qo_stride + h * D;
       } else {
-        const int pl = place_sh[k], e = pl / pg.page_size;
-        const int page = paged_entry(pg, b, e);
-        if (page >= 0)
-          dst = (is_v ? pg.v : pg.k) + (int64_t)page * pg.page_stride + (int64_t)(pl - e * pg.page_size) * pg.token_stride +
-                (int64_t)h * pg.head_stride;
+        dst = (is_v ? pg.v : pg.k) + at_sh[k] + (int64_t)h * pg.head_stride;
       }
     }
     const uint16_t* gain = is_q ? a.q_norm : is_v ? nullptr : a.k_norm;
@@ -187,15 +202,19 @@ __global__ void __launch_bounds__(RP_THREADS) rope_append_kernel(const RopeArgs 
     }
     if (!dst) continue;
     if (!is_v) {
+      // two neighbouring pairs' cosines and sines a load
+      auto pairs2 = [&](int i) -> float4 { return *reinterpret_cast<const float4*>(&cs[k][cs_at<ADJ>(i)]); };
       if (ADJ) {
         auto turn = [&](Chunk& c, int ch) {
           if (8 * ch < a.rot) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 t2 = cs[k][4 * ch + i];
-              const float x = c.x[2 * i], y = c.x[2 * i + 1];
-              c.x[2 * i] = x * t2.x - y * t2.y;
-              c.x[2 * i + 1] = y * t2.x + x * t2.y;
+            for (int i = 0; i < 4; i += 2) {
+              const float4 u = pairs2(4 * ch + i);
+              const float x = c.x[2 * i], y = c.x[2 * i + 1], z = c.x[2 * i + 2], v = c.x[2 * i + 3];
+              c.x[2 * i] = x * u.x - y * u.y;
+              c.x[2 * i + 1] = y * u.x + x * u.y;
+              c.x[2 * i + 2] = z * u.z - v * u.w;
+              c.x[2 * i + 3] = v * u.z + z * u.w;
             }
           }
         };
@@ -203,11 +222,13 @@ __global__ void __launch_bounds__(RP_THREADS) rope_append_kernel(const RopeArgs 
         if (cb >= 0) turn(Bc, cb);
       } else if (lane < pairs) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 t2 = cs[k][8 * lane + i];
-          const float x = A.x[i], y = Bc.x[i];
-          A.x[i] = x * t2.x - y * t2.y;
-          Bc.x[i] = y * t2.x + x * t2.y;
+        for (int i = 0; i < 8; i += 2) {
+          const float4 u = pairs2(8 * lane + i);
+          const float x = A.x[i], y = Bc.x[i], z = A.x[i + 1], v = Bc.x[i + 1];
+          A.x[i] = x * u.x - y * u.y;
+          Bc.x[i] = y * u.x + x * u.y;
+          A.x[i + 1] = z * u.z - v * u.w;
+          Bc.x[i + 1] = v * u.z + z * u.w;
         }
       }
     }
@@ -221,9 +242,15 @@ mt_status rope_launch(const RopeArgs& a0, const Launch& l, int sms) {
   RopeArgs a = a0;
   const int rows = a.q_heads + 2 * a.pg.kv_heads, groups = RP_THREADS / L;
   const int T = a.pg.T;
+  // Two tokens a block (11 000 tokens: 61 us as it then was; one: 66, four: 62;
+  // 2900 tokens: 21, 21 and 26).  Where the blocks come to several rounds, 32
+  // registers a thread and 16 blocks an SM: 54 against 58 us for 11 000 tokens,
+  // 33 and 32 for 5800, 24 and 18 for 2900.
   if (T >= 8 * sms) {
     a.heads_per_block = rows;
-    return launch(rope_append_kernel<L, ADJ, 4>, dim3((T + 3) / 4), dim3(RP_THREADS), 0, l, a);
+    const dim3 grid((T + 1) / 2);
+    return T >= 48 * sms ? launch(rope_append_kernel<L, ADJ, 2, 16>, grid, dim3(RP_THREADS), 0, l, a)
+                         : launch(rope_append_kernel<L, ADJ, 2, 10>, grid, dim3(RP_THREADS), 0, l, a);
   }
   // few tokens: their heads over several blocks, one row per lane group, until
   // the blocks fill the GPU
@@ -231,7 +258,7 @@ mt_status rope_launch(const RopeArgs& a0, const Launch& l, int sms) {
   while (parts > 1 && (long)T * parts > 8L * sms) parts = (parts + 1) / 2;
   a.heads_per_block = (rows + parts - 1) / parts;
   parts = (rows + a.heads_per_block - 1) / a.heads_per_block;
-  return launch(rope_append_kernel<L, ADJ, 1>, dim3(T, parts), dim3(RP_THREADS), 0, l, a);
+  return launch(rope_append_kernel<L, ADJ, 1, 10>, dim3(T, parts), dim3(RP_THREADS), 0, l, a);
 }
 
 }  // namespace

@@ -145,6 +145,13 @@ def test_many_tokens(mt):
     case(mt, [(1, b % 50 + 1) for b in range(700)], 4, 2, 128, axes=2, seed=9)
 
 
+@pytest.mark.parametrize("adjacent,norm,order", [(False, True, "hnd"), (True, False, "kv")])
+def test_thousands_of_tokens(mt, adjacent, norm, order):
+    lens = [(700, 760), (0, 3), (1, 1), (233, 200), (379, 380)] + [(1, 17 + b) for b in range(40)]
+    case(mt, lens, 4, 2, 64, adjacent=adjacent, norm=norm, order=order, page=24, axes=3, seed=11)
+    case(mt, [(7900, 7900), (3, 9)], 3, 1, 32, adjacent=adjacent, norm=norm, order=order, page=24, axes=2, seed=12)
+
+
 def test_page_out_of_range_is_reported(mt):
     p = Paged([(3, 20)], 4, 2, 64, 16, seed=10)
     q, kc, vc, pages, q_start, kv_len = p.cuda()
