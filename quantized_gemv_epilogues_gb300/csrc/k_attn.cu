@@ -68,7 +68,9 @@ mt_status mt_paged_attention(const void* q, int64_t q_stride, int q_heads, const
   a.q_heads = q_heads;
   a.group = q_heads / Hk;
   a.scale_log2 = (float)((double)scale * 1.4426950408889634);
-  a.window = window;
+  // a window that no text here outgrows is none (and a position less it stays
+  // within 32 bits)
+  a.window = window < a.pg.max_kv ? window : 0;
   a.sinks = sinks;
   const Launch l{(cudaStream_t)stream, mt_get_option(MT_OPT_PDL) != 0};
   a.max_q = batch->max_q;

@@ -87,6 +87,15 @@ def test_window_and_sinks(mt, window, sinks, lens):
         compare(mt, Paged(lens, *heads, page=16, seed=5), window, sinks)
 
 
+@pytest.mark.parametrize("window", [512, 513, 2 ** 30, 2 ** 31 - 100, 2 ** 31 - 1])
+@pytest.mark.parametrize("lens", [[(1, 500), (1, 3)], [(200, 512), (9, 4), (1, 300)]], ids=["decode", "chunk"])
+def test_windows_wider_than_any_text(mt, window, lens):
+    # (9, 4): the first tokens' positions are negative; pages of 12 are not the chunk kernel's
+    for page in (16, 12):
+        for sinks in (0, 2 ** 31 - 1):
+            compare(mt, Paged(lens, 8, 2, 64, page=page, seed=24), window, sinks)
+
+
 @pytest.mark.parametrize("max_q", [1, 1000])
 def test_the_hint_changes_no_result(mt, max_q):
     compare(mt, Paged([(1, 130), (90, 401), (1, 1)], 8, 2, 64, page=16, seed=6), max_q=max_q)
