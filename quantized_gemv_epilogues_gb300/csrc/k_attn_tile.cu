@@ -215,7 +215,7 @@ constexpr int AT_PIECES = 4;
 // What follows the tiles in shared memory (all of it is dynamic, so that the
 // tiles start where it starts, on a 1024-byte boundary).
 struct AtShared {
-  uint64_t bars[2 * 10 + 6 + 4 + 2 + 2 * AT_PIECES + 2];
+  uint64_t bars[2 * 10 + 6 + 4 + 2 + 2 * AT_PIECES + 2 + AT_PIECES];
   uint32_t tmem;
   int abort;
   Piece piece[AT_PIECES];
@@ -241,13 +241,20 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   auto kv_free = [&](int i) { return smem_u32(&bars[NS + i]); };
   auto s_full = [&](int s) { return smem_u32(&bars[2 * NS + s]); };      // S of a block is in tensor memory
   auto p_full = [&](int s) { return smem_u32(&bars[2 * NS + 2 + s]); };  // P is (and O rescaled)
-  auto o_full = [&](int s) { return smem_u32(&bars[2 * NS + 4 + s]); };  // O of the piece is complete
+  // o_full(0): the first tile's O of the piece is complete; o_full(1): O of a
+  // block, in pieces with rows in the first tile only
+  auto o_full = [&](int s) { return smem_u32(&bars[2 * NS + 4 + s]); };
   auto p_half = [&](int s) { return smem_u32(&bars[2 * NS + 12 + 2 * AT_PIECES + s]); };  // P of the block's first 64 keys is
   auto q_full = [&](int s) { return smem_u32(&bars[2 * NS + 6 + s]); };
   auto q_free = [&](int s) { return smem_u32(&bars[2 * NS + 8 + s]); };
   const uint32_t tail_bar = smem_u32(&bars[2 * NS + 10]), mma_done = smem_u32(&bars[2 * NS + 11]);
   auto piece_full = [&](int k) { return smem_u32(&bars[2 * NS + 12 + k % AT_PIECES]); };
   auto piece_free = [&](int k) { return smem_u32(&bars[2 * NS + 12 + AT_PIECES + k % AT_PIECES]); };
+  // every product of the piece is complete: a barrier per place in the ring of
+  // pieces, which is not used again before every warp has left the piece, so
+  // that a warp that waits for it is never two phases behind (a parity would
+  // not tell it)
+  auto piece_done = [&](int k) { return smem_u32(&bars[2 * NS + 14 + 2 * AT_PIECES + k % AT_PIECES]); };
   auto q_tile = [&](int s) { return smem_u32(smem + (size_t)s * S::TILE); };
   auto stage = [&](int i) { return smem_u32(smem + S::OFF_KV + (size_t)i * S::TILE); };
 
@@ -267,6 +274,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     for (int k = 0; k < AT_PIECES; ++k) {
       mbar_init(piece_full(k), 1);
       mbar_init(piece_free(k), AT_SOFT + 3);  // one arrival per warp that reads it
+      mbar_init(piece_done(k), 1);
     }
     mbar_init(tail_bar, 1);
     mbar_init(mma_done, 1);
@@ -544,7 +552,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
               if (j >= n) continue;
               if (!pv(s, iv, s, j > 0)) return false;
               if (j + 1 == n) {
-                tc_commit(o_full(s));
+                if (s == 0) tc_commit(o_full(0));  // the second tile's last block is the piece's (n1 >= n0)
               } else {
                 if (!have_k && !wait1(kv_full(ik), ((st + 1) / NS) & 1)) return false;
                 have_k = true;
@@ -569,6 +577,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           const int n0 = p.n[0], n1 = p.n[1];
           mbar_arrive(piece_free(k));
           if ((n0 > 0 || n1 > 0) && !products(n0, n1)) break;
+          tc_commit(piece_done(k));
         }
         tc_commit(mma_done);  // completes when every MMA issued above has
       }
@@ -696,7 +705,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         if (!ok) break;
         // ---- the piece's rows
         if (n > 0) {
-          ok = wait(o_full(s), (s ? op1 : op0) & 1);
+          ok = s ? wait(piece_done(k), (k / AT_PIECES) & 1) : wait(o_full(0), op0 & 1);
           if (!ok) break;
           tc_fence_after();
         }
@@ -787,15 +796,15 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         // the reads of O above come before the next piece's products, which this tile's P allows
         tc_fence_before();
       }
-      // The second tile's warps keep to the first one's pieces: a parity only
-      // tells a phase from its neighbours, and theirs have passed here too.
-      // (The first tile's warps are kept by S of a piece's first block, which
-      // completes after everything before it.)
-      if (s == 1 && single && n_first > 0 && !wait(o_full(0), op0 & 1)) break;
+      // The second tile's warps keep to the first one's pieces, which may need
+      // nothing of them: the phases of s_full(1) that those use have passed when
+      // the piece is done.  (The first tile's warps are kept by S of a piece's
+      // first block, which completes after everything before it.)
+      if (s == 1 && !wait(piece_done(k), (k / AT_PIECES) & 1)) break;
       sp0 += single ? (n_first + 1) >> 1 : n_first;
       sp1 += single ? n_first >> 1 : n_second;
       op0 += n_first > 0;
-      op1 += single ? max(n_first - 1, 0) : 1;
+      op1 += single ? max(n_first - 1, 0) : 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(piece_free(k));
     }
