@@ -600,7 +600,8 @@ mt_status mt_paged_attention(const void* q, int64_t q_stride, int q_heads,
  *   allowed     : uint32 [B][allowed_ld], bit t % 32 of word t / 32 set if
  *                 token t is allowed; NULL: all are
  *   n_history, n_bias : entries of history and of bias_ids (ranges are
- *                 clamped to them)
+ *                 clamped to them; of a sequence's history the first 2^30 - 1
+ *                 tokens count)
  * Arithmetic is fp32 with one rounding to dtype; counts are integers, so that
  * results do not depend on the order of the history.
  * Limits: 0 <= B <= 65535 (0 does nothing), 1 <= V <= 2^24; arrays aligned to their elements;

@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(LT_THREADS) token_kernel(const LogitArgs a) {
   if (a.history) {
     h0 = min(max(__ldg(a.history_start + b), 0), a.n_history);
     h1 = min(max(__ldg(a.history_start + b + 1), h0), a.n_history);
+    if (h1 - h0 > (int)LG_TIMES) h1 = h0 + (int)LG_TIMES;  // a count stays within its bits
     hp = h0 + (a.prompt_len ? min(max(__ldg(a.prompt_len + b), 0), h1 - h0) : 0);  // the end of the prompt
   }
   if (a.bias_ids) {
@@ -200,36 +201,38 @@ __global__ void __launch_bounds__(LT_THREADS) token_kernel(const LogitArgs a) {
       n = __shfl_sync(0xffffffffu, n, 0);
       if (first) list[n + __popc(who & ((1u << (tid & 31)) - 1u))] = (uint16_t)at;
     };
-    for (int i0 = h0; i0 < h1; i0 += N * LT_THREADS) {
+    // indices past the end of a list of nearly 2^31 entries need the 32nd bit
+    for (uint32_t i0 = h0; i0 < (uint32_t)h1; i0 += N * LT_THREADS) {
       int id[N];
 #pragma unroll
       for (int q = 0; q < N; ++q) {
-        const int i = i0 + q * LT_THREADS + tid;
-        id[q] = i < h1 ? __ldg(a.history + i) : -1;
+        const uint32_t i = i0 + q * LT_THREADS + tid;
+        id[q] = i < (uint32_t)h1 ? __ldg(a.history + i) : -1;
       }
 #pragma unroll
       for (int q = 0; q < N; ++q) {
-        if (i0 + q * LT_THREADS >= h1) break;
+        if (i0 + q * LT_THREADS >= (uint32_t)h1) break;
         const int t = id[q];
         bool first = false;
         int at = 0;
         if (mine(t)) {
           at = place(t);
           // (a prompt's token is marked once: frequent ones would queue up at their word)
-          if (i0 + q * LT_THREADS + tid >= hp) first = atomicAdd(&word[at], 1u) == 0;
+          if (i0 + q * LT_THREADS + tid >= (uint32_t)hp) first = atomicAdd(&word[at], 1u) == 0;
           else if (!(*const_cast<volatile uint32_t*>(&word[at]) & LG_PROMPT)) first = atomicOr(&word[at], LG_PROMPT) == 0;
         }
         enlist(first, at);
       }
     }
-    for (int i0 = b0; i0 < b1; i0 += LT_THREADS) {
-      const int i = i0 + tid, t = i < b1 ? __ldg(a.bias_ids + i) : -1;
+    for (uint32_t i0 = b0; i0 < (uint32_t)b1; i0 += LT_THREADS) {
+      const uint32_t i = i0 + tid;
+      const int t = i < (uint32_t)b1 ? __ldg(a.bias_ids + i) : -1;
       bool first = false;
       int at = 0;
       if (mine(t)) {
         at = place(t);
         first = atomicOr(&word[at], LG_BIASED) == 0;
-        atomicMax(&slot[at], (uint32_t)(i - b0 + 1));
+        atomicMax(&slot[at], i - (uint32_t)b0 + 1u);
       }
       enlist(first, at);
     }
