@@ -67,6 +67,16 @@ class Model:
         self.inv_freq = (c.theta ** (-torch.arange(0, D, 2, dtype=torch.float64) / D)).float().to(device)
 
 
+def last_rows(new: list[list[int]]) -> list[int]:
+    """The row of the last new token of every text that has any."""
+    rows, at = [], 0
+    for n in new:
+        at += len(n)
+        if n:
+            rows.append(at - 1)
+    return rows
+
+
 class Runner:
     """The paged cache of up to ``len(texts)`` texts and the buffers of a step."""
 
@@ -117,8 +127,14 @@ class Runner:
 
     def step(self, new: list[list[int]]):
         """Takes each text's new tokens (none for a text that waits); returns
-        the fp32 logits after each text's last token, [texts, vocab]."""
+        the fp32 logits after the last token of every text that has new ones,
+        in their order, [those texts, vocab]."""
         c, m = self.m.cfg, self.m
+        if len(new) != self.texts or not any(new):
+            raise ValueError(f"new tokens of {self.texts} texts, at least one of them with some, are required")
+        for b, n in enumerate(new):
+            if self.lens[b] + len(n) > self.width * c.page:
+                raise ValueError(f"text {b}: the cache has room for {self.width * c.page} tokens")
         D, H, KV = c.head_dim, c.q_heads, c.kv_heads
         starts = [0]
         for n in new:
@@ -146,8 +162,8 @@ class Runner:
                                   sinks=c.sinks)
             residual, n = self._norm(self._linear(a.view(T, H * D), layer["o"]), residual, layer["n2"])
             x = self._mlp(n, residual, layer)
-        last = [s - 1 for s in starts[1:]]
-        _, n = self._norm(x[last], zero[:len(last)], m.norm)
+        last = last_rows(new)
+        _, n = self._norm(x[last], zero[last], m.norm)
         return self._linear(n, m.head, torch.float32)
 
 
@@ -188,6 +204,8 @@ def generate(model: Model, prompts: list[list[int]], tokens: int, repetition: fl
     """Greedy continuation of the prompts under a repetition penalty, without
     the token `banned`; returns the texts and each step's raw logits."""
     c, B = model.cfg, len(prompts)
+    if not all(prompts):
+        raise ValueError("a prompt needs at least one token")
     run = Runner(model, max(map(len, prompts)) + tokens, B)
     texts, new, raw = [list(p) for p in prompts], [list(p) for p in prompts], []
     words = torch.full((B, (c.vocab + 31) // 32), -1, dtype=torch.int32)
