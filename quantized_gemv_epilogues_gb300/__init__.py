@@ -38,6 +38,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmt.so")
@@ -114,10 +115,15 @@ class PagedBatch(ctypes.Structure):
                 ("max_pages", _I), ("max_q", _I)]
 
 
+# The two as the calls below pass them: bytes, as building the structures takes 1 us more
+_CACHE = struct.Struct("PPqqqiiii").pack
+_BATCH = struct.Struct("PPPqiiii").pack
+
+
 class MTError(RuntimeError):
-    def __init__(self, status: int, call: str):
+    def __init__(self, status: int, call: str, what: str | None = None):
         self.status = status
-        msg = _lib.mt_status_string(status).decode()
+        msg = what or _lib.mt_status_string(status).decode()
         if status == MT_ERR_CUDA:
             msg += f" (cudaError {_lib.mt_last_cuda_error()})"
         super().__init__(f"{call}: {msg}")
@@ -343,6 +349,15 @@ def mt_mlp_stack_run_noalloc(layers, d, f, group, fmt, eps, values, residual, ou
                                          _stream(stream)), "mt_mlp_stack_run_noalloc")
 
 
+def _on_device(call, **tensors):
+    """Refuses tensors whose memory a kernel cannot read: all but the GPU's and
+    pinned host memory (which has a device address of its own).  Called where
+    not all are the GPU's (asked for each by name: a loop over them takes 2 us)."""
+    for name, t in tensors.items():
+        if t is not None and not t.is_cuda and t.numel() and not t.is_pinned():
+            raise MTError(MT_ERR_NULL, call, f"{name}: a tensor on the GPU is required, this one is in host memory")
+
+
 def _typed(name, t, dtype, dim):
     if t.dtype is not dtype or t.dim() != dim:
         raise TypeError(f"{name}: a {dim}-dimensional {dtype} tensor is required, got {t.dim()}-dimensional {t.dtype}")
@@ -374,7 +389,7 @@ def _head_rows(name, t, dtype, shape):
 
 
 def _paged(k_cache, v_cache, pages, q_start, kv_len, T, max_q):
-    """The cache and batch arguments from tensors: caches [pages, page, heads, dim]
+    """The cache and batch arguments and the cache's heads and head size, from tensors: caches [pages, page, heads, dim]
     (any strides with contiguous dim, the same for both), pages int32 [B, n],
     q_start int32 [B + 1], kv_len int32 [B]."""
     bf, i32 = _torch.bfloat16, _torch.int32
@@ -393,10 +408,10 @@ def _paged(k_cache, v_cache, pages, q_start, kv_len, T, max_q):
     ld, one = pages.stride()
     if one != 1 and width > 1:
         raise ValueError("pages: the last dimension must be contiguous")
-    cache = PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1], st[2], n, page, heads, dim)
-    batch = PagedBatch(_flat("q_start", q_start, i32, B + 1), _flat("kv_len", kv_len, i32, B), pages.data_ptr(),
-                       ld if B > 1 else width, B, T, width, max_q)
-    return cache, batch
+    cache = _CACHE(k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1], st[2], n, page, heads, dim)
+    batch = _BATCH(_flat("q_start", q_start, i32, B + 1), _flat("kv_len", kv_len, i32, B), pages.data_ptr(),
+                   ld if B > 1 else width, B, T, width, max_q if 0 < max_q < 1 << 31 else 1)
+    return cache, batch, heads, dim
 
 
 def mt_rope_append(q, k, v, positions, inv_freq, q_out, k_cache, v_cache, pages, q_start, kv_len, axis=None,
@@ -411,10 +426,10 @@ def mt_rope_append(q, k, v, positions, inv_freq, q_out, k_cache, v_cache, pages,
     if len(shape) != 3:
         raise TypeError("q: a 3-dimensional tensor is required")
     T, H, D = shape
-    cache, batch = _paged(k_cache, v_cache, pages, q_start, kv_len, T, 1)
-    if D != cache.head_dim:
-        raise ValueError(f"the cache's head size is {cache.head_dim}, q's is {D}")
-    kv_shape = (T, cache.kv_heads, D)
+    cache, batch, kv_heads, dim = _paged(k_cache, v_cache, pages, q_start, kv_len, T, 1)
+    if D != dim:
+        raise ValueError(f"the cache's head size is {dim}, q's is {D}")
+    kv_shape = (T, kv_heads, D)
     qp, qs = _head_rows("q", q, bf, shape)
     kp, ks = _head_rows("k", k, bf, kv_shape)
     vp, vs = _head_rows("v", v, bf, kv_shape)
@@ -428,10 +443,15 @@ def mt_rope_append(q, k, v, positions, inv_freq, q_out, k_cache, v_cache, pages,
         _typed("positions", positions, torch.int32, positions.dim())
         raise ValueError(f"positions: contiguous rows of {T} tokens are required")
     half = inv_freq.numel()
+    if not (q.is_cuda and k.is_cuda and v.is_cuda and positions.is_cuda and inv_freq.is_cuda and q_out.is_cuda and k_cache.is_cuda
+            and v_cache.is_cuda and pages.is_cuda and q_start.is_cuda and kv_len.is_cuda and (axis is None or axis.is_cuda)
+            and (q_norm is None or q_norm.is_cuda) and (k_norm is None or k_norm.is_cuda)):
+        _on_device("mt_rope_append", q=q, k=k, v=v, positions=positions, inv_freq=inv_freq, q_out=q_out, k_cache=k_cache,
+                   v_cache=v_cache, pages=pages, q_start=q_start, kv_len=kv_len, axis=axis, q_norm=q_norm, k_norm=k_norm)
     _check(_lib.mt_rope_append(qp, qs, kp, ks, vp, vs, H, _flat("q_norm", q_norm, bf, D), _flat("k_norm", k_norm, bf, D), eps,
                                positions.data_ptr(), axes, _flat("inv_freq", inv_freq, torch.float32),
                                _flat("axis", axis, torch.uint8, half), 2 * half, pairing, op, os_,
-                               ctypes.byref(cache), ctypes.byref(batch), _stream(stream)), "mt_rope_append")
+                               cache, batch, _stream(stream)), "mt_rope_append")
 
 
 def mt_paged_attention_workspace_bytes(T, B, q_heads, kv_heads, head_dim) -> int:
@@ -448,9 +468,9 @@ def mt_paged_attention(q, k_cache, v_cache, pages, q_start, kv_len, max_q, scale
     if len(shape) != 3:
         raise TypeError("q: a 3-dimensional tensor is required")
     T, H, D = shape
-    cache, batch = _paged(k_cache, v_cache, pages, q_start, kv_len, T, max_q)
-    if D != cache.head_dim:
-        raise ValueError(f"the cache's head size is {cache.head_dim}, q's is {D}")
+    cache, batch, _, dim = _paged(k_cache, v_cache, pages, q_start, kv_len, T, max_q)
+    if D != dim:
+        raise ValueError(f"the cache's head size is {dim}, q's is {D}")
     qp, qs = _head_rows("q", q, torch.bfloat16, shape)
     f32 = out.dtype is torch.float32
     op, os_ = _head_rows("out", out, torch.float32 if f32 else torch.bfloat16, shape)
@@ -460,7 +480,11 @@ def mt_paged_attention(q, k_cache, v_cache, pages, q_start, kv_len, max_q, scale
             _typed("lse", lse, torch.float32, 2)
             raise ValueError(f"lse: a contiguous tensor of shape {(T, H)} is required")
         lp = lse.data_ptr()
-    _check(_lib.mt_paged_attention(qp, qs, H, ctypes.byref(cache), ctypes.byref(batch), scale, window, sinks, op, os_,
+    if not (q.is_cuda and k_cache.is_cuda and v_cache.is_cuda and pages.is_cuda and q_start.is_cuda and kv_len.is_cuda and out.is_cuda
+            and workspace.is_cuda and (lse is None or lse.is_cuda)):
+        _on_device("mt_paged_attention", q=q, k_cache=k_cache, v_cache=v_cache, pages=pages, q_start=q_start, kv_len=kv_len, out=out,
+                   workspace=workspace, lse=lse)
+    _check(_lib.mt_paged_attention(qp, qs, H, cache, batch, scale, window, sinks, op, os_,
                                    MT_F32 if f32 else MT_BF16, lp, workspace.data_ptr(), workspace.nbytes,
                                    _stream(stream)), "mt_paged_attention")
 
@@ -509,6 +533,15 @@ def mt_logit_penalties(logits, out, history=None, history_start=None, prompt_len
         ap = allowed.data_ptr()
         if B == 1:
             ald = words
+    if not (logits.is_cuda and out.is_cuda and (hist is None or history.is_cuda) and (start is None or history_start.is_cuda)
+            and (prompt is None or prompt_len.is_cuda) and (repetition is None or repetition.is_cuda)
+            and (presence is None or presence.is_cuda) and (frequency is None or frequency.is_cuda)
+            and (ids is None or bias_ids.is_cuda) and (values is None or bias_values.is_cuda)
+            and (bstart is None or bias_start.is_cuda)
+            and (allowed is None or allowed.is_cuda)):
+        _on_device("mt_logit_penalties", logits=logits, out=out, history=history, history_start=history_start,
+                   prompt_len=prompt_len, repetition=repetition, presence=presence, frequency=frequency, bias_ids=bias_ids,
+                   bias_values=bias_values, bias_start=bias_start, allowed=allowed)
     _check(_lib.mt_logit_penalties(logits.data_ptr(), ld, out.data_ptr(), out_ld, MT_F32 if dt is f32 else MT_BF16, B, V,
                                    hist, start, prompt, n_hist, _flat("repetition", repetition, f32, B),
                                    _flat("presence", presence, f32, B), _flat("frequency", frequency, f32, B), ids, values,
