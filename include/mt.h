@@ -528,6 +528,9 @@ typedef enum mt_rope_pairing {
  * cosine, so that it is as exact at position 2^30 as at 1 (an fp32 product
  * would be off by 2^-24 of the angle, whole turns at long positions);
  * everything else is fp32, with one rounding to bf16.
+ * The cache's rows may not share elements: of its strides, each must span all
+ * that the smaller ones reach (MT_ERR_SHAPE), and no row of V may lie in one of
+ * K (MT_ERR_ALIAS).
  * Limits: 1 <= n_axes <= 8; 1 <= q_heads <= 1024; 1 <= kv_heads <= 1024;
  *         strides multiples of 8; pointers 16-byte aligned (positions,
  *         inv_freq 4, axis 1).

@@ -51,6 +51,11 @@ __device__ __forceinline__ int paged_entry(const PagedArgs& a, int b, int i) {
 // ---- host side (k_paged.cu)
 // Checks of the cache and batch arguments; fills `a` (without the error word).
 mt_status paged_args(const mt_paged_cache* c, const mt_paged_batch* b, PagedArgs* a);
+// Whether no two (page, token, head) rows of K (or of V) share an element, for
+// checked arguments: each stride spans the dimensions of smaller strides.
+bool paged_rows_apart(const mt_paged_cache* c);
+// Whether no row of K shares an element with one of V; rows apart only.
+bool paged_kv_apart(const mt_paged_cache* c);
 // Bytes from a cache pointer to the end of its last element.
 size_t paged_cache_bytes(const mt_paged_cache* c);
 

@@ -287,6 +287,9 @@ extern "C" mt_status mt_rope_append(const void* q, int64_t q_stride, const void*
   for (const void* p : al)
     if (!aligned_to(p, 16)) return MT_ERR_ALIGN;
   if (!aligned_to(positions, 4) || !aligned_to(inv_freq, 4)) return MT_ERR_ALIGN;
+  // tokens are written by blocks that run at the same time
+  if (!paged_rows_apart(cache)) return MT_ERR_SHAPE;
+  if (!paged_kv_apart(cache)) return MT_ERR_ALIAS;
   const ByteRange iq = byte_range(q, rows_bytes(T, q_stride, (int64_t)q_heads * D, 2));
   const ByteRange oq = byte_range(q_out, rows_bytes(T, q_out_stride, (int64_t)q_heads * D, 2));
   const ByteRange ik = byte_range(k, rows_bytes(T, k_stride, (int64_t)Hk * D, 2));
