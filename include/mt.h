@@ -519,7 +519,8 @@ typedef enum mt_rope_pairing {
  *   rot      : elements of a head that turn, a multiple of 16, 0 < rot <=
  *              head_dim; the others pass through
  *   q_out    : bf16 [T][q_heads][head_dim], rows q_out_stride apart; may be q
- *              itself (the same address and stride)
+ *              itself (the same address and stride; k and v may then be other
+ *              columns of the same rows)
  * Row t of sequence b goes to the cache position of its token; a token whose
  * position is not in the cache (kv_len - n + i < 0, or a page out of range)
  * is not written.  Rows that belong to no sequence are neither read nor

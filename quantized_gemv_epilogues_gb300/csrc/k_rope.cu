@@ -298,7 +298,14 @@ extern "C" mt_status mt_rope_append(const void* q, int64_t q_stride, const void*
   const bool in_place = q_out == q && q_out_stride == q_stride;
   if (!in_place && ranges_overlap(oq, iq)) return MT_ERR_ALIAS;
   // in place, k and v may be other columns of the same rows
-  if (!in_place && (ranges_overlap(oq, ik) || ranges_overlap(oq, iv))) return MT_ERR_ALIAS;
+  const auto beside = [&](const void* p, int64_t stride) {
+    if (T < 2 || stride % q_stride) return false;
+    int64_t col = ((int64_t)(uintptr_t)p - (int64_t)(uintptr_t)q) / 2 % q_stride;
+    if (col < 0) col += q_stride;
+    return col >= (int64_t)q_heads * D && col + (int64_t)Hk * D <= q_stride;
+  };
+  if (ranges_overlap(oq, ik) && !(in_place && beside(k, k_stride))) return MT_ERR_ALIAS;
+  if (ranges_overlap(oq, iv) && !(in_place && beside(v, v_stride))) return MT_ERR_ALIAS;
   const ByteRange others[] = {byte_range(positions, (size_t)n_axes * T * 4), byte_range(inv_freq, (size_t)rot * 2),
                               byte_range(axis, rot / 2), byte_range(q_norm, D * 2), byte_range(k_norm, D * 2),
                               byte_range(batch->q_start, (size_t)(batch->B + 1) * 4), byte_range(batch->kv_len, (size_t)batch->B * 4),
