@@ -625,7 +625,7 @@ int mt_get_option(mt_option opt);
 
 /* Device error word: MT_ERR_TIMEOUT if a kernel's bounded wait expired, or
  * MT_ERR_PAGE if a kernel met a page out of range, since the word was last
- * cleared, 0 otherwise, -1 if it cannot be read.  Reading it
+ * cleared (a timeout where there were both), 0 otherwise, -1 if it cannot be read.  Reading it
  * synchronises with the device (cudaMemcpyFromSymbol); clear != 0 resets it. */
 int mt_device_error(int clear);
 

@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             const int x = e - e0 < 32 ? p_here : p_there;
             row = k0 - e * a.pg.page_size;
             if ((unsigned)x < (unsigned)a.pg.num_pages) page = x;
-            else atomicExch(a.pg.err, (int)MT_ERR_PAGE);
+            else page_error(a.pg);
           }
           const int q = st % NS;
           if (st >= NS) ok = wait(kv_free(q), ((st / NS) + 1) & 1);

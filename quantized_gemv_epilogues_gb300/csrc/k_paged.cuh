@@ -39,12 +39,16 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedArgs& a, int b) {
   return PagedSeq{s, e - s, min(max(__ldg(a.kv_len + b), 0), a.max_kv)};
 }
 
+// Records a page out of range, unless the word already holds an error: a
+// timeout stays until it is cleared.
+__device__ __forceinline__ void page_error(const PagedArgs& a) { atomicCAS(a.err, 0, (int)MT_ERR_PAGE); }
+
 // Page index of entry i of sequence b, or -1 (with the error word set) if it
 // is out of range.  i < max_pages.
 __device__ __forceinline__ int paged_entry(const PagedArgs& a, int b, int i) {
   const int p = __ldg(a.pages + (int64_t)b * a.pages_ld + i);
   if ((unsigned)p < (unsigned)a.num_pages) return p;
-  atomicExch(a.err, (int)MT_ERR_PAGE);
+  page_error(a);
   return -1;
 }
 
