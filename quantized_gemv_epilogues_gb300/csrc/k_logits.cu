@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(LT_THREADS) token_kernel(const LogitArgs a) {
     b0 = min(max(__ldg(a.bias_start + b), 0), a.n_bias);
     b1 = min(max(__ldg(a.bias_start + b + 1), b0), a.n_bias);
   }
-  const float rep = a.repetition ? __ldg(a.repetition + b) : 1.f, rep_inv = 1.f / rep;
+  const float rep = a.repetition ? __ldg(a.repetition + b) : 1.f;
   const float freq = a.frequency ? __ldg(a.frequency + b) : 0.f, pres = a.presence ? __ldg(a.presence + b) : 0.f;
   const char* in = a.in + (int64_t)b * a.in_ld * ES;
   char* out = a.out + (int64_t)b * a.out_ld * ES;
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(LT_THREADS) token_kernel(const LogitArgs a) {
       for (int q = 0; q < M; ++q) {
         float y = x[q];
         if (w[q] & LG_BIASED) y += add[q];
-        if (w[q] & (LG_PROMPT | LG_TIMES)) y *= y > 0.f ? rep_inv : rep;
+        if (w[q] & (LG_PROMPT | LG_TIMES)) y = y > 0.f ? __fdiv_rn(y, rep) : y * rep;
         if (w[q] & LG_TIMES) y = y - freq * (float)(w[q] & LG_TIMES) - pres;
         if (!((m[q] >> (t[q] & 31)) & 1u)) y = -INFINITY;
         if (i0 + q * LT_THREADS < n) logit_put<F32>(out, t[q], y);
