@@ -2,7 +2,7 @@
 // allowed-token masks in one pass over the vocabulary's logits.
 //
 //   x = logit + bias;  seen: x > 0 ? x / r : x * r;
-//   generated n > 0 times: x - f n - p;  not allowed: -inf
+//   generated n > 0 times: x - (f n + p);  not allowed: -inf
 //
 // Bound: memory, each logit read and written once (and one mask bit); a
 // sequence's history touches a few thousand of its 10^5 logits.  Two kernels:
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(LT_THREADS) token_kernel(const LogitArgs a) {
         float y = x[q];
         if (w[q] & LG_BIASED) y += add[q];
         if (w[q] & (LG_PROMPT | LG_TIMES)) y = y > 0.f ? __fdiv_rn(y, rep) : y * rep;
-        if (w[q] & LG_TIMES) y = y - freq * (float)(w[q] & LG_TIMES) - pres;
+        if (w[q] & LG_TIMES) y -= fmaf(freq, (float)(w[q] & LG_TIMES), pres);
         if (!((m[q] >> (t[q] & 31)) & 1u)) y = -INFINITY;
         if (i0 + q * LT_THREADS < n) logit_put<F32>(out, t[q], y);
       }

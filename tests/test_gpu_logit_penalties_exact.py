@@ -37,3 +37,13 @@ def test_repetition_is_a_quotient(mt, dtype):  # noqa: F811
     y = x.float()
     want = torch.where(y > 0, y / r, y * r).to(dtype)
     assert same(got, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_frequency_and_presence_are_added_first(mt, dtype):  # noqa: F811
+    # terms that cancel, beside which the logit would be lost; and one that is not finite
+    x = (torch.randn(4, 777, generator=torch.Generator().manual_seed(2)) * 4).to(dtype)
+    freq, pres = [2.0 ** 100, -(2.0 ** 60), 0.5, math.inf], [-(2.0 ** 100), 2.0 ** 60, 0.25, 1.0]
+    got = call(mt, x, torch.empty_like(x, device="cuda"), frequency=freq, presence=pres)
+    want = x.float() - torch.tensor([0.0, 0.0, 0.75, math.inf])[:, None]
+    assert same(got, want.to(dtype))
