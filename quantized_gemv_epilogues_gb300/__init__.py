@@ -480,6 +480,11 @@ def mt_paged_attention(q, k_cache, v_cache, pages, q_start, kv_len, max_q, scale
             _typed("lse", lse, torch.float32, 2)
             raise ValueError(f"lse: a contiguous tensor of shape {(T, H)} is required")
         lp = lse.data_ptr()
+    # a C int would take the lower 32 bits of what is wider than any text
+    if not -1 < window < 1 << 31:
+        window = -1 if window < 0 else 0x7FFFFFFF
+    if not -1 < sinks < 1 << 31:
+        sinks = -1 if sinks < 0 else 0x7FFFFFFF
     if not (q.is_cuda and k_cache.is_cuda and v_cache.is_cuda and pages.is_cuda and q_start.is_cuda and kv_len.is_cuda and out.is_cuda
             and workspace.is_cuda and (lse is None or lse.is_cuda)):
         _on_device("mt_paged_attention", q=q, k_cache=k_cache, v_cache=v_cache, pages=pages, q_start=q_start, kv_len=kv_len, out=out,
@@ -533,6 +538,8 @@ def mt_logit_penalties(logits, out, history=None, history_start=None, prompt_len
         ap = allowed.data_ptr()
         if B == 1:
             ald = words
+    if (B | V | n_hist | n_bias) >> 31:
+        raise ValueError("logits and lists of fewer than 2^31 rows, tokens and entries are required")
     if not (logits.is_cuda and out.is_cuda and (hist is None or history.is_cuda) and (start is None or history_start.is_cuda)
             and (prompt is None or prompt_len.is_cuda) and (repetition is None or repetition.is_cuda)
             and (presence is None or presence.is_cuda) and (frequency is None or frequency.is_cuda)
