@@ -480,6 +480,8 @@ def mt_paged_attention(q, k_cache, v_cache, pages, q_start, kv_len, max_q, scale
             _typed("lse", lse, torch.float32, 2)
             raise ValueError(f"lse: a contiguous tensor of shape {(T, H)} is required")
         lp = lse.data_ptr()
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor is required")
     # a C int would take the lower 32 bits of what is wider than any text
     if not -1 < window < 1 << 31:
         window = -1 if window < 0 else 0x7FFFFFFF

@@ -75,3 +75,11 @@ def test_lists_without_their_starts_are_refused_as_before(mt):
         with pytest.raises(mt.MTError) as e:
             mt.mt_logit_penalties(x, torch.zeros(1, 50), **kw, stream=0)
         assert e.value.status == mt.MT_ERR_NULL
+
+
+def test_a_workspace_of_repeated_elements(mt):
+    # nbytes counts an expanded tensor's one element as often as it is repeated
+    kw = calls(mt, "cpu")["mt_paged_attention"]
+    kw["workspace"] = torch.zeros(1, dtype=torch.uint8).expand(kw["workspace"].numel())
+    with pytest.raises(ValueError, match="contiguous"):
+        mt.mt_paged_attention(**kw, stream=0)
