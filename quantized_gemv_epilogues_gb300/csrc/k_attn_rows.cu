@@ -1,16 +1,19 @@
-// k_attn_rows.cu - attention over a paged cache for few rows: decode steps
-// (one or a few new tokens a sequence), and every layout that the kernel for
-// long chunks does not take.
+// k_attn_rows.cu - attention over a paged cache for the layouts that the chunk
+// kernel (k_attn_tile.cu) does not take: fp32 outputs, head sizes below 64 or
+// above 128, pages that are no multiple of 8 tokens.
 //
-// Bound: memory.  A key and its value (4 D bytes) are read once for all query
-// heads that share them, so at 16 rows a tile a CTA does 16 * 4 D flops for
-// 4 D bytes.  The products run on mma.sync m16n8k16 (16 rows is its whole M;
-// a tcgen05 tile would be 128 rows of which 1 to 16 are there), each of the
+// Bound: memory for single tokens.  A key and its value (4 D bytes) are read
+// once for 16 rows, so a CTA does 16 * 4 D flops for 4 D bytes: 48 ragged texts
+// of 32 / 8 heads of 128, 209 us (5.2 TB/s) where the chunk kernel takes 176.
+// Prompts read the keys again for every 16 rows and are bound by mma.sync: one
+// of 3000 tokens 1029 us, 78 in the chunk kernel.  The products run on
+// mma.sync m16n8k16 (16 rows is its whole M, and rows of any head size and
+// pages of any length reach its fragments), each of the
 // four warps over its own 16 of a block's 64 keys with its own running
 // maximum and sum, joined through shared memory at the tile's end.  K and V
 // blocks come by 16-byte cp.async into a ring of ST stages, which runs on
 // across tiles; page indices are fetched a block ahead of the copies that
-// need them.  P enters the second product as bf16 hi + lo (2^-16 of each
+// need them.  (Head size 256: 255 registers and 84 bytes of spills.)  P enters the second product as bf16 hi + lo (2^-16 of each
 // weight; the tensor pipe has the time).
 #include <math.h>
 

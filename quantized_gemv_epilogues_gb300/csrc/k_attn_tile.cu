@@ -883,6 +883,13 @@ mt_status run_tile(AttnArgs a, void* ws, const Launch& l, const DeviceInfo* di) 
 
 }  // namespace
 
+// This kernel takes every layout that it can, single tokens too: against
+// k_attn_rows.cu 176 and 209 us for 48 ragged texts of 32 / 8 heads of 128, 27
+// and 37 for 2 of 100 000 with 14 / 2 of 64, 28 and 30 for 8 of 2000 with 16 / 16
+// of 128, 12.3 and 12.2 for one of 777, 17 and 36 for a prompt of 300, 77 and 449
+// for a chunk beside single tokens.  It cannot take fp32 outputs (weights of one
+// bf16), head sizes below 64 or above 128 (its tensor memory's columns), and
+// pages that are no multiple of 8 tokens (a box is whole 8-row swizzle atoms).
 bool attn_tile_takes(const AttnArgs& a) {
   return !a.out_f32 && a.pg.head_dim >= 64 && a.pg.head_dim <= 128 && at_box(a.pg.page_size) >= 8;
 }

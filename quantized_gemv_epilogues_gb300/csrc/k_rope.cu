@@ -254,8 +254,8 @@ mt_status rope_launch(const RopeArgs& a0, const Launch& l, int sms) {
   const int T = a.pg.T;
   // Two tokens a block (11 000 tokens: 61 us as it then was; one: 66, four: 62;
   // 2900 tokens: 21, 21 and 26).  Where the blocks come to several rounds, 32
-  // registers a thread and 16 blocks an SM: 54 against 58 us for 11 000 tokens,
-  // 33 and 32 for 5800, 24 and 18 for 2900.
+  // registers a thread (20 to 24 bytes of them spilled) and 16 blocks an SM: 54
+  // against 58 us for 11 000 tokens, 33 and 32 for 5800, 24 and 18 for 2900.
   if (T >= 8 * sms) {
     a.heads_per_block = rows;
     const dim3 grid((T + 1) / 2);
