@@ -41,6 +41,20 @@
  *   mt_logit_penalties  biases, penalties for repeated tokens and
  *                     allowed-token masks on the vocabulary's logits
  *
+ * and, where a small model drafts a tree of tokens that the large one takes in
+ * one pass:
+ *
+ *   mt_tree_layout    positions and visibility bits of a tree's tokens from
+ *                     their parents
+ *   mt_tree_attention attention of the tree's tokens over the paged cache and
+ *                     over the new tokens that each one's bits name
+ *   mt_token_probs    probabilities of logits under a temperature
+ *   mt_tree_verify    drafted tokens accepted against the target's
+ *                     probabilities from given random numbers, and the token
+ *                     after them
+ *   mt_cache_keep     the accepted tokens' keys and values moved together in
+ *                     every layer's cache
+ *
  * plus the offline packer mt_pack_affine (affine group quantisation of fp32
  * weights into the stored layout), and the warmed executor mt_mlp_plan_*
  * that runs L such layers back to back as one persistent kernel.
@@ -618,6 +632,150 @@ mt_status mt_logit_penalties(const void* logits, int64_t logits_ld, void* out, i
                              const float* frequency, const int32_t* bias_ids,
                              const float* bias_values, const int32_t* bias_start, int n_bias,
                              const uint32_t* allowed, int64_t allowed_ld, void* stream);
+
+/*
+ * ---- Drafted tokens
+ *
+ * A drafted tree is the new tokens of a sequence (mt_paged_batch), in an order
+ * in which every token follows its parent.  parent[t] is the index of t's
+ * parent among the sequence's new tokens; an index that is not an earlier
+ * token's (-1, by custom) means none: such a token follows the last one before
+ * the new ones.  A chain, parent[i] = i - 1, is an ordinary chunk.  The tree's
+ * tokens are written to the cache like any others (mt_rope_append, with the
+ * positions below): token i at kv_len - n + i.
+ *
+ * Visibility bits are rows of `words` 32-bit words, visible_ld words apart: bit
+ * j % 32 of word j / 32 of token i's row stands for the sequence's new token j.
+ * Bits of j >= n count as not set, and new tokens from 32 * words on are seen by
+ * none.
+ */
+#define MT_TREE_WORDS 32 /* the most words of a row: trees of up to 1024 tokens */
+
+/*
+ * Positions and visibility bits of the new tokens from their parents:
+ *   positions[t] = kv_len - n + (number of t's ancestors)
+ *   visible      : bits of the token itself and of its ancestors
+ *   parent    : int32 [T]
+ *   q_start   : int32 [B + 1], kv_len: int32 [B], as in mt_paged_batch (kv_len
+ *               may be NULL: positions then start at 0)
+ *   positions : int32 [T], or NULL
+ *   visible   : uint32 [T][words], rows visible_ld words apart, or NULL
+ * Any number of tokens may be in a sequence; of `visible`, the bits of the first
+ * 32 * words are written.  Rows of T that belong to no sequence are not written.
+ * Limits: 1 <= B <= 1024; 0 <= T <= 2^22 (0 does nothing); 1 <= words <= 32
+ *         and visible_ld >= words where visible is given; pointers 4-byte
+ *         aligned.
+ */
+mt_status mt_tree_layout(const int32_t* parent, const int32_t* q_start, const int32_t* kv_len, int B, int T,
+                         int32_t* positions, uint32_t* visible, int64_t visible_ld, int words,
+                         void* stream);
+
+/*
+ * Attention of the new tokens over the paged cache, by visibility bits in place
+ * of the order of the new tokens.  With base = kv_len - n and s_i the number of
+ * bits set in token i's row (its position is base + max(s_i, 1) - 1), token i
+ * sees
+ *   key j < base      if window == 0 or j > position - window or j < sinks,
+ *   key base + j      if bit j of its row is set (itself among them),
+ * and out, lse are as in mt_paged_attention, whose other arguments, kernels,
+ * roundings, limits and workspace (mt_paged_attention_workspace_bytes) these
+ * are.
+ *   visible   : uint32 [T][words], rows visible_ld words apart
+ * Page-table entries of a sequence are followed for its first `sinks` tokens and
+ * from key base - window + 1 on.  New tokens that none of a tile's tokens sees
+ * do not reach its output, NaN or not.
+ * Limits: as mt_paged_attention; 1 <= words <= 32; visible_ld >= words; visible
+ *         4-byte aligned.
+ */
+mt_status mt_tree_attention(const void* q, int64_t q_stride, int q_heads, const mt_paged_cache* cache,
+                            const mt_paged_batch* batch, const uint32_t* visible, int64_t visible_ld,
+                            int words, float scale, int window, int sinks, void* out, int64_t out_stride,
+                            mt_dtype out_dtype, float* lse, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/*
+ * Probabilities of the tokens of R rows of logits under each row's temperature:
+ *   p = exp((x - max x) / temperature) / sum exp((x - max x) / temperature)
+ * A temperature that is not above 0 gives 1 at the largest logit (the first of
+ * equal ones) and 0 elsewhere; one above 2^100 shares alike among the logits
+ * above -inf; one below 2^-100 counts as that.  A logit of -inf has probability
+ * 0, and so have all of a row that holds nothing else.  A row with a NaN or +inf
+ * is NaN throughout.
+ *   logits      : [R][V] of dtype, rows logits_ld elements apart
+ *   temperature : float [R], or NULL (1)
+ *   probs       : float [R][V], rows probs_ld elements apart; may be logits
+ *                 (fp32, the same address and stride)
+ * Arithmetic is fp32 (the exponent's argument to twice that), one rounding at
+ * the end.
+ * Limits: 0 <= R <= 2^22 (0 does nothing), 1 <= V <= 2^24; logits_ld, probs_ld
+ *         >= V; arrays aligned to their elements.
+ */
+mt_status mt_token_probs(const void* logits, int64_t logits_ld, mt_dtype dtype, int R, int V,
+                         const float* temperature, float* probs, int64_t probs_ld, void* stream);
+
+/*
+ * Verification of drafted tokens.  The first new token of a sequence is known
+ * (the last one drawn, or a prompt's last) and the others are a tree below it.
+ * Starting at the first, at a token whose target row is p and draft row q, the
+ * children are tried in the order of their indices with S = 0, R = 1:
+ *   with draft    : r(v) = max(p(v) - S q(v), 0); the child with token x is
+ *                   accepted if random * q(x) * R < r(x); if not, S += R and
+ *                   R = sum_v max(p(v) - S q(v), 0)
+ *   without draft : r = p; accepted if random * R < r(x); if not, R -= r(x),
+ *                   r(x) = 0 (children that are not drawn at random: the
+ *                   draft's most probable tokens, for instance)
+ * where random is the child's own number.  An accepted child is the next token
+ * whose children are tried; where none is, or where the path has `cols` tokens,
+ * the last token is drawn from r: the first v with r(0) + .. + r(v) > random_0 *
+ * sum r, random_0 being the first new token's number.  (From p where r is zero;
+ * -1 where p is, too.)  With numbers uniform on [0, 1), and children drawn
+ * independently from q or chosen beforehand, the tokens are distributed as if
+ * drawn from p one after another.
+ *   target     : float [T][V], rows target_ld apart: the target's probabilities
+ *                after each new token (mt_token_probs)
+ *   draft      : float [T][V], rows draft_ld apart: the distribution that each
+ *                token's children were drawn from, or NULL; rows of tokens
+ *                without children may hold anything
+ *   tokens, parent : int32 [T]; a token outside [0, V) is refused
+ *   random     : float [T], from [0, 1) (others are clamped to it, NaN to 0)
+ *   out_tokens : int32 [B][cols]: the accepted tokens, the drawn one, then -1
+ *   out_path   : int32 [B][cols]: the indices of the first new token and of the
+ *                accepted ones among the sequence's, then -1
+ *   out_count  : int32 [B]: tokens of the path, as many as out_tokens has; 0
+ *                for a sequence without new tokens
+ * Probabilities count in steps of 2^-56 (above 1 as 1, below 0 and NaN as 0),
+ * their sums and products are 64-bit integers: results are the same on every
+ * run, whatever the order.  Rows should sum to about 1 (at most 255).
+ * Limits: 1 <= B <= 1024; 0 <= T <= 2^22 (0 does nothing); 1 <= V <= 2^24;
+ *         1 <= cols <= 2^20; target_ld, draft_ld >= V; pointers 4-byte aligned.
+ */
+mt_status mt_tree_verify(const float* target, int64_t target_ld, const float* draft, int64_t draft_ld, int V,
+                         const int32_t* tokens, const int32_t* parent, const float* random,
+                         const int32_t* q_start, int B, int T, int32_t* out_tokens, int32_t* out_path,
+                         int32_t* out_count, int cols, void* stream);
+
+/*
+ * Moves the keys and values of the new tokens path[b][0 .. count[b]) of every
+ * sequence together, in each of L caches: the token at kv_len - n + path[b][i]
+ * goes to kv_len - n + i, and
+ *   new_len[b] = kv_len - n + (tokens kept)
+ * is the sequence's length from then on.  What lies behind stays as it was.
+ *   caches    : host array of L caches (read during the call) of the same
+ *               strides and sizes; no two share an element
+ *   batch     : q_start, kv_len, pages as in mt_paged_attention
+ *   path      : int32 [B][cols], each row increasing from an index >= 0 (as
+ *               mt_tree_verify writes it); a row ends at the first index that is
+ *               not above the one before it, or not below n
+ *   count     : int32 [B] (clamped to [0, cols])
+ *   new_len   : int32 [B], or NULL; may not be kv_len
+ * A token whose page is out of range, or whose position is not in the cache, is
+ * not moved.
+ * Limits: 1 <= L <= 1024; 1 <= cols <= 2^20; pointers 4-byte aligned; the
+ *         caches' rows may not share elements, as in mt_rope_append.
+ */
+mt_status mt_cache_keep(const mt_paged_cache* caches, int L, const mt_paged_batch* batch,
+                        const int32_t* path, const int32_t* count, int cols, int32_t* new_len,
+                        void* stream);
 
 /* Library options.  Returns MT_ERR_FORMAT for an unknown option. */
 mt_status mt_set_option(mt_option opt, int value);

@@ -24,6 +24,11 @@ Calls (same names as the C ABI):
   (workspace of :func:`mt_paged_attention_workspace_bytes` bytes).
 * :func:`mt_logit_penalties` -- biases, penalties for repeated tokens and
   allowed-token masks on logits.
+* :func:`mt_tree_layout`, :func:`mt_tree_attention`, :func:`mt_token_probs`,
+  :func:`mt_tree_verify`, :func:`mt_cache_keep` -- a tree of drafted tokens:
+  its positions and visibility bits, its attention over the pages, the target's
+  probabilities, the accepted path and the token after it, and that path's keys
+  and values moved together.
 * :func:`mt_pack_affine` / :func:`mt_unpack_affine` -- affine group packer.
 * :func:`mt_pack_mx` -- MXFP8 / MXFP4 block-scaled packer (E8M0 scales).
 * :func:`mt_mlp_plan_create` / :func:`mt_mlp_plan_run` / :func:`mt_mlp_plan_destroy`
@@ -84,6 +89,11 @@ _SIGS = {
     "mt_paged_attention_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I]),
     "mt_paged_attention": (_I, [_P, _L, _I, _P, _P, _F, _I, _I, _P, _L, _I, _P, _P, ctypes.c_size_t, _P]),
     "mt_logit_penalties": (_I, [_P, _L, _P, _L, _I, _I, _I, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _I, _P, _L, _P]),
+    "mt_tree_layout": (_I, [_P, _P, _P, _I, _I, _P, _P, _L, _I, _P]),
+    "mt_tree_attention": (_I, [_P, _L, _I, _P, _P, _P, _L, _I, _F, _I, _I, _P, _L, _I, _P, _P, ctypes.c_size_t, _P]),
+    "mt_token_probs": (_I, [_P, _L, _I, _I, _I, _P, _P, _L, _P]),
+    "mt_tree_verify": (_I, [_P, _L, _P, _L, _I, _P, _P, _P, _P, _I, _I, _P, _P, _P, _I, _P]),
+    "mt_cache_keep": (_I, [_P, _I, _P, _P, _P, _I, _P, _P]),
     "mt_mlp_stack_run_noalloc": (_I, [_P, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -463,6 +473,25 @@ def mt_paged_attention(q, k_cache, v_cache, pages, q_start, kv_len, max_q, scale
     """Attention of the new tokens q [T, q_heads, dim] over the paged cache;
     out [T, q_heads, dim] (bf16 or fp32), lse float [T, q_heads] or None,
     window 0 for none.  max_q: the most new tokens of a sequence (a hint)."""
+    _attention("mt_paged_attention", q, k_cache, v_cache, pages, q_start, kv_len, None, max_q, scale, out, workspace, lse, window,
+               sinks, stream)
+
+
+def _bit_rows(name, t, T):
+    """Address, row stride and words of int32 [T, words] rows of bits."""
+    i32 = _torch.int32
+    if t.dtype is not i32 or t.dim() != 2:
+        _typed(name, t, i32, 2)
+    rows, words = t.shape
+    ld, one = t.stride()
+    if rows != T or (words > 1 and one != 1):
+        raise ValueError(f"{name}: {T} contiguous rows are required")
+    if words >> 31:
+        raise ValueError(f"{name}: rows of fewer than 2^31 words are required")
+    return t.data_ptr(), (ld if T > 1 else words), words
+
+
+def _attention(call, q, k_cache, v_cache, pages, q_start, kv_len, visible, max_q, scale, out, workspace, lse, window, sinks, stream):
     torch = _torch or _get_torch()
     shape = q.shape
     if len(shape) != 3:
@@ -482,18 +511,151 @@ def mt_paged_attention(q, k_cache, v_cache, pages, q_start, kv_len, max_q, scale
         lp = lse.data_ptr()
     if not workspace.is_contiguous():
         raise ValueError("workspace: a contiguous tensor is required")
+    if visible is not None:
+        bp, bld, words = _bit_rows("visible", visible, T)
     # a C int would take the lower 32 bits of what is wider than any text
     if not -1 < window < 1 << 31:
         window = -1 if window < 0 else 0x7FFFFFFF
     if not -1 < sinks < 1 << 31:
         sinks = -1 if sinks < 0 else 0x7FFFFFFF
     if not (q.is_cuda and k_cache.is_cuda and v_cache.is_cuda and pages.is_cuda and q_start.is_cuda and kv_len.is_cuda and out.is_cuda
-            and workspace.is_cuda and (lse is None or lse.is_cuda)):
-        _on_device("mt_paged_attention", q=q, k_cache=k_cache, v_cache=v_cache, pages=pages, q_start=q_start, kv_len=kv_len, out=out,
+            and workspace.is_cuda and (lse is None or lse.is_cuda) and (visible is None or visible.is_cuda)):
+        _on_device(call, q=q, k_cache=k_cache, v_cache=v_cache, pages=pages, q_start=q_start, kv_len=kv_len, visible=visible, out=out,
                    workspace=workspace, lse=lse)
-    _check(_lib.mt_paged_attention(qp, qs, H, cache, batch, scale, window, sinks, op, os_,
-                                   MT_F32 if f32 else MT_BF16, lp, workspace.data_ptr(), workspace.nbytes,
-                                   _stream(stream)), "mt_paged_attention")
+    dt, wp, wb = MT_F32 if f32 else MT_BF16, workspace.data_ptr(), workspace.nbytes
+    if visible is None:
+        st = _lib.mt_paged_attention(qp, qs, H, cache, batch, scale, window, sinks, op, os_, dt, lp, wp, wb, _stream(stream))
+    else:
+        st = _lib.mt_tree_attention(qp, qs, H, cache, batch, bp, bld, words, scale, window, sinks, op, os_, dt, lp, wp, wb,
+                                    _stream(stream))
+    _check(st, call)
+
+
+def mt_tree_attention(q, k_cache, v_cache, pages, q_start, kv_len, visible, max_q, scale, out, workspace, lse=None, window=0,
+                      sinks=0, stream=None) -> None:
+    """:func:`mt_paged_attention` for drafted trees: of the sequence's new
+    tokens, a token sees those whose bits are set in its row of visible, int32
+    [T, words].  A window (0 for none) ends at the position that the number of
+    its bits gives."""
+    if visible is None:
+        raise TypeError("visible: rows of bits are required")
+    _attention("mt_tree_attention", q, k_cache, v_cache, pages, q_start, kv_len, visible, max_q, scale, out, workspace, lse, window,
+               sinks, stream)
+
+
+def mt_tree_layout(parent, q_start, kv_len=None, positions=None, visible=None, stream=None) -> None:
+    """Positions int32 [T] and visibility bits int32 [T, words] (either may be
+    None) of the new tokens from their parents, int32 [T]: indices within each
+    sequence, -1 for none.  kv_len int32 [B], or None (positions from 0)."""
+    torch = _torch or _get_torch()
+    i32 = torch.int32
+    if q_start.numel() < 2:
+        raise ValueError("q_start: B + 1 entries are required")
+    pp, T, B = _flat("parent", parent, i32), parent.numel(), q_start.numel() - 1
+    bp, bld, words = _bit_rows("visible", visible, T) if visible is not None else (None, 0, 0)
+    sp, kp, op = _flat("q_start", q_start, i32), _flat("kv_len", kv_len, i32, B), _flat("positions", positions, i32, T)
+    if (T | B) >> 31:
+        raise ValueError("fewer than 2^31 tokens and sequences are required")
+    if not (parent.is_cuda and q_start.is_cuda and (kv_len is None or kv_len.is_cuda) and (positions is None or positions.is_cuda)
+            and (visible is None or visible.is_cuda)):
+        _on_device("mt_tree_layout", parent=parent, q_start=q_start, kv_len=kv_len, positions=positions, visible=visible)
+    _check(_lib.mt_tree_layout(pp, sp, kp, B, T, op, bp, bld, words, _stream(stream)), "mt_tree_layout")
+
+
+def _rows_of(name, t, dtype, shape):
+    """Address and row stride of a [R, V] tensor with contiguous rows."""
+    if t.dtype is not dtype or t.dim() != 2:
+        _typed(name, t, dtype, 2)
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(shape)} is required, got {tuple(t.shape)}")
+    R, V = t.shape
+    ld, one = t.stride()
+    if V > 1 and one != 1:
+        raise ValueError(f"{name}: contiguous rows are required")
+    return t.data_ptr(), (ld if R > 1 else V)
+
+
+def mt_token_probs(logits, probs, temperature=None, stream=None) -> None:
+    """Probabilities probs float [R, V] of logits [R, V] (bf16 or fp32; fp32
+    ones may be probs) under temperature float [R] (None: 1; not above 0: the
+    most probable token alone)."""
+    torch = _torch or _get_torch()
+    f32 = torch.float32
+    wide = logits.dtype is f32
+    lp, ld = _rows_of("logits", logits, f32 if wide else torch.bfloat16, None)
+    R, V = logits.shape
+    pp, pld = _rows_of("probs", probs, f32, logits.shape)
+    hp = _flat("temperature", temperature, f32, R)
+    if (R | V) >> 31:
+        raise ValueError("fewer than 2^31 rows and tokens are required")
+    if not (logits.is_cuda and probs.is_cuda and (temperature is None or temperature.is_cuda)):
+        _on_device("mt_token_probs", logits=logits, probs=probs, temperature=temperature)
+    _check(_lib.mt_token_probs(lp, ld, MT_F32 if wide else MT_BF16, R, V, hp, pp, pld, _stream(stream)), "mt_token_probs")
+
+
+def mt_tree_verify(target, tokens, parent, random, q_start, out_tokens, out_path, out_count, draft=None, stream=None) -> None:
+    """The accepted path through each sequence's drafted tree and the token
+    after it: target float [T, V] probabilities after each new token, tokens
+    and parent int32 [T], random float [T] from [0, 1), draft float [T, V] the
+    distributions that the children were drawn from (None: chosen beforehand);
+    out_tokens and out_path int32 [B, cols], out_count int32 [B]."""
+    torch = _torch or _get_torch()
+    f32, i32 = torch.float32, torch.int32
+    tp, tld = _rows_of("target", target, f32, None)
+    T, V = target.shape
+    dp, dld = _rows_of("draft", draft, f32, target.shape) if draft is not None else (None, 0)
+    B = out_count.numel()
+    if out_tokens.dim() != 2:
+        _typed("out_tokens", out_tokens, i32, 2)
+    cols = out_tokens.shape[1]
+    for name, t in (("out_tokens", out_tokens), ("out_path", out_path)):
+        if t.dtype is not i32 or t.shape != (B, cols) or not t.is_contiguous():
+            _typed(name, t, i32, 2)
+            raise ValueError(f"{name}: a contiguous tensor of shape {(B, cols)} is required")
+    ids, up, rp = _flat("tokens", tokens, i32, T), _flat("parent", parent, i32, T), _flat("random", random, f32, T)
+    sp, cp = _flat("q_start", q_start, i32, B + 1), _flat("out_count", out_count, i32)
+    if (T | V | B | cols) >> 31:
+        raise ValueError("fewer than 2^31 rows, tokens, sequences and columns are required")
+    if not (target.is_cuda and tokens.is_cuda and parent.is_cuda and random.is_cuda and q_start.is_cuda and out_tokens.is_cuda
+            and out_path.is_cuda and out_count.is_cuda and (draft is None or draft.is_cuda)):
+        _on_device("mt_tree_verify", target=target, tokens=tokens, parent=parent, random=random, q_start=q_start,
+                   out_tokens=out_tokens, out_path=out_path, out_count=out_count, draft=draft)
+    _check(_lib.mt_tree_verify(tp, tld, dp, dld, V, ids, up, rp, sp, B, T, out_tokens.data_ptr(), out_path.data_ptr(), cp, cols,
+                               _stream(stream)), "mt_tree_verify")
+
+
+def mt_cache_keep(caches, pages, q_start, kv_len, path, count, new_len=None, stream=None) -> None:
+    """Moves the keys and values of the new tokens path[b][:count[b]] (int32 [B,
+    cols], int32 [B]) together in each of the caches, (k_cache, v_cache) pairs
+    of equal shapes and strides; new_len int32 [B] (or None) takes the
+    sequences' lengths with them."""
+    torch = _torch or _get_torch()
+    i32, bf = torch.int32, torch.bfloat16
+    if not caches:
+        raise ValueError("caches: at least one pair is required")
+    most = 1 << 22  # rows of the step: none is read here
+    cache, batch, _, _ = _paged(*caches[0], pages, q_start, kv_len, most, 1)
+    k0 = caches[0][0]
+    shape, st = k0.shape, k0.stride()
+    packed = [cache]
+    for k, v in caches[1:]:
+        if k.dtype is not bf or v.dtype is not bf or k.shape != shape or v.shape != shape or k.stride() != st or v.stride() != st:
+            raise ValueError("caches: bf16 tensors of equal shapes and strides are required")
+        packed.append(_CACHE(k.data_ptr(), v.data_ptr(), st[0], st[1], st[2], shape[0], shape[1], shape[2], shape[3]))
+    B = pages.shape[0]
+    if path.dtype is not i32 or path.dim() != 2 or path.shape[0] != B or not path.is_contiguous():
+        _typed("path", path, i32, 2)
+        raise ValueError(f"path: {B} contiguous rows are required")
+    cols = path.shape[1]
+    cp, np_ = _flat("count", count, i32, B), _flat("new_len", new_len, i32, B)
+    if cols >> 31:
+        raise ValueError("path: fewer than 2^31 columns are required")
+    if not (pages.is_cuda and q_start.is_cuda and kv_len.is_cuda and path.is_cuda and count.is_cuda
+            and (new_len is None or new_len.is_cuda) and all(k.is_cuda and v.is_cuda for k, v in caches)):
+        _on_device("mt_cache_keep", pages=pages, q_start=q_start, kv_len=kv_len, path=path, count=count, new_len=new_len)
+        for k, v in caches:
+            _on_device("mt_cache_keep", k_cache=k, v_cache=v)
+    _check(_lib.mt_cache_keep(b"".join(packed), len(packed), batch, path.data_ptr(), cp, cols, np_, _stream(stream)), "mt_cache_keep")
 
 
 def mt_logit_penalties(logits, out, history=None, history_start=None, prompt_len=None, repetition=None, presence=None,

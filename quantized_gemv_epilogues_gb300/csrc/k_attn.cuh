@@ -1,4 +1,4 @@
-// k_attn.cuh - mt_paged_attention: how the work of a batch is shared out over
+// k_attn.cuh - mt_paged_attention and mt_tree_attention: how the work of a batch is shared out over
 // the GPU, and the joining of the parts.
 //
 // Mathematics.  Row r of a tile is one (new token, query head) pair; with
@@ -24,6 +24,12 @@
 // tiles has rows.  (A chunk of 384 beside 15 single tokens: 78 us, and 85 with
 // equal blocks, 94 with 3 and 4; a prompt of 8000: 338, 343 and 341 us.)  A
 // stretch border within a block leaves the block to the later stretch.
+//
+// Trees (mt_tree_attention, TREE): a row sees those of the sequence's new tokens
+// whose bits are set in its row of `visible`, and of the tokens before them all,
+// or a window that ends at the row's position, which is the first new token's
+// plus the number of new tokens that the row sees, less one.  A tile's keys run
+// from the first position's window to the sequence's end.
 #pragma once
 #include <float.h>
 
@@ -44,6 +50,9 @@ struct AttnArgs {
   int window, sinks;
   int tile_tokens;  // tokens of a tile, 0: tiles of packed rows that may start within a token
   int max_q;        // the host's hint
+  const uint32_t* visible;  // trees: [T] rows of `words` words, visible_ld apart
+  int64_t visible_ld;
+  int words;
   int min_units;    // fewest blocks of a CTA's stretch
   float* part_o;    // [2 * CTAs][R][DP], or as part_at() says
   float2* part_ml;  // [2 * CTAs][R]
@@ -57,11 +66,11 @@ struct TileSpan {
   int win_lo;               // first key of the first token's window
   int sink, win, n;
 };
-template <int BK>
+template <int BK, bool TREE>
 __device__ __forceinline__ TileSpan tile_span(const PagedSeq& s, int i0, int i1, int window, int sinks) {
   TileSpan t;
-  t.first_pos = s.kv - s.n + i0;
-  t.last_pos = s.kv - s.n + i1;
+  t.first_pos = s.kv - s.n + (TREE ? 0 : i0);
+  t.last_pos = TREE ? s.kv - 1 : s.kv - s.n + i1;
   t.key_end = max(t.last_pos + 1, 0);
   t.win_lo = window > 0 ? max(t.first_pos - window + 1, 0) : 0;
   const int end = (t.key_end + BK - 1) / BK;
@@ -97,10 +106,10 @@ template <int EXTRA>
 __device__ __forceinline__ int block_units(const AttnArgs& a, const TileRows& r) {
   return EXTRA == 0 ? 1 : r.rows > a.tile_tokens / 2 * a.group ? 3 : 2;
 }
-template <int R, int BK, int EXTRA>
+template <int R, int BK, int EXTRA, bool TREE>
 __device__ __forceinline__ int tile_units(const AttnArgs& a, const PagedSeq& s, int rt) {
   const TileRows r = tile_rows<R>(a, s, rt);
-  return EXTRA + block_units<EXTRA>(a, r) * tile_span<BK>(s, r.i0, r.i1, a.window, a.sinks).n;
+  return EXTRA + block_units<EXTRA>(a, r) * tile_span<BK, TREE>(s, r.i0, r.i1, a.window, a.sinks).n;
 }
 
 // A position in the line of units.
@@ -111,13 +120,13 @@ struct Cursor {
   TileRows r;
 };
 
-template <int R, int BK>
+template <int R, int BK, bool TREE>
 __device__ __forceinline__ void cursor_tile(const AttnArgs& a, Cursor& c) {
   c.r = tile_rows<R>(a, c.s, c.rt);
-  c.t = tile_span<BK>(c.s, c.r.i0, c.r.i1, a.window, a.sinks);
+  c.t = tile_span<BK, TREE>(c.s, c.r.i0, c.r.i1, a.window, a.sinks);
 }
 // The next unit (there is one).
-template <int R, int BK>
+template <int R, int BK, bool TREE>
 __device__ __forceinline__ void cursor_next(const AttnArgs& a, Cursor& c) {
   if (++c.i < c.t.n) return;
   c.i = 0;
@@ -133,7 +142,7 @@ __device__ __forceinline__ void cursor_next(const AttnArgs& a, Cursor& c) {
       if (c.s.n == 0) return;
     }
   }
-  cursor_tile<R, BK>(a, c);
+  cursor_tile<R, BK, TREE>(a, c);
 }
 
 // a / b for counts: by the 32-bit divider where both fit (a 64-bit division takes
@@ -152,7 +161,7 @@ struct PlanShared {
 
 // The head, tile and unit of a sequence's unit `at`, of `each` to a head: by
 // every warp for itself, 32 tiles at a time.
-template <int R, int BK, int EXTRA>
+template <int R, int BK, int EXTRA, bool TREE>
 __device__ __forceinline__ void plan_tile(const AttnArgs& a, Cursor& c, long long each, long long at, int lane) {
   c.tiles = tile_count<R>(a, c.s);
   c.h = (int)div_count(at, each);
@@ -160,7 +169,7 @@ __device__ __forceinline__ void plan_tile(const AttnArgs& a, Cursor& c, long lon
   for (int rt0 = 0; rt0 < c.tiles; rt0 += 32) {
     const int rt = rt0 + lane;
     long long n = 0;
-    if (rt < c.tiles) n = tile_units<R, BK, EXTRA>(a, c.s, rt);
+    if (rt < c.tiles) n = tile_units<R, BK, EXTRA, TREE>(a, c.s, rt);
     long long in = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -176,13 +185,13 @@ __device__ __forceinline__ void plan_tile(const AttnArgs& a, Cursor& c, long lon
     }
     rest -= __shfl_sync(0xffffffffu, in, 31);
   }
-  cursor_tile<R, BK>(a, c);
+  cursor_tile<R, BK, TREE>(a, c);
 }
 
 // The plan for up to 32 sequences, a lane each, by every warp for itself: no
 // barrier and no shared memory.  (A kernel's first instructions run cold, and
 // the general plan below takes 6000 cycles, half of a short decode step.)
-template <int R, int BK, int EXTRA>
+template <int R, int BK, int EXTRA, bool TREE>
 __device__ __forceinline__ void plan_small(const AttnArgs& a, int cta, int ctas, long long* u0, long long* u1, long long* per, Cursor* cur) {
   const PagedArgs& pg = a.pg;
   const int lane = threadIdx.x & 31;
@@ -190,13 +199,13 @@ __device__ __forceinline__ void plan_small(const AttnArgs& a, int cta, int ctas,
   if (lane < pg.B) s = paged_seq(pg, lane);
   const int tiles = tile_count<R>(a, s);
   long long n = 0;  // units a head
-  if (tiles == 1) n = tile_units<R, BK, EXTRA>(a, s, 0);
+  if (tiles == 1) n = tile_units<R, BK, EXTRA, TREE>(a, s, 0);
   for (unsigned big = __ballot_sync(0xffffffffu, tiles > 1); big; big &= big - 1) {
     const int l = __ffs(big) - 1;
     const PagedSeq x = {__shfl_sync(0xffffffffu, s.row0, l), __shfl_sync(0xffffffffu, s.n, l), __shfl_sync(0xffffffffu, s.kv, l)};
     const int count = __shfl_sync(0xffffffffu, tiles, l);
     long long m = 0;
-    for (int rt = lane; rt < count; rt += 32) m += tile_units<R, BK, EXTRA>(a, x, rt);
+    for (int rt = lane; rt < count; rt += 32) m += tile_units<R, BK, EXTRA, TREE>(a, x, rt);
 #pragma unroll
     for (int o = 16; o; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
     if (lane == l) n = m;
@@ -217,7 +226,7 @@ __device__ __forceinline__ void plan_small(const AttnArgs& a, int cta, int ctas,
     const int lo = __ffs(__ballot_sync(0xffffffffu, inc > *u0)) - 1;
     c.b = lo;
     c.s = PagedSeq{__shfl_sync(0xffffffffu, s.row0, lo), __shfl_sync(0xffffffffu, s.n, lo), __shfl_sync(0xffffffffu, s.kv, lo)};
-    plan_tile<R, BK, EXTRA>(a, c, __shfl_sync(0xffffffffu, n, lo), *u0 - __shfl_sync(0xffffffffu, inc - units, lo), lane);
+    plan_tile<R, BK, EXTRA, TREE>(a, c, __shfl_sync(0xffffffffu, n, lo), *u0 - __shfl_sync(0xffffffffu, inc - units, lo), lane);
   }
   *cur = c;
 }
@@ -226,12 +235,12 @@ __device__ __forceinline__ void plan_small(const AttnArgs& a, int cta, int ctas,
 // stretch: [u0, u1) of all units, `per` to a CTA; cur->i counts the tile's
 // units, the EXTRA ones first.  Every thread of the block
 // (NT of them) calls it and gets the same answers; ends with a barrier.
-template <int R, int BK, int NT, int EXTRA>
+template <int R, int BK, int NT, int EXTRA, bool TREE>
 __device__ void plan(const AttnArgs& a, PlanShared* sh, int cta, int ctas, long long* u0, long long* u1, long long* per,
                      Cursor* cur) {
   const PagedArgs& pg = a.pg;
   if (pg.B <= 32) {
-    plan_small<R, BK, EXTRA>(a, cta, ctas, u0, u1, per, cur);
+    plan_small<R, BK, EXTRA, TREE>(a, cta, ctas, u0, u1, per, cur);
     __syncthreads();
     return;
   }
@@ -244,7 +253,7 @@ __device__ void plan(const AttnArgs& a, PlanShared* sh, int cta, int ctas, long 
     const int tiles = tile_count<R>(a, s);
     long long n = 0;
     if (tiles <= 4) {
-      for (int rt = 0; rt < tiles; ++rt) n += tile_units<R, BK, EXTRA>(a, s, rt);
+      for (int rt = 0; rt < tiles; ++rt) n += tile_units<R, BK, EXTRA, TREE>(a, s, rt);
     } else {
       sh->big[atomicAdd(&sh->n_big, 1)] = b;
     }
@@ -256,7 +265,7 @@ __device__ void plan(const AttnArgs& a, PlanShared* sh, int cta, int ctas, long 
     const PagedSeq s = paged_seq(pg, b);
     const int tiles = tile_count<R>(a, s);
     long long n = 0;
-    for (int rt = tid; rt < tiles; rt += NT) n += tile_units<R, BK, EXTRA>(a, s, rt);
+    for (int rt = tid; rt < tiles; rt += NT) n += tile_units<R, BK, EXTRA, TREE>(a, s, rt);
 #pragma unroll
     for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
     // (one per warp: a 64-bit addition to one word by every thread took 13000 cycles)
@@ -298,7 +307,7 @@ __device__ void plan(const AttnArgs& a, PlanShared* sh, int cta, int ctas, long 
     }
     c.b = lo;
     c.s = paged_seq(pg, lo);
-    plan_tile<R, BK, EXTRA>(a, c, div_count(sh->pre[lo + 1] - sh->pre[lo], pg.kv_heads), *u0 - sh->pre[lo], lane);
+    plan_tile<R, BK, EXTRA, TREE>(a, c, div_count(sh->pre[lo + 1] - sh->pre[lo], pg.kv_heads), *u0 - sh->pre[lo], lane);
   }
   *cur = c;
   __syncthreads();
@@ -309,6 +318,31 @@ __device__ void plan(const AttnArgs& a, PlanShared* sh, int cta, int ctas, long 
 __device__ __forceinline__ void put_cut(const AttnArgs& a, int cta, int last, const Cursor& c) {
   a.cut[2 * cta] = make_int4(last, c.s.row0, c.h, c.r.p0);
   a.cut[2 * cta + 1] = make_int4(c.r.rows, 0, 0, 0);
+}
+
+// Bits [0, n), n clamped to 0 .. 32.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
+
+// Trees: new token i's row of `visible`; its bits [at, at + 32) (at may be
+// negative; bits before the row, past its words or past the sequence's n new
+// tokens are 0); the number of them; and the token's position.
+__device__ __forceinline__ const uint32_t* tree_row(const AttnArgs& a, int row0, int i) {
+  return a.visible + (int64_t)(row0 + i) * a.visible_ld;
+}
+__device__ __forceinline__ uint32_t tree_bits(const AttnArgs& a, const uint32_t* row, int n, int at) {
+  const int end = min(32 * a.words, n);
+  if (at >= end || at <= -32) return 0u;
+  const int w = at >> 5;  // -1 at the least
+  const uint32_t lo = w >= 0 ? __ldg(row + w) : 0u, hi = w + 1 < a.words ? __ldg(row + w + 1) : 0u;
+  return __funnelshift_r(lo, hi, at & 31) & low_bits(end - at);
+}
+__device__ __forceinline__ int tree_count(const AttnArgs& a, const uint32_t* row, int n) {
+  int count = 0;
+  for (int w = 0; w < a.words && 32 * w < n; ++w) count += __popc(__ldg(row + w) & low_bits(n - 32 * w));
+  return count;
+}
+__device__ __forceinline__ int tree_pos(const AttnArgs& a, const uint32_t* row, int n, int base) {
+  return base + max(tree_count(a, row, n), 1) - 1;
 }
 
 __device__ __forceinline__ float exp2_(float x) { return exp2f(x); }

@@ -67,7 +67,7 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   lo = (uint32_t)f2bf(x - bf16f(hx)) | ((uint32_t)f2bf(y - bf16f(hy)) << 16);
 }
 
-template <int DP>
+template <int DP, bool TREE>
 __global__ void __launch_bounds__(AR_THREADS, ArShape<DP>::PER_SM) attn_rows_kernel(const AttnArgs a) {
   using S = ArShape<DP>;
   constexpr int ST = S::ST, CPR = DP / 8, NT8 = DP / 8;
@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(AR_THREADS, ArShape<DP>::PER_SM) attn_rows_ker
   pdl_trigger();
   long long u0, u1, per;
   Cursor ld;  // of the block whose page indices are fetched next
-  plan<AR_R, AR_BK, AR_THREADS, 0>(a, reinterpret_cast<PlanShared*>(ring), cta, ctas, &u0, &u1, &per, &ld);
+  plan<AR_R, AR_BK, AR_THREADS, 0, TREE>(a, reinterpret_cast<PlanShared*>(ring), cta, ctas, &u0, &u1, &per, &ld);
   if (tid == 0) a.cut[2 * cta].x = -1;
   if (u0 >= u1) return;
   const int units = (int)(u1 - u0);
@@ -92,6 +92,18 @@ __global__ void __launch_bounds__(AR_THREADS, ArShape<DP>::PER_SM) attn_rows_ker
   auto fetch = [&](const Cursor& c) -> int64_t {
     const int key = span_block(c.t, c.i) * AR_BK + tid;
     if (tid >= AR_BK || key >= c.t.key_end || (key < c.t.win_lo && key >= a.sinks)) return -1;
+    if constexpr (TREE) {
+      // a new token, or one that the window of no row may reach: does a row of the tile see it?
+      const int n = c.s.n, base = c.s.kv - n;
+      if (key >= base || (a.window > 0 && key >= a.sinks && key <= base + n - 1 - a.window)) {
+        bool seen = false;
+        for (int i = c.r.i0; i <= c.r.i1 && !seen; ++i) {
+          const uint32_t* row = tree_row(a, c.s.row0, i);
+          seen = key >= base ? tree_bits(a, row, n, key - base) & 1u : key > tree_pos(a, row, n, base) - a.window;
+        }
+        if (!seen) return -1;
+      }
+    }
     const int e = key / a.pg.page_size, page = paged_entry(a.pg, c.b, e);
     if (page < 0) return -1;
     return (int64_t)page * a.pg.page_stride + (int64_t)(key - e * a.pg.page_size) * a.pg.token_stride +
@@ -118,7 +130,7 @@ __global__ void __launch_bounds__(AR_THREADS, ArShape<DP>::PER_SM) attn_rows_ker
     if (u < units) {
       const int64_t off = fetch(ld);
       if (tid < AR_BK) off_sh[u & 1][tid] = off;
-      if (u + 1 < units) cursor_next<AR_R, AR_BK>(a, ld);
+      if (u + 1 < units) cursor_next<AR_R, AR_BK, TREE>(a, ld);
     }
     __syncthreads();
     if (u < ST - 1) {
@@ -135,6 +147,8 @@ __global__ void __launch_bounds__(AR_THREADS, ArShape<DP>::PER_SM) attn_rows_ker
   int i_first = cc.i;
   bool fresh = true;
   int pos0 = 0, pos1 = 0;
+  const uint32_t* row0 = nullptr;  // trees: of rows g and g + 8
+  const uint32_t* row1 = nullptr;
   for (int u = 0; u < units; ++u) {
     if (fresh) {  // a new tile: its rows of Q
       fresh = false;
@@ -145,6 +159,14 @@ __global__ void __launch_bounds__(AR_THREADS, ArShape<DP>::PER_SM) attn_rows_ker
       const uint16_t* q1 = a.q + (int64_t)(cc.s.row0 + (h1 ? r1 / G : 0)) * a.q_stride + (int64_t)(cc.h * G + (h1 ? r1 % G : 0)) * D;
       pos0 = h0 ? cc.s.kv - cc.s.n + r0 / G : -1;
       pos1 = h1 ? cc.s.kv - cc.s.n + r1 / G : -1;
+      if constexpr (TREE) {
+        row0 = h0 ? tree_row(a, cc.s.row0, r0 / G) : nullptr;
+        row1 = h1 ? tree_row(a, cc.s.row0, r1 / G) : nullptr;
+        if (a.window > 0) {
+          if (h0) pos0 = tree_pos(a, row0, cc.s.n, cc.s.kv - cc.s.n);
+          if (h1) pos1 = tree_pos(a, row1, cc.s.n, cc.s.kv - cc.s.n);
+        }
+      }
 #pragma unroll
       for (int ks = 0; ks < DP / 16; ++ks) {
         const int c = ks * 16 + 2 * tq;
@@ -166,7 +188,7 @@ __global__ void __launch_bounds__(AR_THREADS, ArShape<DP>::PER_SM) attn_rows_ker
     const bool more = u + ST < units;
     if (more) {
       off_next = fetch(ld);
-      if (u + ST + 1 < units) cursor_next<AR_R, AR_BK>(a, ld);
+      if (u + ST + 1 < units) cursor_next<AR_R, AR_BK, TREE>(a, ld);
     }
 
     const uint32_t kb = smem_u32(ring + (size_t)(u % ST) * 2 * S::HALF), vb = kb + S::HALF;
@@ -192,8 +214,13 @@ __global__ void __launch_bounds__(AR_THREADS, ArShape<DP>::PER_SM) attn_rows_ker
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int key = key0 + 8 * n + e;
-        const bool v0 = key <= pos0 && (a.window == 0 || key > pos0 - a.window || key < a.sinks);
-        const bool v1 = key <= pos1 && (a.window == 0 || key > pos1 - a.window || key < a.sinks);
+        bool v0 = key <= pos0 && (a.window == 0 || key > pos0 - a.window || key < a.sinks);
+        bool v1 = key <= pos1 && (a.window == 0 || key > pos1 - a.window || key < a.sinks);
+        if constexpr (TREE) {
+          const int at = key - (cc.s.kv - cc.s.n);
+          v0 = row0 && (at < 0 ? a.window == 0 || key > pos0 - a.window || key < a.sinks : tree_bits(a, row0, cc.s.n, at) & 1u);
+          v1 = row1 && (at < 0 ? a.window == 0 || key > pos1 - a.window || key < a.sinks : tree_bits(a, row1, cc.s.n, at) & 1u);
+        }
         s[n][e] = v0 ? s[n][e] * a.scale_log2 : -INFINITY;
         s[n][2 + e] = v1 ? s[n][2 + e] * a.scale_log2 : -INFINITY;
         x0 = fmaxf(x0, s[n][e]);
@@ -332,7 +359,7 @@ __global__ void __launch_bounds__(AR_THREADS, ArShape<DP>::PER_SM) attn_rows_ker
         put_cut(a, cta, (int)div_count(u0 + u + (cc.t.n - 1 - cc.i), per), cc);
       fresh = true;
     }
-    if (u + 1 < units) cursor_next<AR_R, AR_BK>(a, cc);
+    if (u + 1 < units) cursor_next<AR_R, AR_BK, TREE>(a, cc);
   }
   cp_async_wait_all();
 }
@@ -340,7 +367,7 @@ __global__ void __launch_bounds__(AR_THREADS, ArShape<DP>::PER_SM) attn_rows_ker
 int ar_ctas(int dp, int sms) { return sms * (dp == 64 ? 3 : dp == 128 ? 2 : 1); }
 int ar_dp(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
-template <int DP>
+template <int DP, bool TREE>
 mt_status run_rows(AttnArgs a, void* ws, const Launch& l, const DeviceInfo* di) {
   using S = ArShape<DP>;
   static std::atomic<bool> set[64];
@@ -348,7 +375,7 @@ mt_status run_rows(AttnArgs a, void* ws, const Launch& l, const DeviceInfo* di) 
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e);
   if (dev >= 0 && dev < 64 && !set[dev].load()) {
-    e = cudaFuncSetAttribute(attn_rows_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM);
+    e = cudaFuncSetAttribute(attn_rows_kernel<DP, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM);
     if (e != cudaSuccess) return cuda_fail(e);
     set[dev].store(true);
   }
@@ -361,7 +388,7 @@ mt_status run_rows(AttnArgs a, void* ws, const Launch& l, const DeviceInfo* di) 
   a.part_ml = reinterpret_cast<float2*>(w);
   w += (size_t)ctas * 2 * AR_R * sizeof(float2);
   a.part_o = reinterpret_cast<float*>(w);
-  if (const mt_status st = launch(attn_rows_kernel<DP>, dim3(ctas), dim3(AR_THREADS), S::SMEM, l, a)) return st;
+  if (const mt_status st = launch(attn_rows_kernel<DP, TREE>, dim3(ctas), dim3(AR_THREADS), S::SMEM, l, a)) return st;
   return launch(attn_join_kernel<AR_R, DP>, dim3(ctas, join_blocks(a)), dim3(32 * JOIN_WARPS), 0, l, a);
 }
 
@@ -373,10 +400,11 @@ size_t attn_rows_ws(int head_dim, int sms) {
 }
 
 mt_status launch_attn_rows(AttnArgs a, void* ws, const Launch& l, const DeviceInfo* di) {
+  const bool tree = a.visible != nullptr;
   switch (ar_dp(a.pg.head_dim)) {
-    case 64: return run_rows<64>(a, ws, l, di);
-    case 128: return run_rows<128>(a, ws, l, di);
-    default: return run_rows<256>(a, ws, l, di);
+    case 64: return tree ? run_rows<64, true>(a, ws, l, di) : run_rows<64, false>(a, ws, l, di);
+    case 128: return tree ? run_rows<128, true>(a, ws, l, di) : run_rows<128, false>(a, ws, l, di);
+    default: return tree ? run_rows<256, true>(a, ws, l, di) : run_rows<256, false>(a, ws, l, di);
   }
 }
 

@@ -193,9 +193,6 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int x, int 
 __device__ __forceinline__ void bulk_reads_done() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// Bits [0, n), n clamped to 0 .. 32.
-__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
-
 // A piece of a tile: the part of its blocks that lies in this CTA's stretch.
 // One warp walks the stretch and puts the pieces into a small ring in shared
 // memory for the others (each walking for itself cost them registers and, at
@@ -293,7 +290,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   pdl_trigger();
   long long u0, u1, per;
   Cursor c;
-  plan<AT_R, AT_BK, AT_THREADS, AT_EXTRA>(a, reinterpret_cast<PlanShared*>(smem + S::OFF_KV), blockIdx.x, gridDim.x, &u0, &u1, &per, &c);
+  plan<AT_R, AT_BK, AT_THREADS, AT_EXTRA, false>(a, reinterpret_cast<PlanShared*>(smem + S::OFF_KV), blockIdx.x, gridDim.x, &u0, &u1, &per, &c);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the plan's accesses before TMA's to the same memory
   tc_fence_before();
   __syncthreads();
@@ -371,7 +368,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           left -= end - c.i;
           if (left > 0) {
             c.i = c.t.n - 1;
-            cursor_next<AT_R, AT_BK>(a, c);
+            cursor_next<AT_R, AT_BK, false>(a, c);
           }
         }
       }
@@ -891,7 +888,7 @@ mt_status run_tile(AttnArgs a, void* ws, const Launch& l, const DeviceInfo* di) 
 // bf16), head sizes below 64 or above 128 (its tensor memory's columns), and
 // pages that are no multiple of 8 tokens (a box is whole 8-row swizzle atoms).
 bool attn_tile_takes(const AttnArgs& a) {
-  return !a.out_f32 && a.pg.head_dim >= 64 && a.pg.head_dim <= 128 && at_box(a.pg.page_size) >= 8;
+  return !a.visible && !a.out_f32 && a.pg.head_dim >= 64 && a.pg.head_dim <= 128 && at_box(a.pg.page_size) >= 8;
 }
 
 size_t attn_tile_ws(int head_dim, int sms) {

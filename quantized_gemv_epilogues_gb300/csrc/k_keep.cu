@@ -1,0 +1,134 @@
+// k_keep.cu - mt_cache_keep: the keys and values of a drafted path moved
+// together, in every layer's cache.
+//
+// Bound: latency for few texts, then memory: a token's K and V of every layer
+// read and written once.  A thread owns 16 bytes of a token's K or V (one
+// layer, head and column) and moves them for every token of the path, in order:
+// the path's indices increase and each is at least its place in the path, so a
+// place is written only after the token that lay there was read, and no thread
+// waits for another.
+#include <algorithm>
+
+#include "k_paged.cuh"
+
+namespace mt {
+
+namespace {
+
+constexpr int CK_THREADS = 256, CK_LAYERS = 64, CK_MOVES = 4;
+
+struct KeepArgs {
+  PagedArgs pg;  // of the first cache
+  const int32_t* path;
+  const int32_t* count;
+  int cols;
+  int32_t* new_len;
+  uint16_t* kv[CK_LAYERS][2];
+};
+
+__global__ void __launch_bounds__(CK_THREADS) cache_keep_kernel(const __grid_constant__ KeepArgs a) {
+  const PagedArgs& pg = a.pg;
+  const int b = blockIdx.x, layer = blockIdx.y;
+  pdl_wait();
+  pdl_trigger();
+  const PagedSeq s = paged_seq(pg, b);
+  const int base = s.kv - s.n, most = min(max(__ldg(a.count + b), 0), a.cols);
+  const int32_t* path = a.path + (int64_t)b * a.cols;
+  const int chunks = pg.head_dim / 8, units = 2 * pg.kv_heads * chunks;
+  for (int u = blockIdx.z * CK_THREADS + threadIdx.x; u < units; u += gridDim.z * CK_THREADS) {
+    const int side = u / (pg.kv_heads * chunks), rest = u - side * pg.kv_heads * chunks, h = rest / chunks;
+    uint16_t* const kv = a.kv[layer][side] + (int64_t)h * pg.head_stride + 8 * (rest - h * chunks);
+    auto place = [&](int pos) -> int64_t {  // of a token's row in the cache, or -1
+      if (pos < 0) return -1;
+      const int e = pos / pg.page_size, page = paged_entry(pg, b, e);
+      return page < 0 ? -1 : (int64_t)page * pg.page_stride + (int64_t)(pos - e * pg.page_size) * pg.token_stride;
+    };
+    int before = -1;
+    for (int i0 = 0; i0 < most; i0 += CK_MOVES) {
+      uint4 x[CK_MOVES];
+      int64_t to[CK_MOVES];
+      bool end = false;
+#pragma unroll
+      for (int q = 0; q < CK_MOVES; ++q) {
+        to[q] = -1;
+        const int i = i0 + q;
+        const int at = i < most ? __ldg(path + i) : -1;
+        end |= at <= before || at >= s.n;
+        if (end) continue;
+        before = at;
+        if (at == i) continue;
+        const int64_t from = place(base + at);
+        to[q] = from < 0 ? -1 : place(base + i);
+        if (to[q] >= 0) x[q] = *reinterpret_cast<const uint4*>(kv + from);
+      }
+#pragma unroll
+      for (int q = 0; q < CK_MOVES; ++q)
+        if (to[q] >= 0) *reinterpret_cast<uint4*>(kv + to[q]) = x[q];
+      if (end) break;
+    }
+  }
+  if (a.new_len && layer == 0 && blockIdx.z == 0 && threadIdx.x == 0) {
+    int i = 0, before = -1;
+    for (; i < most; ++i) {
+      const int at = __ldg(path + i);
+      if (at <= before || at >= s.n) break;
+      before = at;
+    }
+    a.new_len[b] = base + i;
+  }
+}
+
+}  // namespace
+
+}  // namespace mt
+
+using namespace mt;
+
+extern "C" mt_status mt_cache_keep(const mt_paged_cache* caches, int L, const mt_paged_batch* batch, const int32_t* path,
+                                   const int32_t* count, int cols, int32_t* new_len, void* stream) {
+  if (!caches || !batch || !path || !count) return MT_ERR_NULL;
+  if (L < 1 || L > PG_MAX_LAYERS || cols < 1 || cols > (1 << 20)) return MT_ERR_SHAPE;
+  KeepArgs a = {};
+  for (int i = L - 1; i >= 0; --i) {
+    const mt_paged_cache &c = caches[i], &f = caches[0];
+    if (const mt_status st = paged_args(&c, batch, &a.pg)) return st;
+    if (c.page_stride != f.page_stride || c.token_stride != f.token_stride || c.head_stride != f.head_stride ||
+        c.num_pages != f.num_pages || c.page_size != f.page_size || c.kv_heads != f.kv_heads || c.head_dim != f.head_dim)
+      return MT_ERR_SHAPE;
+  }
+  if (!aligned_to(path, 4) || !aligned_to(count, 4) || !aligned_to(new_len, 4)) return MT_ERR_ALIGN;
+  if (!paged_rows_apart(&caches[0])) return MT_ERR_SHAPE;
+  if (!paged_layers_apart(caches, L)) return MT_ERR_ALIAS;
+  const size_t bytes = paged_cache_bytes(&caches[0]);
+  const ByteRange ins[] = {byte_range(batch->q_start, (size_t)(batch->B + 1) * 4), byte_range(batch->kv_len, (size_t)batch->B * 4),
+                           byte_range(batch->pages, (size_t)((batch->B - 1) * batch->pages_ld + batch->max_pages) * 4),
+                           byte_range(path, (size_t)batch->B * cols * 4), byte_range(count, (size_t)batch->B * 4)};
+  const ByteRange rn = byte_range(new_len, (size_t)batch->B * 4);
+  for (const ByteRange& r : ins)
+    if (ranges_overlap(r, rn)) return MT_ERR_ALIAS;
+  for (int i = 0; i < L; ++i)
+    for (const void* p : {caches[i].k, caches[i].v}) {
+      const ByteRange rc = byte_range(p, bytes);
+      if (ranges_overlap(rc, rn)) return MT_ERR_ALIAS;
+      for (const ByteRange& r : ins)
+        if (ranges_overlap(r, rc)) return MT_ERR_ALIAS;
+    }
+  a.pg.err = device_error_ptr();
+  if (!a.pg.err) return MT_ERR_CUDA;
+  a.path = path;
+  a.count = count;
+  a.cols = cols;
+  const Launch l{(cudaStream_t)stream, mt_get_option(MT_OPT_PDL) != 0};
+  const int units = 2 * a.pg.kv_heads * (a.pg.head_dim / 8);
+  for (int i = 0; i < L; i += CK_LAYERS) {
+    const int layers = std::min(CK_LAYERS, L - i);
+    a.new_len = i == 0 ? new_len : nullptr;
+    for (int j = 0; j < layers; ++j) {
+      a.kv[j][0] = (uint16_t*)caches[i + j].k;
+      a.kv[j][1] = (uint16_t*)caches[i + j].v;
+    }
+    const dim3 grid(batch->B, layers, (units + CK_THREADS - 1) / CK_THREADS);
+    if (const mt_status st = launch(cache_keep_kernel, grid, dim3(CK_THREADS), 0, l, a)) return st;
+  }
+  return MT_OK;
+}

@@ -62,6 +62,23 @@ bool paged_kv_apart(const mt_paged_cache* c) {
   return !rows_meet(((int64_t)(uintptr_t)c->v - (int64_t)(uintptr_t)c->k) / 2, d, n, c->head_dim);
 }
 
+bool paged_layers_apart(const mt_paged_cache* c, int L) {
+  const int64_t bytes = (int64_t)paged_cache_bytes(c);
+  int64_t at[2 * PG_MAX_LAYERS];
+  for (int i = 0; i < L; ++i) {
+    at[2 * i] = (int64_t)(uintptr_t)c[i].k;
+    at[2 * i + 1] = (int64_t)(uintptr_t)c[i].v;
+  }
+  std::sort(at, at + 2 * L);
+  Dim d[3];
+  const int n = cache_dims(c, d);
+  // most caches span no other; the rows of those that do are compared
+  for (int i = 0; i < 2 * L; ++i)
+    for (int j = i + 1; j < 2 * L && at[j] - at[i] < bytes; ++j)
+      if (rows_meet((at[j] - at[i]) / 2, d, n, c->head_dim)) return false;
+  return true;
+}
+
 mt_status paged_args(const mt_paged_cache* c, const mt_paged_batch* b, PagedArgs* a) {
   if (!c || !b || !c->k || !c->v || !b->q_start || !b->kv_len || !b->pages) return MT_ERR_NULL;
   if (c->num_pages < 1 || c->page_size < 1 || c->page_size > 65536 || c->kv_heads < 1 || c->kv_heads > 1024 ||

@@ -12,6 +12,7 @@
 namespace mt {
 
 constexpr int PG_MAX_B = 1024;
+constexpr int PG_MAX_LAYERS = 1024;
 
 struct PagedArgs {
   uint16_t* k;
@@ -60,6 +61,9 @@ mt_status paged_args(const mt_paged_cache* c, const mt_paged_batch* b, PagedArgs
 bool paged_rows_apart(const mt_paged_cache* c);
 // Whether no row of K shares an element with one of V; rows apart only.
 bool paged_kv_apart(const mt_paged_cache* c);
+// Whether no two of the K and V of L caches of equal strides and sizes share an
+// element; rows apart and L <= PG_MAX_LAYERS only.
+bool paged_layers_apart(const mt_paged_cache* c, int L);
 // Bytes from a cache pointer to the end of its last element.
 size_t paged_cache_bytes(const mt_paged_cache* c);
 
