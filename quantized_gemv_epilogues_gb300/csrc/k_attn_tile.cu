@@ -223,7 +223,7 @@ constexpr size_t at_smem() {
 }
 static_assert(at_smem<128>() <= 227 * 1024 && at_smem<64>() <= 227 * 1024, "shared memory plan");
 
-template <int DP>
+template <int DP, bool TREE>
 __global__ void __launch_bounds__(AT_THREADS, 1)
     attn_tile_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap, const AttnArgs a,
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   pdl_trigger();
   long long u0, u1, per;
   Cursor c;
-  plan<AT_R, AT_BK, AT_THREADS, AT_EXTRA, false>(a, reinterpret_cast<PlanShared*>(smem + S::OFF_KV), blockIdx.x, gridDim.x, &u0, &u1, &per, &c);
+  plan<AT_R, AT_BK, AT_THREADS, AT_EXTRA, TREE>(a, reinterpret_cast<PlanShared*>(smem + S::OFF_KV), blockIdx.x, gridDim.x, &u0, &u1, &per, &c);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the plan's accesses before TMA's to the same memory
   tc_fence_before();
   __syncthreads();
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
               const int first = c.r.i0 + s * tps, last = min(first + tps - 1, c.r.i1);
-              const int to = (max(c.s.kv - c.s.n + last + 1, 0) + AT_BK - 1) / AT_BK;
+              const int to = ((TREE ? c.t.key_end : max(c.s.kv - c.s.n + last + 1, 0)) + AT_BK - 1) / AT_BK;
               const int all = min(c.t.sink, to) + max(0, to - c.t.win);  // of the tile's blocks, those up to the last token
               p.n[s] = first > c.r.i1 ? 0 : min(max(all - i0, 0), i1 - i0);
             }
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           left -= end - c.i;
           if (left > 0) {
             c.i = c.t.n - 1;
-            cursor_next<AT_R, AT_BK, false>(a, c);
+            cursor_next<AT_R, AT_BK, TREE>(a, c);
           }
         }
       }
@@ -395,6 +395,14 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         const int32_t* const table = a.pg.pages + (int64_t)p.b * a.pg.pages_ld;
         auto entries = [&](int e) -> int { return e + lane < a.pg.max_pages ? __ldg(table + e + lane) : -1; };
         int e0 = -(1 << 30), here = -1, there = -1;
+        // trees: the tile's window starts at its least position, not at the sequence's,
+        // and is one of the tokens before the new ones
+        int win_lo = TREE ? p.win_lo : 0;
+        if (TREE && kv && a.window > 0) {
+          int least = 1 << 30;
+          for (int i = p.i0 + lane; i <= p.i1; i += 32) least = min(least, tree_pos(a, tree_row(a, p.row0, i), p.kv - p.base, p.base));
+          win_lo = max(min(__reduce_min_sync(0xffffffffu, least) - a.window + 1, p.base), 0);
+        }
         if (kv == 0 && lane == 0) {
           const int tps = a.tile_tokens >> 1;
 #pragma unroll
@@ -415,9 +423,25 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           // last token's) end, and lie between the sinks and the first window.
           // Where such a border falls within a box, V's rows beyond it are
           // zeroed below: a weight of zero times what lies there may be NaN.
-          const int end = p.key_end - blk0, gap0 = a.sinks - blk0, gap1 = p.win_lo - blk0;
+          const int end = p.key_end - blk0, gap0 = a.sinks - blk0, gap1 = (TREE ? win_lo : p.win_lo) - blk0;
           auto within = [&](int x) -> bool { return x > 0 && x < AT_BK && (x & (box_rows - 1)); };
-          const bool patch = kv && (within(end) || (gap1 > gap0 && (within(gap1) || within(gap0))));
+          bool patch = kv && (within(end) || (gap1 > gap0 && (within(gap1) || within(gap0))));
+          // trees: so do new tokens that none of the tile's tokens sees
+          uint32_t hidden[AT_BK / 32];
+          if (TREE && kv) {
+#pragma unroll
+            for (int q = 0; q < AT_BK / 32; ++q) hidden[q] = 0;
+            if (blk0 + AT_BK > p.base) {
+#pragma unroll
+              for (int q = 0; q < AT_BK / 32; ++q) {
+                uint32_t seen = 0;
+                for (int i = p.i0 + lane; i <= p.i1; i += 32)
+                  seen |= tree_bits(a, tree_row(a, p.row0, i), p.kv - p.base, blk0 + 32 * q - p.base);
+                hidden[q] = low_bits(end - 32 * q) & ~low_bits(p.base - blk0 - 32 * q) & ~__reduce_or_sync(0xffffffffu, seen);
+                patch |= hidden[q] != 0;
+              }
+            }
+          }
           // this lane's box: the table's entry and the row in the page
           const int k0 = blk0 + lane * box_rows, e = k0 / a.pg.page_size;
           const int first = __shfl_sync(0xffffffffu, e, 0), last = __shfl_sync(0xffffffffu, e, boxes - 1);
@@ -432,7 +456,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           }
           const int p_here = __shfl_sync(0xffffffffu, here, (e - e0) & 31), p_there = __shfl_sync(0xffffffffu, there, (e - e0) & 31);
           int page = a.pg.num_pages, row = 0;  // beyond the cache: zeros, for a box that no row sees
-          if (lane < boxes && k0 < p.key_end && (k0 + box_rows > p.win_lo || k0 < a.sinks)) {
+          if (lane < boxes && k0 < p.key_end && (k0 + box_rows > (TREE ? win_lo : p.win_lo) || k0 < a.sinks)) {
             const int x = e - e0 < 32 ? p_here : p_there;
             row = k0 - e * a.pg.page_size;
             if ((unsigned)x < (unsigned)a.pg.num_pages) page = x;
@@ -455,7 +479,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             ++tails;
             unsigned char* v = smem + S::OFF_KV + (size_t)q * S::TILE;
             for (int r = lane; r < AT_BK; r += 32)
-              if (r >= end || (r >= gap0 && r < gap1))
+              if (r >= end || (r >= gap0 && r < gap1) || (TREE && ((hidden[r >> 5] >> lane) & 1u)))
                 for (int c = 0; c < 8 * S::CH; ++c)  // 16 bytes each
                   *reinterpret_cast<uint4*>(v + (c >> 3) * S::HALF + r * 128 + 16 * ((c + r) & 7)) = make_uint4(0, 0, 0, 0);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -600,7 +624,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       if (tok0 <= p.i1) {  // the tile has rows
         const int tok = tok0 + r_tok;
         const bool row = r < tps * G && tok <= p.i1;
-        const int pos = row ? p.base + tok : -1;
+        const int fresh = p.kv - p.base;  // the sequence's new tokens
+        const uint32_t* const bits = TREE && row ? tree_row(a, p.row0, tok) : nullptr;
+        const int pos = !row ? -1 : !TREE ? p.base + tok : a.window ? tree_pos(a, bits, fresh, p.base) : 0;
         const int pos_first = p.base + tok0, pos_last = p.base + min(tok0 + tps - 1, p.i1);
         float m = -INFINITY;  // reference maximum, in units of scores
         float l = 0.f;
@@ -618,16 +644,20 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
 #pragma unroll
           for (int q = 0; q < 4; ++q) at_ld_done32(x + 32 * q);
           // every row sees the whole block, unless it reaches past the first row or out of the last row's window
-          const bool clear = k0 + AT_BK - 1 <= pos_first && (a.window == 0 || k0 > pos_last - a.window || k0 + AT_BK <= a.sinks);
+          const bool clear = k0 + AT_BK - (TREE ? 0 : 1) <= (TREE ? p.base : pos_first) &&
+                             (a.window == 0 || k0 > (TREE ? p.kv - 1 : pos_last) - a.window || k0 + AT_BK <= a.sinks);
           if (!clear) {
             // a bit for each key that the row sees: [lo, hi) and the sinks [0, sk).
             // The empty statement keeps the selects inside the branch (without it
             // every block paid for them: 2200 of a block's 5800 cycles)
             asm volatile("");
-            const int hi = pos - k0 + 1, lo = a.window ? hi - a.window : 0, sk = min(a.sinks - k0, hi);
+            // (trees: of the tokens before the new ones)
+            const int hi = TREE ? (row ? p.base - k0 : 0) : pos - k0 + 1;
+            const int lo = a.window ? (TREE ? pos - k0 + 1 : hi) - a.window : 0, sk = min(a.sinks - k0, hi);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const uint32_t w = (low_bits(hi - 32 * q) & ~low_bits(lo - 32 * q)) | low_bits(sk - 32 * q);
+              uint32_t w = (low_bits(hi - 32 * q) & ~low_bits(lo - 32 * q)) | low_bits(sk - 32 * q);
+              if (TREE && bits) w |= tree_bits(a, bits, fresh, k0 + 32 * q - p.base);
               if (__all_sync(0xffffffffu, w == 0xFFFFFFFFu)) continue;
               asm volatile("");
 #pragma unroll
@@ -827,14 +857,14 @@ bool at_map(CUtensorMap* m, const void* p, int rank, const cuuint64_t* dims, con
 // Tokens of a box: the largest power of two that divides the page size, at most a block.
 int at_box(int page_size) { return std::min(page_size & -page_size, AT_BK); }
 
-template <int DP>
+template <int DP, bool TREE>
 mt_status run_tile(AttnArgs a, void* ws, const Launch& l, const DeviceInfo* di) {
   static std::atomic<bool> set[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e);
   if (dev >= 0 && dev < 64 && !set[dev].load()) {
-    e = cudaFuncSetAttribute(attn_tile_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)at_smem<DP>());
+    e = cudaFuncSetAttribute(attn_tile_kernel<DP, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)at_smem<DP>());
     if (e != cudaSuccess) return cuda_fail(e);
     set[dev].store(true);
   }
@@ -874,7 +904,7 @@ mt_status run_tile(AttnArgs a, void* ws, const Launch& l, const DeviceInfo* di) 
   a.part_ml = reinterpret_cast<float2*>(w);
   w += (size_t)ctas * 2 * AT_R * sizeof(float2);
   a.part_o = reinterpret_cast<float*>(w);
-  if (const mt_status st = launch(attn_tile_kernel<DP>, dim3(ctas), dim3(AT_THREADS), at_smem<DP>(), l, qmap, kmap, vmap, omap, a, box)) return st;
+  if (const mt_status st = launch(attn_tile_kernel<DP, TREE>, dim3(ctas), dim3(AT_THREADS), at_smem<DP>(), l, qmap, kmap, vmap, omap, a, box)) return st;
   return launch(attn_join_kernel<AT_R, DP>, dim3(ctas, join_blocks(a)), dim3(32 * JOIN_WARPS), 0, l, a);
 }
 
@@ -888,7 +918,7 @@ mt_status run_tile(AttnArgs a, void* ws, const Launch& l, const DeviceInfo* di) 
 // bf16), head sizes below 64 or above 128 (its tensor memory's columns), and
 // pages that are no multiple of 8 tokens (a box is whole 8-row swizzle atoms).
 bool attn_tile_takes(const AttnArgs& a) {
-  return !a.visible && !a.out_f32 && a.pg.head_dim >= 64 && a.pg.head_dim <= 128 && at_box(a.pg.page_size) >= 8;
+  return !a.out_f32 && a.pg.head_dim >= 64 && a.pg.head_dim <= 128 && at_box(a.pg.page_size) >= 8;
 }
 
 size_t attn_tile_ws(int head_dim, int sms) {
@@ -897,7 +927,8 @@ size_t attn_tile_ws(int head_dim, int sms) {
 }
 
 mt_status launch_attn_tile(AttnArgs a, void* ws, const Launch& l, const DeviceInfo* di) {
-  return a.pg.head_dim <= 64 ? run_tile<64>(a, ws, l, di) : run_tile<128>(a, ws, l, di);
+  if (a.visible) return a.pg.head_dim <= 64 ? run_tile<64, true>(a, ws, l, di) : run_tile<128, true>(a, ws, l, di);
+  return a.pg.head_dim <= 64 ? run_tile<64, false>(a, ws, l, di) : run_tile<128, false>(a, ws, l, di);
 }
 
 }  // namespace mt
