@@ -16,9 +16,17 @@
 // another order of the sum.
 //
 // Bound: latency, then memory: a float for each child that is tried and one row
-// of p (and of q) for the token that is drawn.  A block a sequence.
+// of p (and of q) for the token that is drawn.  A cluster of blocks shares out a
+// sequence's vocabulary.  The parents, tokens, numbers and probabilities of all
+// of its children are fetched at the start, in one round of loads; every block
+// walks the tree for itself in shared memory, all children of a token in a warp
+// at a time; sums over the vocabulary meet through distributed shared memory.
+// R is summed up only where another child comes: not in chains.
 #include <math.h>
 
+#include <algorithm>
+
+#include "k_cluster.cuh"
 #include "k_paged.cuh"
 
 namespace mt {
@@ -26,6 +34,7 @@ namespace mt {
 namespace {
 
 constexpr int VF_THREADS = 512, VF_WARPS = VF_THREADS / 32;
+constexpr int VF_TREE = 512;  // tokens of a sequence that are kept in shared memory
 constexpr uint64_t VF_ONE = 1ull << 56;
 
 struct VerifyArgs {
@@ -42,6 +51,7 @@ struct VerifyArgs {
   int32_t* out_path;
   int32_t* out_count;
   int cols;
+  int blocks;  // of a sequence
 };
 
 // A probability in steps of 2^-56: above 1 as 1, below 0 and NaN as 0.
@@ -64,78 +74,178 @@ __device__ __forceinline__ uint64_t left_of(const float* p, const float* q, int 
   return DRAFT && S ? less(x, times(S, steps(__ldg(q + v)))) : x;
 }
 
+// The sum of x over a warp.
+__device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+// The sum of x over the lanes up to and with this one.
+__device__ __forceinline__ uint64_t warp_upto(uint64_t x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
 template <bool DRAFT>
 __global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArgs a) {
-  __shared__ uint64_t part[VF_WARPS];  // sums of each warp's stretch of the vocabulary
+  __shared__ int32_t t_parent[VF_TREE], t_token[VF_TREE];
+  __shared__ float t_random[VF_TREE], t_p[VF_TREE], t_q[DRAFT ? VF_TREE : 1];
+  __shared__ uint64_t part[VF_WARPS];  // sums of each warp's stretch of this block's share of the vocabulary
+  __shared__ uint64_t share[2][16];    // of each block's share, in turn
   __shared__ uint64_t s_S, s_U;
   __shared__ int s_node, s_more, s_refused, s_count;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x, V = a.V;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, C = a.blocks, V = a.V;
+  const int rank = C > 1 ? (int)cluster_rank() : 0, b = blockIdx.x / C;
+  if (C > 1) cluster_arrive();  // this block runs: the others may write to it
   pdl_wait();
   pdl_trigger();
   const int row0 = min(max(__ldg(a.q_start + b), 0), a.T);
   const int n = min(max(__ldg(a.q_start + b + 1), row0), a.T) - row0;
   int32_t* out_tokens = a.out_tokens + (int64_t)b * a.cols;
   int32_t* out_path = a.out_path + (int64_t)b * a.cols;
+  const bool writes = rank == 0;
   if (n == 0) {
-    for (int i = tid; i < a.cols; i += VF_THREADS) out_tokens[i] = out_path[i] = -1;
-    if (tid == 0) a.out_count[b] = 0;
+    if (writes) {
+      for (int i = tid; i < a.cols; i += VF_THREADS) out_tokens[i] = out_path[i] = -1;
+      if (tid == 0) a.out_count[b] = 0;
+    }
+    __syncwarp();
+    if (C > 1) cluster_wait();
     return;
   }
-  const int per = ((V + VF_WARPS - 1) / VF_WARPS + 31) & ~31;  // tokens of a warp's stretch
-  const int v0 = min(warp * per, V), v1 = min(v0 + per, V);
   auto target = [&](int node) { return a.target + (int64_t)(row0 + node) * a.target_ld; };
   auto draft = [&](int node) { return DRAFT ? a.draft + (int64_t)(row0 + node) * a.draft_ld : nullptr; };
+  for (int i = tid; i < min(n, VF_TREE); i += VF_THREADS) {
+    const int up = __ldg(a.parent + row0 + i), x = __ldg(a.tokens + row0 + i);
+    const bool in = up >= 0 && up < i && x >= 0 && x < V;
+    t_random[i] = __ldg(a.random + row0 + i);
+    t_parent[i] = up;
+    t_token[i] = x;
+    t_p[i] = in ? __ldg(target(up) + x) : 0.f;
+    if (DRAFT) t_q[i] = in ? __ldg(draft(up) + x) : 0.f;
+  }
+  __syncthreads();
+  auto parent = [&](int i) { return i < VF_TREE ? t_parent[i] : __ldg(a.parent + row0 + i); };
+  auto token = [&](int i) { return i < VF_TREE ? t_token[i] : __ldg(a.tokens + row0 + i); };
+  // is token c a child of `node`?
+  auto child_at = [&](int node, int c) { return c > node && c < n && parent(c) == node; };
+  // (whole warps) has a child of `node` before this lane's, c0 + lane, its token x?
+  auto said_before = [&](int node, int c0, bool child, int x) {
+    const unsigned kids = __ballot_sync(0xffffffffu, child);
+    const unsigned same = __match_any_sync(0xffffffffu, x) & kids & ((1u << lane) - 1u);
+    bool again = same != 0;
+    for (int d0 = node + 1; d0 < c0; d0 += 32) {
+      const bool early = child_at(node, d0 + lane);
+      const int y = early ? token(d0 + lane) : 0;
+      for (unsigned who = __ballot_sync(0xffffffffu, early); who; who &= who - 1) again |= __shfl_sync(0xffffffffu, y, __ffs(who) - 1) == x;
+    }
+    return child && again;
+  };
+
+  // This block's share of the vocabulary, and each warp's stretch of it.  Rows
+  // are read four floats at a time where they all lie on 16-byte boundaries.
+  const int per_block = ((V + C - 1) / C + 31) & ~31, b0 = min(rank * per_block, V), b1 = min(b0 + per_block, V);
+  const int per = ((b1 - b0 + VF_WARPS - 1) / VF_WARPS + 31) & ~31;
+  const int v0 = min(b0 + warp * per, b1), v1 = min(v0 + per, b1);
+  const bool fours = ((uintptr_t)a.target & 15) == 0 && a.target_ld % 4 == 0 && (!DRAFT || (((uintptr_t)a.draft & 15) == 0 && a.draft_ld % 4 == 0));
   auto sum_stretch = [&](int node, uint64_t S) {
     const float* p = target(node);
     const float* q = draft(node);
     uint64_t sum = 0;
-#pragma unroll 8
-    for (int v = v0 + lane; v < v1; v += 32) sum += left_of<DRAFT>(p, q, v, S);
+    int v = v0 + lane;
+    if (fours) {
+      auto add = [&](float x, float y) { sum += DRAFT && S ? less(steps(x), times(S, steps(y))) : steps(x); };
+      constexpr int F = 4;
+      for (v = v0 + 4 * lane; v + 4 <= v1; v += 128 * F) {
+        float4 x[F], y[F];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        for (int i = 0; i < F; ++i) {
+          const bool in = v + 128 * i + 4 <= v1;
+          x[i] = in ? __ldg(reinterpret_cast<const float4*>(p + v + 128 * i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          if (DRAFT) y[i] = in && S ? __ldg(reinterpret_cast<const float4*>(q + v + 128 * i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+          add(x[i].x, DRAFT ? y[i].x : 0.f);
+          add(x[i].y, DRAFT ? y[i].y : 0.f);
+          add(x[i].z, DRAFT ? y[i].z : 0.f);
+          add(x[i].w, DRAFT ? y[i].w : 0.f);
+        }
+      }
+      v = v1 - (v1 - v0) % 4 + lane;  // a stretch starts on a multiple of 32
+    }
+#pragma unroll 4
+    for (; v < v1; v += 32) sum += left_of<DRAFT>(p, q, v, S);
+    sum = warp_sum(sum);
     if (lane == 0) part[warp] = sum;
   };
-  // is token c a child of `node`?
-  auto child_at = [&](int node, int c) { return c > node && c < n && __ldg(a.parent + row0 + c) == node; };
+  // (the whole block, part[] written and a barrier passed) the blocks' sums, in share[turn]
+  int turn = 0;
+  bool met = C == 1;
+  auto meet = [&]() {
+    if (!met) cluster_wait();  // every block runs
+    met = true;
+    turn ^= 1;
+    if (tid < C) {
+      uint64_t sum = 0;
+      for (int w = 0; w < VF_WARPS; ++w) sum += part[w];
+      if (C > 1) cluster_put(&share[turn][rank], tid, sum);
+      else share[turn][0] = sum;
+    }
+    __syncwarp();
+    if (C > 1) {
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
+  };
+  auto shared_sum = [&]() {
+    uint64_t sum = 0;
+    for (int r = 0; r < C; ++r) sum += share[turn][r];
+    return sum;
+  };
 
   if (warp == 0) {
     // ---- the walk; the other warps add up rows for it
     int node = 0, count = 0;
-    bool refused = false;
+    bool refused = false, known = true;  // is R?
     uint64_t S = 0, R = VF_ONE;
     for (;;) {
-      if (lane == 0) out_path[count] = node;
+      if (lane == 0 && writes) out_path[count] = node;
       ++count;
       S = 0;
       R = VF_ONE;
       refused = false;
+      known = true;
       if (count == a.cols) break;
       int next = -1;
       for (int c0 = node + 1; c0 < n && next < 0; c0 += 32) {
-        for (unsigned kids = __ballot_sync(0xffffffffu, child_at(node, c0 + lane)); kids; kids &= kids - 1) {
-          const int c = c0 + __ffs(kids) - 1, x = __ldg(a.tokens + row0 + c);
-          const bool in = x >= 0 && x < V;
-          const uint64_t U = chance(__ldg(a.random + row0 + c));
-          uint64_t r = in ? left_of<DRAFT>(target(node), draft(node), x, S) : 0;
-          bool take;
-          if (DRAFT) {
-            const uint64_t q = in ? steps(__ldg(draft(node) + x)) : 0;
-            take = __umul64hi(times(R, q), U) < r;
-          } else {
-            // a token that was refused here before has nothing left
-            for (int d0 = node + 1; d0 < c && r; d0 += 32) {
-              const int d = d0 + lane;
-              if (__any_sync(0xffffffffu, d < c && child_at(node, d) && __ldg(a.tokens + row0 + d) == x)) r = 0;
-            }
-            take = __umul64hi(R, U) < r;
-          }
-          if (take) {
-            next = c;
-            break;
-          }
+        const int c = c0 + lane;
+        const bool child = child_at(node, c);
+        unsigned kids = __ballot_sync(0xffffffffu, child);
+        if (!kids) continue;
+        const int x = child ? token(c) : -1;
+        const bool in = x >= 0 && x < V;
+        const uint64_t U = child ? chance(c < VF_TREE ? t_random[c] : __ldg(a.random + row0 + c)) : 0;
+        const uint64_t p = in ? steps(c < VF_TREE ? t_p[c] : __ldg(target(node) + x)) : 0;
+        if (!DRAFT) {
+          // all of them at once: R is down by the earlier ones' shares
+          const uint64_t r = said_before(node, c0, child, x) ? 0 : p;
+          const uint64_t upto = warp_upto(r, lane);
+          const unsigned taken = __ballot_sync(0xffffffffu, child && __umul64hi(less(R, upto - r), U) < r);
+          if (taken) next = c0 + __ffs(taken) - 1;
+          R = less(R, __shfl_sync(0xffffffffu, upto, 31));
           refused = true;
-          if (DRAFT) {
-            S += R;
+          continue;
+        }
+        const uint64_t q = in ? steps(c < VF_TREE ? t_q[DRAFT ? c : 0] : __ldg(draft(node) + x)) : 0;
+        for (; kids; kids &= kids - 1) {
+          if (!known) {
             if (lane == 0) {
               s_S = S;
               s_node = node;
@@ -144,15 +254,22 @@ __global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArg
             __syncthreads();
             sum_stretch(node, S);
             __syncthreads();
-            R = 0;
-            for (int w = 0; w < VF_WARPS; ++w) R += part[w];
-          } else {
-            R = less(R, r);
+            meet();
+            R = shared_sum();
+            known = true;
           }
+          const int who = __ffs(kids) - 1;
+          const uint64_t left = S ? less(p, times(S, q)) : p;
+          if (__shfl_sync(0xffffffffu, (int)(__umul64hi(times(R, q), U) < left), who)) {
+            next = c0 + who;
+            break;
+          }
+          S += R;
+          known = false;
         }
       }
       if (next < 0) break;
-      if (lane == 0) out_tokens[count - 1] = __ldg(a.tokens + row0 + next);
+      if (lane == 0 && writes) out_tokens[count - 1] = token(next);
       node = next;
     }
     if (lane == 0) {
@@ -161,10 +278,11 @@ __global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArg
       s_more = 0;
       s_refused = refused;
       s_count = count;
-      s_U = chance(__ldg(a.random + row0));
-      a.out_count[b] = count;
+      s_U = chance(t_random[0]);
+      if (writes) a.out_count[b] = count;
     }
-    for (int i = count + lane; i < a.cols; i += 32) out_tokens[i] = out_path[i] = -1;
+    if (writes)
+      for (int i = count + lane; i < a.cols; i += 32) out_tokens[i] = out_path[i] = -1;
     __syncthreads();
   } else {
     for (;;) {
@@ -172,6 +290,7 @@ __global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArg
       if (!s_more) break;
       sum_stretch(s_node, s_S);
       __syncthreads();
+      meet();
     }
   }
   // ---- the draw
@@ -184,51 +303,69 @@ __global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArg
     if (without) {
       // each refused token once: the first child that has it
       for (int c0 = node + 1 + warp * 32; c0 < n; c0 += VF_THREADS) {
-        for (unsigned kids = __ballot_sync(0xffffffffu, child_at(node, c0 + lane)); kids; kids &= kids - 1) {
-          const int c = c0 + __ffs(kids) - 1, x = __ldg(a.tokens + row0 + c);
-          bool again = x < 0 || x >= V;
-          for (int d0 = node + 1; d0 < c && !again; d0 += 32) {
-            const int d = d0 + lane;
-            again = __any_sync(0xffffffffu, d < c && child_at(node, d) && __ldg(a.tokens + row0 + d) == x);
-          }
-          if (!again && lane == 0)
-            atomicAdd(reinterpret_cast<unsigned long long*>(&part[x / per]), (unsigned long long)(0ull - steps(__ldg(target(node) + x))));
+        const int c = c0 + lane;
+        const bool child = child_at(node, c);
+        const int x = child ? token(c) : -1;
+        const bool again = said_before(node, c0, child, x);
+        if (child && !again && x >= b0 && x < b1) {
+          const uint64_t p = steps(c < VF_TREE ? t_p[c] : __ldg(target(node) + x));
+          atomicAdd(reinterpret_cast<unsigned long long*>(&part[(x - b0) / per]), (unsigned long long)(0ull - p));
         }
       }
       __syncthreads();
     }
-    uint64_t total = 0;
-    for (int w = 0; w < VF_WARPS; ++w) total += part[w];
+    meet();
+    const uint64_t total = shared_sum();
     if (total > 0) {
-      // the first token whose running sum is above random * total
+      // the first token whose running sum is above random * total: its block,
       uint64_t rest = __umul64hi(total, s_U);
+      int r = 0;
+      while (rest >= share[turn][r]) rest -= share[turn][r++];
+      if (r != rank) return;
+      // its stretch,
       int w = 0;
       while (rest >= part[w]) rest -= part[w++];
-      if (w != warp) return;
+      const int w0 = min(b0 + w * per, b1), w1 = min(w0 + per, b1);
+      // and there a few tokens a thread
       const float* p = target(node);
       const float* q = draft(node);
-      for (int v = v0; v < v1; v += 32) {
-        uint64_t x = v + lane < v1 ? left_of<DRAFT>(p, q, v + lane, S) : 0;
-        if (without) {
-          for (int c0 = node + 1; c0 < n; c0 += 32) {
-            int t = child_at(node, c0 + lane) ? __ldg(a.tokens + row0 + c0 + lane) : -1;
-            t = t >= v && t < v + 32 ? t : -1;
-            for (unsigned who = __ballot_sync(0xffffffffu, t >= 0); who; who &= who - 1)
-              if (__shfl_sync(0xffffffffu, t, __ffs(who) - 1) == v + lane) x = 0;
+      const int each = (w1 - w0 + VF_THREADS - 1) / VF_THREADS, i0 = min(w0 + tid * each, w1), i1 = min(i0 + each, w1);
+      const int lo = min(w0 + (tid & ~31) * each, w1), hi = min(lo + 32 * each, w1);  // of the warp
+      auto gone = [&](int v) {  // (whole warps) is v, within [lo, hi), a refused token?
+        bool is = false;
+        for (int c0 = node + 1; c0 < n; c0 += 32) {
+          int t = child_at(node, c0 + lane) ? token(c0 + lane) : -1;
+          t = t >= lo && t < hi ? t : -1;
+          for (unsigned who = __ballot_sync(0xffffffffu, t >= 0); who; who &= who - 1) is |= __shfl_sync(0xffffffffu, t, __ffs(who) - 1) == v;
+        }
+        return is;
+      };
+      uint64_t mine = 0;
+      for (int i = 0; i < each; ++i) {
+        const int v = i0 + i;
+        const bool out = without && gone(v);
+        if (v < i1 && !out) mine += left_of<DRAFT>(p, q, v, S);
+      }
+      const uint64_t upto = warp_upto(mine, lane);
+      __syncthreads();  // part[] has been read
+      if (lane == 31) part[warp] = upto;
+      __syncthreads();
+      uint64_t before = upto - mine;
+      for (int k = 0; k < warp; ++k) before += part[k];
+      const bool here = rest >= before && rest - before < mine;
+      if (__any_sync(0xffffffffu, here)) {
+        rest -= before;
+        bool open = here;
+        for (int i = 0; i < each; ++i) {
+          const int v = i0 + i;
+          const bool out = without && gone(v);
+          const uint64_t x = v < i1 && !out ? left_of<DRAFT>(p, q, v, S) : 0;
+          if (open && rest < x) {
+            out_tokens[s_count - 1] = v;
+            open = false;
           }
+          rest -= x;
         }
-        uint64_t upto = x;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint64_t y = __shfl_up_sync(0xffffffffu, upto, o);
-          if (lane >= o) upto += y;
-        }
-        const unsigned over = __ballot_sync(0xffffffffu, upto > rest);
-        if (over) {
-          if (lane == 0) out_tokens[s_count - 1] = v + __ffs(over) - 1;
-          return;
-        }
-        rest -= __shfl_sync(0xffffffffu, upto, 31);
       }
       return;
     }
@@ -238,7 +375,7 @@ __global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArg
     without = false;
     S = 0;
   }
-  if (tid == 0) out_tokens[s_count - 1] = -1;
+  if (writes && tid == 0) out_tokens[s_count - 1] = -1;
 }
 
 }  // namespace
@@ -270,8 +407,17 @@ extern "C" mt_status mt_tree_verify(const float* target, int64_t target_ld, cons
       if (ranges_overlap(outs[i], outs[j])) return MT_ERR_ALIAS;
   }
   if (T == 0) return MT_OK;
-  const VerifyArgs a = {target, draft, target_ld, draft_ld, V, tokens, parent, random, q_start, T, out_tokens, out_path, out_count, cols};
+  int derr = 0;
+  const DeviceInfo* di = device_info(&derr);
+  if (!di) return cuda_fail((cudaError_t)derr);
+  VerifyArgs a = {target, draft, target_ld, draft_ld, V, tokens, parent, random, q_start, T, out_tokens, out_path, out_count, cols, 1};
+  // as many blocks a sequence as the GPU holds at a time, two an SM, but no fewer
+  // than 2048 tokens each
+  while (a.blocks < 8 && B * a.blocks * 2 <= 2 * di->sm_count && V / (a.blocks * 2) >= 2048) a.blocks *= 2;
   const Launch l{(cudaStream_t)stream, mt_get_option(MT_OPT_PDL) != 0};
-  return draft ? launch(tree_verify_kernel<true>, dim3(B), dim3(VF_THREADS), 0, l, a)
-               : launch(tree_verify_kernel<false>, dim3(B), dim3(VF_THREADS), 0, l, a);
+  const dim3 grid(B * a.blocks);
+  auto go = [&](auto kernel) {
+    return a.blocks > 1 ? launch_cluster(kernel, a.blocks, grid, dim3(VF_THREADS), 0, l, a) : launch(kernel, grid, dim3(VF_THREADS), 0, l, a);
+  };
+  return draft ? go(tree_verify_kernel<true>) : go(tree_verify_kernel<false>);
 }
