@@ -15,7 +15,7 @@ namespace mt {
 
 namespace {
 
-constexpr int CK_THREADS = 256, CK_LAYERS = 64, CK_MOVES = 4;
+constexpr int CK_THREADS = 256, CK_LAYERS = 64, CK_MOVES = 4, CK_MANY = 4;
 
 struct KeepArgs {
   PagedArgs pg;  // of the first cache
@@ -23,12 +23,15 @@ struct KeepArgs {
   const int32_t* count;
   int cols;
   int32_t* new_len;
+  int layers;
   uint16_t* kv[CK_LAYERS][2];
 };
 
+// LAYERS layers a block, whose pages and places are looked up once.
+template <int LAYERS>
 __global__ void __launch_bounds__(CK_THREADS) cache_keep_kernel(const __grid_constant__ KeepArgs a) {
   const PagedArgs& pg = a.pg;
-  const int b = blockIdx.x, layer = blockIdx.y;
+  const int b = blockIdx.x, layer = blockIdx.y * LAYERS;
   pdl_wait();
   pdl_trigger();
   const PagedSeq s = paged_seq(pg, b);
@@ -37,7 +40,10 @@ __global__ void __launch_bounds__(CK_THREADS) cache_keep_kernel(const __grid_con
   const int chunks = pg.head_dim / 8, units = 2 * pg.kv_heads * chunks;
   for (int u = blockIdx.z * CK_THREADS + threadIdx.x; u < units; u += gridDim.z * CK_THREADS) {
     const int side = u / (pg.kv_heads * chunks), rest = u - side * pg.kv_heads * chunks, h = rest / chunks;
-    uint16_t* const kv = a.kv[layer][side] + (int64_t)h * pg.head_stride + 8 * (rest - h * chunks);
+    const int64_t column = (int64_t)h * pg.head_stride + 8 * (rest - h * chunks);
+    uint16_t* kv[LAYERS];
+#pragma unroll
+    for (int l = 0; l < LAYERS; ++l) kv[l] = a.kv[min(layer + l, a.layers - 1)][side] + column;
     auto place = [&](int pos) -> int64_t {  // of a token's row in the cache, or -1
       if (pos < 0) return -1;
       const int e = pos / pg.page_size, page = paged_entry(pg, b, e);
@@ -45,25 +51,32 @@ __global__ void __launch_bounds__(CK_THREADS) cache_keep_kernel(const __grid_con
     };
     int before = -1;
     for (int i0 = 0; i0 < most; i0 += CK_MOVES) {
-      uint4 x[CK_MOVES];
+      uint4 x[CK_MOVES][LAYERS];
       int64_t to[CK_MOVES];
       bool end = false;
+      int at[CK_MOVES];
+#pragma unroll
+      for (int q = 0; q < CK_MOVES; ++q) at[q] = i0 + q < most ? __ldg(path + i0 + q) : -1;
 #pragma unroll
       for (int q = 0; q < CK_MOVES; ++q) {
         to[q] = -1;
-        const int i = i0 + q;
-        const int at = i < most ? __ldg(path + i) : -1;
-        end |= at <= before || at >= s.n;
+        end |= at[q] <= before || at[q] >= s.n;
         if (end) continue;
-        before = at;
-        if (at == i) continue;
-        const int64_t from = place(base + at);
-        to[q] = from < 0 ? -1 : place(base + i);
-        if (to[q] >= 0) x[q] = *reinterpret_cast<const uint4*>(kv + from);
+        before = at[q];
+        if (at[q] == i0 + q) continue;
+        const int64_t from = place(base + at[q]);
+        to[q] = from < 0 ? -1 : place(base + i0 + q);
+        if (to[q] < 0) continue;
+#pragma unroll
+        for (int l = 0; l < LAYERS; ++l) x[q][l] = *reinterpret_cast<const uint4*>(kv[l] + from);
       }
 #pragma unroll
-      for (int q = 0; q < CK_MOVES; ++q)
-        if (to[q] >= 0) *reinterpret_cast<uint4*>(kv + to[q]) = x[q];
+      for (int q = 0; q < CK_MOVES; ++q) {
+        if (to[q] < 0) continue;
+#pragma unroll
+        for (int l = 0; l < LAYERS; ++l)
+          if (layer + l < a.layers) *reinterpret_cast<uint4*>(kv[l] + to[q]) = x[q][l];
+      }
       if (end) break;
     }
   }
@@ -113,6 +126,9 @@ extern "C" mt_status mt_cache_keep(const mt_paged_cache* caches, int L, const mt
       for (const ByteRange& r : ins)
         if (ranges_overlap(r, rc)) return MT_ERR_ALIAS;
     }
+  int derr = 0;
+  const DeviceInfo* di = device_info(&derr);
+  if (!di) return cuda_fail((cudaError_t)derr);
   a.pg.err = device_error_ptr();
   if (!a.pg.err) return MT_ERR_CUDA;
   a.path = path;
@@ -121,14 +137,19 @@ extern "C" mt_status mt_cache_keep(const mt_paged_cache* caches, int L, const mt
   const Launch l{(cudaStream_t)stream, mt_get_option(MT_OPT_PDL) != 0};
   const int units = 2 * a.pg.kv_heads * (a.pg.head_dim / 8);
   for (int i = 0; i < L; i += CK_LAYERS) {
-    const int layers = std::min(CK_LAYERS, L - i);
+    a.layers = std::min(CK_LAYERS, L - i);
     a.new_len = i == 0 ? new_len : nullptr;
-    for (int j = 0; j < layers; ++j) {
+    for (int j = 0; j < a.layers; ++j) {
       a.kv[j][0] = (uint16_t*)caches[i + j].k;
       a.kv[j][1] = (uint16_t*)caches[i + j].v;
     }
-    const dim3 grid(batch->B, layers, (units + CK_THREADS - 1) / CK_THREADS);
-    if (const mt_status st = launch(cache_keep_kernel, grid, dim3(CK_THREADS), 0, l, a)) return st;
+    // one layer a block for few texts, several where there are blocks enough
+    const int parts = (units + CK_THREADS - 1) / CK_THREADS;
+    const bool many = (int64_t)batch->B * a.layers * parts > 8 * (int64_t)di->sm_count;
+    const dim3 grid(batch->B, many ? (a.layers + CK_MANY - 1) / CK_MANY : a.layers, parts);
+    const mt_status st = many ? launch(cache_keep_kernel<CK_MANY>, grid, dim3(CK_THREADS), 0, l, a)
+                              : launch(cache_keep_kernel<1>, grid, dim3(CK_THREADS), 0, l, a);
+    if (st) return st;
   }
   return MT_OK;
 }
