@@ -756,12 +756,14 @@ mt_status mt_tree_verify(const float* target, int64_t target_ld, const float* dr
 
 /*
  * Moves the keys and values of the new tokens path[b][0 .. count[b]) of every
- * sequence together, in each of L caches: the token at kv_len - n + path[b][i]
+ * sequence together, in the caches of L layers: the token at kv_len - n + path[b][i]
  * goes to kv_len - n + i, and
  *   new_len[b] = kv_len - n + (tokens kept)
  * is the sequence's length from then on.  What lies behind stays as it was.
- *   caches    : host array of L caches (read during the call) of the same
- *               strides and sizes; no two share an element
+ *   cache     : the strides and sizes of all L caches (its k and v are not read)
+ *   layers    : host array [L][2] of the caches' k and v (read during the call),
+ *               device pointers, 16-byte aligned; no two of the 2 L share an
+ *               element
  *   batch     : q_start, kv_len, pages as in mt_paged_attention
  *   path      : int32 [B][cols], each row increasing from an index >= 0 (as
  *               mt_tree_verify writes it); a row ends at the first index that is
@@ -773,9 +775,9 @@ mt_status mt_tree_verify(const float* target, int64_t target_ld, const float* dr
  * Limits: 1 <= L <= 1024; 1 <= cols <= 2^20; pointers 4-byte aligned; the
  *         caches' rows may not share elements, as in mt_rope_append.
  */
-mt_status mt_cache_keep(const mt_paged_cache* caches, int L, const mt_paged_batch* batch,
-                        const int32_t* path, const int32_t* count, int cols, int32_t* new_len,
-                        void* stream);
+mt_status mt_cache_keep(const mt_paged_cache* cache, void* const* layers, int L,
+                        const mt_paged_batch* batch, const int32_t* path, const int32_t* count, int cols,
+                        int32_t* new_len, void* stream);
 
 /* Library options.  Returns MT_ERR_FORMAT for an unknown option. */
 mt_status mt_set_option(mt_option opt, int value);

@@ -15,7 +15,7 @@ namespace mt {
 
 namespace {
 
-constexpr int CK_THREADS = 256, CK_LAYERS = 64, CK_MOVES = 4, CK_MANY = 4;
+constexpr int CK_THREADS = 256, CK_LAYERS = 64, CK_MANY = 4;
 
 struct KeepArgs {
   PagedArgs pg;  // of the first cache
@@ -29,7 +29,8 @@ struct KeepArgs {
 
 // LAYERS layers a block, whose pages and places are looked up once.
 template <int LAYERS>
-__global__ void __launch_bounds__(CK_THREADS) cache_keep_kernel(const __grid_constant__ KeepArgs a) {
+__global__ void __launch_bounds__(CK_THREADS, LAYERS > 1 ? 4 : 1) cache_keep_kernel(const __grid_constant__ KeepArgs a) {
+  constexpr int MOVES = LAYERS > 1 ? 2 : 4;  // tokens whose loads are in flight together
   const PagedArgs& pg = a.pg;
   const int b = blockIdx.x, layer = blockIdx.y * LAYERS;
   pdl_wait();
@@ -50,15 +51,15 @@ __global__ void __launch_bounds__(CK_THREADS) cache_keep_kernel(const __grid_con
       return page < 0 ? -1 : (int64_t)page * pg.page_stride + (int64_t)(pos - e * pg.page_size) * pg.token_stride;
     };
     int before = -1;
-    for (int i0 = 0; i0 < most; i0 += CK_MOVES) {
-      uint4 x[CK_MOVES][LAYERS];
-      int64_t to[CK_MOVES];
+    for (int i0 = 0; i0 < most; i0 += MOVES) {
+      uint4 x[MOVES][LAYERS];
+      int64_t to[MOVES];
       bool end = false;
-      int at[CK_MOVES];
+      int at[MOVES];
 #pragma unroll
-      for (int q = 0; q < CK_MOVES; ++q) at[q] = i0 + q < most ? __ldg(path + i0 + q) : -1;
+      for (int q = 0; q < MOVES; ++q) at[q] = i0 + q < most ? __ldg(path + i0 + q) : -1;
 #pragma unroll
-      for (int q = 0; q < CK_MOVES; ++q) {
+      for (int q = 0; q < MOVES; ++q) {
         to[q] = -1;
         end |= at[q] <= before || at[q] >= s.n;
         if (end) continue;
@@ -71,7 +72,7 @@ __global__ void __launch_bounds__(CK_THREADS) cache_keep_kernel(const __grid_con
         for (int l = 0; l < LAYERS; ++l) x[q][l] = *reinterpret_cast<const uint4*>(kv[l] + from);
       }
 #pragma unroll
-      for (int q = 0; q < CK_MOVES; ++q) {
+      for (int q = 0; q < MOVES; ++q) {
         if (to[q] < 0) continue;
 #pragma unroll
         for (int l = 0; l < LAYERS; ++l)
@@ -97,35 +98,35 @@ __global__ void __launch_bounds__(CK_THREADS) cache_keep_kernel(const __grid_con
 
 using namespace mt;
 
-extern "C" mt_status mt_cache_keep(const mt_paged_cache* caches, int L, const mt_paged_batch* batch, const int32_t* path,
-                                   const int32_t* count, int cols, int32_t* new_len, void* stream) {
-  if (!caches || !batch || !path || !count) return MT_ERR_NULL;
+extern "C" mt_status mt_cache_keep(const mt_paged_cache* cache, void* const* layers, int L, const mt_paged_batch* batch,
+                                   const int32_t* path, const int32_t* count, int cols, int32_t* new_len, void* stream) {
+  if (!cache || !layers || !batch || !path || !count) return MT_ERR_NULL;
   if (L < 1 || L > PG_MAX_LAYERS || cols < 1 || cols > (1 << 20)) return MT_ERR_SHAPE;
+  for (int i = 0; i < 2 * L; ++i)
+    if (!layers[i]) return MT_ERR_NULL;
+  mt_paged_cache c = *cache;
+  c.k = layers[0];
+  c.v = layers[1];
   KeepArgs a = {};
-  for (int i = L - 1; i >= 0; --i) {
-    const mt_paged_cache &c = caches[i], &f = caches[0];
-    if (const mt_status st = paged_args(&c, batch, &a.pg)) return st;
-    if (c.page_stride != f.page_stride || c.token_stride != f.token_stride || c.head_stride != f.head_stride ||
-        c.num_pages != f.num_pages || c.page_size != f.page_size || c.kv_heads != f.kv_heads || c.head_dim != f.head_dim)
-      return MT_ERR_SHAPE;
-  }
+  if (const mt_status st = paged_args(&c, batch, &a.pg)) return st;
+  for (int i = 0; i < 2 * L; ++i)
+    if (!aligned_to(layers[i], 16)) return MT_ERR_ALIGN;
   if (!aligned_to(path, 4) || !aligned_to(count, 4) || !aligned_to(new_len, 4)) return MT_ERR_ALIGN;
-  if (!paged_rows_apart(&caches[0])) return MT_ERR_SHAPE;
-  if (!paged_layers_apart(caches, L)) return MT_ERR_ALIAS;
-  const size_t bytes = paged_cache_bytes(&caches[0]);
+  if (!paged_rows_apart(&c)) return MT_ERR_SHAPE;
+  if (!paged_layers_apart(&c, layers, L)) return MT_ERR_ALIAS;
+  const size_t bytes = paged_cache_bytes(&c);
   const ByteRange ins[] = {byte_range(batch->q_start, (size_t)(batch->B + 1) * 4), byte_range(batch->kv_len, (size_t)batch->B * 4),
                            byte_range(batch->pages, (size_t)((batch->B - 1) * batch->pages_ld + batch->max_pages) * 4),
                            byte_range(path, (size_t)batch->B * cols * 4), byte_range(count, (size_t)batch->B * 4)};
   const ByteRange rn = byte_range(new_len, (size_t)batch->B * 4);
   for (const ByteRange& r : ins)
     if (ranges_overlap(r, rn)) return MT_ERR_ALIAS;
-  for (int i = 0; i < L; ++i)
-    for (const void* p : {caches[i].k, caches[i].v}) {
-      const ByteRange rc = byte_range(p, bytes);
-      if (ranges_overlap(rc, rn)) return MT_ERR_ALIAS;
-      for (const ByteRange& r : ins)
-        if (ranges_overlap(r, rc)) return MT_ERR_ALIAS;
-    }
+  for (int i = 0; i < 2 * L; ++i) {
+    const ByteRange rc = byte_range(layers[i], bytes);
+    if (ranges_overlap(rc, rn)) return MT_ERR_ALIAS;
+    for (const ByteRange& r : ins)
+      if (ranges_overlap(r, rc)) return MT_ERR_ALIAS;
+  }
   int derr = 0;
   const DeviceInfo* di = device_info(&derr);
   if (!di) return cuda_fail((cudaError_t)derr);
@@ -140,8 +141,8 @@ extern "C" mt_status mt_cache_keep(const mt_paged_cache* caches, int L, const mt
     a.layers = std::min(CK_LAYERS, L - i);
     a.new_len = i == 0 ? new_len : nullptr;
     for (int j = 0; j < a.layers; ++j) {
-      a.kv[j][0] = (uint16_t*)caches[i + j].k;
-      a.kv[j][1] = (uint16_t*)caches[i + j].v;
+      a.kv[j][0] = (uint16_t*)layers[2 * (i + j)];
+      a.kv[j][1] = (uint16_t*)layers[2 * (i + j) + 1];
     }
     // one layer a block for few texts, several where there are blocks enough
     const int parts = (units + CK_THREADS - 1) / CK_THREADS;

@@ -62,13 +62,10 @@ bool paged_kv_apart(const mt_paged_cache* c) {
   return !rows_meet(((int64_t)(uintptr_t)c->v - (int64_t)(uintptr_t)c->k) / 2, d, n, c->head_dim);
 }
 
-bool paged_layers_apart(const mt_paged_cache* c, int L) {
+bool paged_layers_apart(const mt_paged_cache* c, void* const* layers, int L) {
   const int64_t bytes = (int64_t)paged_cache_bytes(c);
   int64_t at[2 * PG_MAX_LAYERS];
-  for (int i = 0; i < L; ++i) {
-    at[2 * i] = (int64_t)(uintptr_t)c[i].k;
-    at[2 * i + 1] = (int64_t)(uintptr_t)c[i].v;
-  }
+  for (int i = 0; i < 2 * L; ++i) at[i] = (int64_t)(uintptr_t)layers[i];
   std::sort(at, at + 2 * L);
   Dim d[3];
   const int n = cache_dims(c, d);

@@ -61,9 +61,9 @@ mt_status paged_args(const mt_paged_cache* c, const mt_paged_batch* b, PagedArgs
 bool paged_rows_apart(const mt_paged_cache* c);
 // Whether no row of K shares an element with one of V; rows apart only.
 bool paged_kv_apart(const mt_paged_cache* c);
-// Whether no two of the K and V of L caches of equal strides and sizes share an
-// element; rows apart and L <= PG_MAX_LAYERS only.
-bool paged_layers_apart(const mt_paged_cache* c, int L);
+// Whether no two of the K and V of L caches of c's strides and sizes, at layers[0
+// .. 2 L), share an element; rows apart and L <= PG_MAX_LAYERS only.
+bool paged_layers_apart(const mt_paged_cache* c, void* const* layers, int L);
 // Bytes from a cache pointer to the end of its last element.
 size_t paged_cache_bytes(const mt_paged_cache* c);
 

@@ -152,30 +152,34 @@ __global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArg
   const int per = ((b1 - b0 + VF_WARPS - 1) / VF_WARPS + 31) & ~31;
   const int v0 = min(b0 + warp * per, b1), v1 = min(v0 + per, b1);
   const bool fours = ((uintptr_t)a.target & 15) == 0 && a.target_ld % 4 == 0 && (!DRAFT || (((uintptr_t)a.draft & 15) == 0 && a.draft_ld % 4 == 0));
+  // the fours of a stretch: left(x, y) is what y leaves of x
+  auto sum_fours = [&](const float* p, const float* q, auto left) {
+    uint64_t sum = 0;
+    constexpr int F = 4;
+#pragma unroll 1
+    for (int v = v0 + 4 * lane; v + 4 <= v1; v += 128 * F) {
+      float4 x[F], y[F];
+#pragma unroll
+      for (int i = 0; i < F; ++i) {
+        const bool in = v + 128 * i + 4 <= v1;
+        x[i] = in ? __ldg(reinterpret_cast<const float4*>(p + v + 128 * i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        y[i] = in && q ? __ldg(reinterpret_cast<const float4*>(q + v + 128 * i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int i = 0; i < F; ++i)
+        sum += (left(x[i].x, y[i].x) + left(x[i].y, y[i].y)) + (left(x[i].z, y[i].z) + left(x[i].w, y[i].w));
+    }
+    return sum;
+  };
   auto sum_stretch = [&](int node, uint64_t S) {
     const float* p = target(node);
     const float* q = draft(node);
     uint64_t sum = 0;
     int v = v0 + lane;
     if (fours) {
-      auto add = [&](float x, float y) { sum += DRAFT && S ? less(steps(x), times(S, steps(y))) : steps(x); };
-      constexpr int F = 4;
-      for (v = v0 + 4 * lane; v + 4 <= v1; v += 128 * F) {
-        float4 x[F], y[F];
-#pragma unroll
-        for (int i = 0; i < F; ++i) {
-          const bool in = v + 128 * i + 4 <= v1;
-          x[i] = in ? __ldg(reinterpret_cast<const float4*>(p + v + 128 * i)) : make_float4(0.f, 0.f, 0.f, 0.f);
-          if (DRAFT) y[i] = in && S ? __ldg(reinterpret_cast<const float4*>(q + v + 128 * i)) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll
-        for (int i = 0; i < F; ++i) {
-          add(x[i].x, DRAFT ? y[i].x : 0.f);
-          add(x[i].y, DRAFT ? y[i].y : 0.f);
-          add(x[i].z, DRAFT ? y[i].z : 0.f);
-          add(x[i].w, DRAFT ? y[i].w : 0.f);
-        }
-      }
+      if (!DRAFT || S == 0) sum = sum_fours(p, nullptr, [](float x, float) { return steps(x); });
+      else if (S == VF_ONE) sum = sum_fours(p, q, [](float x, float y) { return less(steps(x), steps(y)); });  // one refused, all there are in a chain
+      else sum = sum_fours(p, q, [&](float x, float y) { return less(steps(x), times(S, steps(y))); });
       v = v1 - (v1 - v0) % 4 + lane;  // a stretch starts on a multiple of 32
     }
 #pragma unroll 4

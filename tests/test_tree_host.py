@@ -50,9 +50,10 @@ def keep(mt, caches=None, b=None, **kw):
     d = dict(path=A(5), count=A(6), cols=4, new_len=A(7))
     d.update(kw)
     caches = caches if caches is not None else [cache(mt), cache(mt, k=A(10), v=A(11))]
-    arr = (mt.PagedCache * max(1, len(caches)))(*caches)
-    return mt.raw("mt_cache_keep")(arr if caches else None, kw.get("L", len(caches)), ctypes.byref(b or batch(mt)), d["path"], d["count"],
-                                   d["cols"], d["new_len"], None)
+    arr = (ctypes.c_void_p * max(1, 2 * len(caches)))(*[p for c in caches for p in (c.k, c.v)])
+    shape = caches[0] if caches else cache(mt)
+    return mt.raw("mt_cache_keep")(ctypes.byref(shape), arr if caches else None, kw.get("L", len(caches)), ctypes.byref(b or batch(mt)),
+                                   d["path"], d["count"], d["cols"], d["new_len"], None)
 
 
 def test_cache_and_batch_refusals(mt):
@@ -112,10 +113,10 @@ def test_keep_refusals(mt, kw, want):
     assert keep(mt, **kw) == want
 
 
-def test_caches_that_share_elements_or_differ(mt):
+def test_caches_that_share_elements(mt):
     two = cache(mt, k=A(10), v=A(11))
-    assert keep(mt, [cache(mt), cache(mt, k=A(10), v=A(11), token_stride=136, page_stride=16 * 136)]) == SHAPE
-    assert keep(mt, [cache(mt), two, cache(mt, k=A(12), v=A(13), num_pages=9)]) == SHAPE
+    assert keep(mt, [cache(mt), two, cache(mt, k=None, v=A(12))]) == NULL
+    assert keep(mt, [cache(mt), cache(mt, k=A(10), v=A(11) + 8)]) == ALIGN
     assert keep(mt, [cache(mt), two, cache(mt, k=A(12), v=A(10))]) == ALIAS        # a layer's values are another's keys
     assert keep(mt, [cache(mt), two, two]) == ALIAS
     assert keep(mt, [cache(mt), cache(mt, k=A(10), v=A(1) + 16)]) == ALIAS
