@@ -54,16 +54,50 @@ struct VerifyArgs {
   int blocks;  // of a sequence
 };
 
+// Two floats p in [-1, 1] as integers of steps: p = A 2^-20 + B 2^-40 + C 2^-56,
+// each the nearest integer to what the ones before leave (exactly, as p has 24
+// bits).  In [8, 16) floats are 2^-20 apart, so that p + 12 rounds p to such steps
+// and their number is the difference of the sum's bits and 12's; likewise B from
+// [2^-17, 2^-16) and C from [2^-33, 2^-32).  (A conversion to 64 bits runs on the
+// FP64 pipe, which kept 64 chains at 43 us; with these 23.)
+struct Steps {
+  uint32_t a, b, c;  // sums of A, B and C
+};
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) { return add2(a, b ^ 0x8000000080000000ull); }
+// The sum of the two words' integers, less the magic number's bits twice.
+__device__ __forceinline__ uint32_t bits2(uint64_t y, uint32_t magic) { return (uint32_t)y + (uint32_t)(y >> 32) - 2u * magic; }
+__device__ __forceinline__ void add_steps(Steps& s, float p0, float p1) {
+  constexpr uint32_t M1 = 0x41400000u, M2 = 0x37400000u, M3 = 0x2F400000u;  // 12, 1.5 2^-17, 1.5 2^-33
+  constexpr uint64_t TWO = 0x100000001ull;
+  const uint64_t p = pack2(p0, p1);
+  const uint64_t y1 = add2(p, M1 * TWO), r1 = sub2(p, sub2(y1, M1 * TWO));
+  const uint64_t y2 = add2(r1, M2 * TWO), r2 = sub2(r1, sub2(y2, M2 * TWO));
+  const uint64_t y3 = add2(r2, M3 * TWO);
+  s.a += bits2(y1, M1);
+  s.b += bits2(y2, M2);
+  s.c += bits2(y3, M3);
+}
+__device__ __forceinline__ uint64_t whole(const Steps& s) {
+  return (uint64_t)((int64_t)(int32_t)s.a << 36) + (uint64_t)((int64_t)(int32_t)s.b << 16) + (uint64_t)(int64_t)(int32_t)s.c;
+}
 // A probability in steps of 2^-56: above 1 as 1, below 0 and NaN as 0.
 __device__ __forceinline__ uint64_t steps(float p) {
-  p = fminf(fmaxf(p, 0.f), 1.f);  // NaN: 0
-  return __float2ull_rn(p * 72057594037927936.f);
+  Steps s = {0, 0, 0};
+  add_steps(s, __saturatef(p), 0.f);
+  return whole(s);
 }
-// A random number in steps of 2^-64, below 1.
-__device__ __forceinline__ uint64_t chance(float u) {
-  u = fminf(fmaxf(u, 0.f), 0.99999994f);
-  return __float2ull_rz(u * 9223372036854775808.f) << 1;
-}
+// A random number in steps of 2^-64 (whole ones of 2^-56), below 1.
+__device__ __forceinline__ uint64_t chance(float u) { return steps(fminf(__saturatef(u), 0.99999994f)) << 8; }
 // a b for numbers in steps of 2^-56, cut to a step.
 __device__ __forceinline__ uint64_t times(uint64_t a, uint64_t b) { return (__umul64hi(a, b) << 8) | ((a * b) >> 56); }
 __device__ __forceinline__ uint64_t less(uint64_t a, uint64_t b) { return a > b ? a - b : 0; }
@@ -93,7 +127,7 @@ __device__ __forceinline__ uint64_t warp_upto(uint64_t x, int lane) {
 template <bool DRAFT>
 __global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArgs a) {
   __shared__ int32_t t_parent[VF_TREE], t_token[VF_TREE];
-  __shared__ float t_random[VF_TREE], t_p[VF_TREE], t_q[DRAFT ? VF_TREE : 1];
+  __shared__ uint64_t t_random[VF_TREE], t_p[VF_TREE], t_q[DRAFT ? VF_TREE : 1];  // in steps
   __shared__ uint64_t part[VF_WARPS];  // sums of each warp's stretch of this block's share of the vocabulary
   __shared__ uint64_t share[2][16];    // of each block's share, in turn
   __shared__ uint64_t s_S, s_U;
@@ -122,11 +156,11 @@ __global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArg
   for (int i = tid; i < min(n, VF_TREE); i += VF_THREADS) {
     const int up = __ldg(a.parent + row0 + i), x = __ldg(a.tokens + row0 + i);
     const bool in = up >= 0 && up < i && x >= 0 && x < V;
-    t_random[i] = __ldg(a.random + row0 + i);
+    t_random[i] = chance(__ldg(a.random + row0 + i));
     t_parent[i] = up;
     t_token[i] = x;
-    t_p[i] = in ? __ldg(target(up) + x) : 0.f;
-    if (DRAFT) t_q[i] = in ? __ldg(draft(up) + x) : 0.f;
+    t_p[i] = in ? steps(__ldg(target(up) + x)) : 0;
+    if (DRAFT) t_q[i] = in ? steps(__ldg(draft(up) + x)) : 0;
   }
   __syncthreads();
   auto parent = [&](int i) { return i < VF_TREE ? t_parent[i] : __ldg(a.parent + row0 + i); };
@@ -152,10 +186,12 @@ __global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArg
   const int per = ((b1 - b0 + VF_WARPS - 1) / VF_WARPS + 31) & ~31;
   const int v0 = min(b0 + warp * per, b1), v1 = min(v0 + per, b1);
   const bool fours = ((uintptr_t)a.target & 15) == 0 && a.target_ld % 4 == 0 && (!DRAFT || (((uintptr_t)a.draft & 15) == 0 && a.draft_ld % 4 == 0));
-  // the fours of a stretch: left(x, y) is what y leaves of x
-  auto sum_fours = [&](const float* p, const float* q, auto left) {
+  // The sum of a stretch's fours: of p, or of what q leaves of it.  (Loads in
+  // flight a thread: with half and twice as many of p and q, 64 chains take 23.2
+  // and 25.4 us in place of 24.4.)
+  auto sum_fours = [&](const float* p, const float* q, auto add) {
     uint64_t sum = 0;
-    constexpr int F = 4;
+    constexpr int F = DRAFT ? 2 : 8;
 #pragma unroll 1
     for (int v = v0 + 4 * lane; v + 4 <= v1; v += 128 * F) {
       float4 x[F], y[F];
@@ -163,11 +199,9 @@ __global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArg
       for (int i = 0; i < F; ++i) {
         const bool in = v + 128 * i + 4 <= v1;
         x[i] = in ? __ldg(reinterpret_cast<const float4*>(p + v + 128 * i)) : make_float4(0.f, 0.f, 0.f, 0.f);
-        y[i] = in && q ? __ldg(reinterpret_cast<const float4*>(q + v + 128 * i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (DRAFT) y[i] = in && q ? __ldg(reinterpret_cast<const float4*>(q + v + 128 * i)) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
-#pragma unroll
-      for (int i = 0; i < F; ++i)
-        sum += (left(x[i].x, y[i].x) + left(x[i].y, y[i].y)) + (left(x[i].z, y[i].z) + left(x[i].w, y[i].w));
+      sum += add(x, y);
     }
     return sum;
   };
@@ -176,10 +210,36 @@ __global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArg
     const float* q = draft(node);
     uint64_t sum = 0;
     int v = v0 + lane;
-    if (fours) {
-      if (!DRAFT || S == 0) sum = sum_fours(p, nullptr, [](float x, float) { return steps(x); });
-      else if (S == VF_ONE) sum = sum_fours(p, q, [](float x, float y) { return less(steps(x), steps(y)); });  // one refused, all there are in a chain
-      else sum = sum_fours(p, q, [&](float x, float y) { return less(steps(x), times(S, steps(y))); });
+    if (fours && (!DRAFT || S == 0 || S == VF_ONE)) {
+      if (!DRAFT || S == 0) {
+        sum = sum_fours(p, nullptr, [](const auto& x, const auto&) {
+          Steps s = {0, 0, 0};
+#pragma unroll
+          for (const float4& f : x) {
+            add_steps(s, __saturatef(f.x), __saturatef(f.y));
+            add_steps(s, __saturatef(f.z), __saturatef(f.w));
+          }
+          return whole(s);
+        });
+      } else {
+        // one refused, as in every chain: p - q where that is positive
+        sum = sum_fours(p, q, [](const auto& x, const auto& y) {
+          Steps s = {0, 0, 0};
+          auto one = [&](float x, float y) {
+            x = __saturatef(x);
+            y = __saturatef(y);
+            add_steps(s, x > y ? x : 0.f, x > y ? -y : 0.f);
+          };
+#pragma unroll
+          for (int i = 0; i < (int)(sizeof(x) / sizeof(x[0])); ++i) {
+            one(x[i].x, y[i].x);
+            one(x[i].y, y[i].y);
+            one(x[i].z, y[i].z);
+            one(x[i].w, y[i].w);
+          }
+          return whole(s);
+        });
+      }
       v = v1 - (v1 - v0) % 4 + lane;  // a stretch starts on a multiple of 32
     }
 #pragma unroll 4
@@ -235,19 +295,23 @@ __global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArg
         if (!kids) continue;
         const int x = child ? token(c) : -1;
         const bool in = x >= 0 && x < V;
-        const uint64_t U = child ? chance(c < VF_TREE ? t_random[c] : __ldg(a.random + row0 + c)) : 0;
-        const uint64_t p = in ? steps(c < VF_TREE ? t_p[c] : __ldg(target(node) + x)) : 0;
+        const uint64_t U = !child ? 0 : c < VF_TREE ? t_random[c] : chance(__ldg(a.random + row0 + c));
+        const uint64_t p = !in ? 0 : c < VF_TREE ? t_p[c] : steps(__ldg(target(node) + x));
         if (!DRAFT) {
           // all of them at once: R is down by the earlier ones' shares
-          const uint64_t r = said_before(node, c0, child, x) ? 0 : p;
-          const uint64_t upto = warp_upto(r, lane);
+          const bool several = refused || (kids & (kids - 1)) != 0;
+          const uint64_t r = several && said_before(node, c0, child, x) ? 0 : p;
+          const uint64_t upto = several ? warp_upto(r, lane) : r;
           const unsigned taken = __ballot_sync(0xffffffffu, child && __umul64hi(less(R, upto - r), U) < r);
-          if (taken) next = c0 + __ffs(taken) - 1;
-          R = less(R, __shfl_sync(0xffffffffu, upto, 31));
-          refused = true;
+          if (taken) {
+            next = c0 + __ffs(taken) - 1;
+          } else {
+            R = less(R, __shfl_sync(0xffffffffu, upto, 31 - __clz(kids)));  // upto the last of them
+            refused = true;
+          }
           continue;
         }
-        const uint64_t q = in ? steps(c < VF_TREE ? t_q[DRAFT ? c : 0] : __ldg(draft(node) + x)) : 0;
+        const uint64_t q = !in ? 0 : c < VF_TREE ? t_q[DRAFT ? c : 0] : steps(__ldg(draft(node) + x));
         for (; kids; kids &= kids - 1) {
           if (!known) {
             if (lane == 0) {
@@ -282,7 +346,7 @@ __global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArg
       s_more = 0;
       s_refused = refused;
       s_count = count;
-      s_U = chance(t_random[0]);
+      s_U = t_random[0];
       if (writes) a.out_count[b] = count;
     }
     if (writes)
@@ -312,7 +376,7 @@ __global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArg
         const int x = child ? token(c) : -1;
         const bool again = said_before(node, c0, child, x);
         if (child && !again && x >= b0 && x < b1) {
-          const uint64_t p = steps(c < VF_TREE ? t_p[c] : __ldg(target(node) + x));
+          const uint64_t p = c < VF_TREE ? t_p[c] : steps(__ldg(target(node) + x));
           atomicAdd(reinterpret_cast<unsigned long long*>(&part[(x - b0) / per]), (unsigned long long)(0ull - p));
         }
       }
