@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArg
     const float* q = draft(node);
     uint64_t sum = 0;
     int v = v0 + lane;
-    if (fours && (!DRAFT || S == 0 || S == VF_ONE)) {
+    if (fours) {
       if (!DRAFT || S == 0) {
         sum = sum_fours(p, nullptr, [](const auto& x, const auto&) {
           Steps s = {0, 0, 0};
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArg
           }
           return whole(s);
         });
-      } else {
+      } else if (S == VF_ONE) {
         // one refused, as in every chain: p - q where that is positive
         sum = sum_fours(p, q, [](const auto& x, const auto& y) {
           Steps s = {0, 0, 0};
@@ -238,6 +238,19 @@ __global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArg
             one(x[i].w, y[i].w);
           }
           return whole(s);
+        });
+      } else {
+        sum = sum_fours(p, q, [&](const auto& x, const auto& y) {
+          uint64_t s = 0;
+          auto one = [&](float x, float y) { s += less(steps(x), times(S, steps(y))); };
+#pragma unroll
+          for (int i = 0; i < (int)(sizeof(x) / sizeof(x[0])); ++i) {
+            one(x[i].x, y[i].x);
+            one(x[i].y, y[i].y);
+            one(x[i].z, y[i].z);
+            one(x[i].w, y[i].w);
+          }
+          return s;
         });
       }
       v = v1 - (v1 - v0) % 4 + lane;  // a stretch starts on a multiple of 32
