@@ -3,16 +3,20 @@
 //
 //   p = e / sum e,  e = exp((x - max x) / t);  t <= 0: 1 at the first largest.
 //
-// Bound: memory, each logit read and each probability written once.  A row lies
-// in the registers of a cluster of up to eight blocks, 8 K logits a thread, so
-// that it is read once; each block takes its exponentials from its own largest
-// logit, and the blocks' largest logits, sums and first places meet in one
-// exchange through distributed shared memory, after which a block's share is
-// scaled by 2^((its largest - the row's) c).
+// Bound: memory, each logit read and each probability written once; the
+// instructions come near it, so that everything is done on two floats at a time.
+// A cluster of up to eight blocks shares out a row; its blocks' largest logits,
+// sums and first places meet in one exchange through distributed shared memory.
+//  * Few rows (token_probs_kernel): the row lies in the blocks' registers, 8 K
+//    logits a thread.  9 rows of 151 936 fp32 logits take 6.5 us.
+//  * Many (token_probs_loop_kernel): a block passes over its share with a running
+//    maximum and sum, and over it again, from L2, for the output: nothing but one
+//    exchange stands between the loads and the stores.  448 rows of 128 256 bf16
+//    logits: LOOP_US.  (The first kernel: 100; with clusters that stay and the next
+//    row's logits on their way 76, most of it waiting between the steps of a row.)
 #include <math.h>
 
 #include <algorithm>
-#include <atomic>
 
 #include "k_cluster.cuh"
 #include "k_paged.cuh"
@@ -21,7 +25,7 @@ namespace mt {
 
 namespace {
 
-constexpr int PB_THREADS = 512, PB_MOST = 5;  // threads of a block, most vectors of 8 logits of one
+constexpr int PB_THREADS = 512, PB_WARPS = PB_THREADS / 32, PB_MOST = 5;  // most vectors of 8 logits of a thread's registers
 
 struct ProbArgs {
   const char* in;
@@ -29,8 +33,7 @@ struct ProbArgs {
   int64_t in_ld, out_ld;
   int V;
   const float* temperature;
-  int R;
-  int blocks, log2_blocks;  // of a row
+  int R, blocks;  // blocks of a row
 };
 
 // 1 / t in units of log2 e, as a sum of two floats: the exponent's argument is
@@ -61,19 +64,6 @@ __device__ __forceinline__ float exp_scaled(float x, float top, Scale c) {
   const float y = d * c.hi;
   const float rest = fmaf(d, c.hi, -y) + d * c.lo;  // what y's rounding left
   return y < -160.f ? 0.f : exp2f(y) * fmaf(rest, 0.693147182f, 1.f);
-}
-
-// The same without results below 2^-126, for parts of a row: 2^((x - top) c) for
-// x <= top, 0 for x = -inf.
-__device__ __forceinline__ float ex2_ftz(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float exp_part(float x, float top, Scale c) {
-  if (c.flat) return x > -INFINITY ? 1.f : 0.f;
-  const float d = x - top, y = d * c.hi, rest = fmaf(d, c.lo, fmaf(d, c.hi, -y));
-  return y > -126.f ? ex2_ftz(y) * fmaf(rest, 0.693147182f, 1.f) : 0.f;
 }
 
 template <bool F32>
@@ -140,366 +130,415 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
                : "memory");
 }
 
-template <bool F32, int K, int T>
-__global__ void __launch_bounds__(T, T <= 512 ? 2 : 1) token_probs_kernel(const ProbArgs a) {
-  constexpr int W = T / 32, ES = F32 ? 4 : 2, Q = F32 ? 2 : 1;  // Q: 16-byte pieces of a vector
-  extern __shared__ __align__(16) uint4 next[];                  // [K][Q][T]: each thread's vectors of the next row
-  __shared__ uint64_t tell[2][8 * W];  // of each warp of the row, in turn: its largest logit, and its sum or that logit's place
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, C = a.blocks, V = a.V;
-  const int rank = C > 1 ? (int)cluster_rank() : 0, clusters = gridDim.x / C;
+__device__ __forceinline__ float ex2_ftz(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Eight consecutive probabilities; `mis`: floats past a 32-byte boundary.
+__device__ __forceinline__ void put8(float* to, int mis, const float (&y)[8]) {
+  if (mis == 0) {
+    store8(to, y);
+  } else if (mis == 4) {
+    reinterpret_cast<float4*>(to)[0] = make_float4(y[0], y[1], y[2], y[3]);
+    reinterpret_cast<float4*>(to)[1] = make_float4(y[4], y[5], y[6], y[7]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) to[i] = y[i];
+  }
+}
+
+// Pairs of 2^(40 + (x - base) c), x <= base: so that what lies below 2^-126 of the
+// largest stays normal.
+struct Exp2 {
+  uint64_t hi, lo;
+  float low, c_hi;  // d as small as 2^-200 needs stands for all that is less, -inf too
+  __device__ __forceinline__ explicit Exp2(const Scale& c) : hi(pack2(c.hi, c.hi)), lo(pack2(c.lo, c.lo)), low(-200.f * rcp(c.hi)), c_hi(c.hi) {}
+  __device__ __forceinline__ uint64_t of(uint64_t d) const {
+    const uint64_t c40 = pack2(40.f, 40.f), y = fma2(d, hi, c40);
+    const uint64_t rest = fma2(d, lo, fma2(d, hi, fma2(y, pack2(-1.f, -1.f), c40)));  // what y's rounding left
+    float u, v;
+    unpack2(y, u, v);
+    return mul2(pack2(ex2_ftz(u), ex2_ftz(v)), fma2(rest, pack2(0.693147182f, 0.693147182f), pack2(1.f, 1.f)));
+  }
+  __device__ __forceinline__ uint64_t of(float u, float v, float base) const { return of(pack2(fmaxf(u - base, low), fmaxf(v - base, low))); }
+  // Two bf16 logits: the least d stands in bf16, rounded down (least()), which
+  // does not do where it would overflow (tame()).
+  __device__ __forceinline__ bool tame(float base) const { return fabsf(base) < 1e30f && fabsf(base) * c_hi < 1e37f; }
+  __device__ __forceinline__ uint32_t least(float base) const {
+    const float x = base + low;
+    const uint16_t h = f2bf(x - 0.0078125f * fabsf(x));
+    return h | (uint32_t)h << 16;
+  }
+  __device__ __forceinline__ uint64_t of(uint32_t w, uint32_t least, float base) const { return of(add_bf16x2(max_bf16x2(w, least), -base)); }
+};
+__device__ __forceinline__ float finite_or_0(float x) { return fabsf(x) < INFINITY ? x : 0.f; }
+__device__ __forceinline__ float is_there(float x) { return x > -INFINITY ? 1.f : 0.f; }
+
+// The vectors of a row start at its first 16-byte boundary.  The logits before it,
+// and those after the last whole vector, are single ones of the first block.
+struct Span {
+  int e0, v0, v1, one;
+};
+template <bool F32>
+__device__ __forceinline__ Span span_of(const char* in, int V, int C, int rank) {
+  const int tid = threadIdx.x;
+  Span s;
+  s.e0 = min(V, (int)((16u - ((uint32_t)(uintptr_t)in & 15u)) & 15u) / (F32 ? 4 : 2));
+  const int nvec = (V - s.e0) / 8, per = (nvec + C - 1) / C, rest = s.e0 + 8 * nvec;
+  s.v0 = min(rank * per, nvec);
+  s.v1 = min(s.v0 + per, nvec);
+  s.one = rank ? -1 : tid < s.e0 ? tid : tid >= 32 && tid - 32 < V - rest ? rest + tid - 32 : -1;
+  return s;
+}
+
+// What the blocks of a row, and the warps of a block, come to together.  `sum` is
+// of 2^(40 + ..) from the same thread's, warp's or block's `top`; cold rows have
+// none, but the first place of the largest.
+struct Meeting {
+  float top[PB_WARPS], sum[PB_WARPS];
+  int first[PB_WARPS];
+  __align__(16) uint64_t share[8][2];
+};
+struct Total {
+  float top, sum;
+  int first;
+};
+// From every thread's own (the cluster's first arrival is behind it).
+__device__ __forceinline__ Total meet(Meeting& m, float top, float sum, int first, bool warm, const Scale& c, int C, int rank) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto join = [&](int n) {  // over the first n lanes, a power of two
+    float all = top;
+    for (int o = n / 2; o; o >>= 1) all = max_nan(all, __shfl_xor_sync(0xffffffffu, all, o));
+    if (warm) {
+      sum *= exp_scaled(top, all, c);
+      if (top == -INFINITY) sum = 0.f;
+      for (int o = n / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    } else {
+      if (top != all) first = 1 << 30;
+      for (int o = n / 2; o; o >>= 1) first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
+    }
+    top = all;
+  };
+  join(32);
+  if (lane == 0) {
+    m.top[warp] = top;
+    m.sum[warp] = sum;
+    m.first[warp] = first;
+  }
+  __syncthreads();
+  if (C > 1) cluster_wait();
+  if (warp == 0) {
+    top = m.top[lane % PB_WARPS];
+    sum = m.sum[lane % PB_WARPS];
+    first = m.first[lane % PB_WARPS];
+    join(PB_WARPS);
+    if (lane < C) {
+      const uint64_t lo = (uint64_t)__float_as_uint(top) | ((uint64_t)__float_as_uint(sum) << 32), hi = (uint32_t)first;
+      if (C > 1) {
+        cluster_put(&m.share[rank][0], lane, lo);
+        cluster_put(&m.share[rank][1], lane, hi);
+      } else {
+        m.share[0][0] = lo;
+        m.share[0][1] = hi;
+      }
+    }
+    __syncwarp();
+  }
+  if (C > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  const uint64_t lo = m.share[lane % C][0];  // C is a power of two
+  top = __uint_as_float((uint32_t)lo);
+  sum = __uint_as_float((uint32_t)(lo >> 32));
+  first = (int)m.share[lane % C][1];
+  join(C);
+  return Total{top, sum, first};
+}
+
+template <bool F32, int K>
+__global__ void __launch_bounds__(PB_THREADS, 2) token_probs_kernel(const ProbArgs a) {
+  constexpr int T = PB_THREADS, ES = F32 ? 4 : 2;
+  __shared__ Meeting m;
+  const int tid = threadIdx.x, C = a.blocks;
+  const int rank = C > 1 ? (int)cluster_rank() : 0, r = blockIdx.x / C;
   if (C > 1) cluster_arrive();  // this block runs: the others may write to it
   pdl_wait();
   pdl_trigger();
-  // A row's vectors start at its first 16-byte boundary.  The logits before it,
-  // and those after the last whole vector, are single ones of the first block.
-  struct Row {
-    int r, e0, v0, v1, one;
-    float x1, t;
-  };
-  auto fetch = [&](int r) {
-    Row w = {r, 0, 0, 0, -1, -INFINITY, 1.f};
-    if (r >= a.R) return w;
-    const char* in = a.in + (int64_t)r * a.in_ld * ES;
-    w.e0 = min(V, (int)((16u - ((uint32_t)(uintptr_t)in & 15u)) & 15u) / ES);
-    const int nvec = (V - w.e0) / 8, per = (nvec + C - 1) >> a.log2_blocks, rest = w.e0 + 8 * nvec;
-    w.v0 = min(rank * per, nvec);
-    w.v1 = min(w.v0 + per, nvec);
-    w.one = rank ? -1 : tid < w.e0 ? tid : tid >= 32 && tid - 32 < V - rest ? rest + tid - 32 : -1;
+  const char* in = a.in + (int64_t)r * a.in_ld * ES;
+  const float t = a.temperature ? __ldg(a.temperature + r) : 1.f;
+  const Span s = span_of<F32>(in, a.V, C, rank);
+  float x[K][8], x1 = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int v = w.v0 + k * T + tid;
-      constexpr uint32_t NONE = F32 ? 0xFF800000u : 0xFF80FF80u;  // -inf
+  for (int k = 0; k < K; ++k) {
+    const int v = s.v0 + k * T + tid;
+    if (v < s.v1) {
+      const uint4* src = reinterpret_cast<const uint4*>(in + ((int64_t)s.e0 + 8 * (int64_t)v) * ES);
+      const uint4 p = src[0], q = src[F32 ? 1 : 0];
+      const uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
 #pragma unroll
-      for (int q = 0; q < Q; ++q) {
-        uint4* to = &next[(k * Q + q) * T + tid];
-        if (v < w.v1) cp_async16(to, in + ((int64_t)w.e0 + 8 * (int64_t)v) * ES + 16 * q);
-        else *to = make_uint4(NONE, NONE, NONE, NONE);
-      }
+      for (int i = 0; i < 8; ++i) x[k][i] = F32 ? __uint_as_float(w[i]) : i & 1 ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[k][i] = -INFINITY;
     }
-    cp_async_commit();
-    if (w.one >= 0) w.x1 = logit_at<F32>(in, w.one);
-    if (a.temperature) w.t = __ldg(a.temperature + r);
-    return w;
-  };
-  Row w = fetch(blockIdx.x / C);
-  if (C > 1) cluster_wait();
-  for (int turn = 0; w.r < a.R; turn ^= 1) {
-    float x1 = w.x1;
-    cp_async_wait_all();  // a thread reads what it fetched itself
-    // 8 logits a vector: fp32 ones where their exponentials will be, bf16 ones as they come
-    float x[K][8];
-    uint32_t u[K][4];
+  }
+  if (s.one >= 0) x1 = logit_at<F32>(in, s.one);
+  const bool warm = t > 0.f;
+  const Scale c = log2_scale(t);
+  const Exp2 ex(c);
+
+  float top = x1;
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) top = max_nan(top, x[k][i], x[k][i + 1]);
+  // exponentials from the warp's largest, which the output takes a scale from
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float sum = 0.f;
+  int first = 1 << 30;
+  if (!warm) {
+    if (x1 == top && s.one >= 0) first = s.one;
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-      for (int q = 0; q < Q; ++q) {
-        const uint4 p = next[(k * Q + q) * T + tid];
-        const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+      for (int i = 7; i >= 0; --i)
+        if (x[k][i] == top) first = min(first, s.e0 + 8 * (s.v0 + k * T + tid) + i);
+  } else if (c.flat) {
+    sum = x1 = is_there(x1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (F32) x[k][4 * q + i] = __uint_as_float(w[i]);
-          else u[k][i] = w[i];
-        }
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += x[k][i] = is_there(x[k][i]);
+  } else {
+    const float base = finite_or_0(top);
+    uint64_t sums[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const uint64_t e = ex.of(x[k][i], x[k][i + 1], base);
+        sums[i / 2 & 1] = add2(sums[i / 2 & 1], e);
+        unpack2(e, x[k][i], x[k][i + 1]);
       }
-    auto logit = [&](int k, int i) { return F32 ? x[k][i] : i & 1 ? bf16hi(u[k][i / 2]) : bf16lo(u[k][i / 2]); };
-    const bool warm = w.t > 0.f;
-    const Scale c = log2_scale(w.t);
-
-    float top = x1;
-    if (F32) {
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) top = max_nan(top, logit(k, i), logit(k, i + 1));
-    } else {
-      uint32_t most = u[0][0];
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = k ? 0 : 1; i < 4; ++i) most = max_nan_bf16x2(most, u[k][i]);
-      top = max_nan(top, bf16lo(most), bf16hi(most));
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-
-    float sum = 0.f;
-    if (!warm) {
-      int first = V;
-      if (x1 == top) first = w.one;
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 7; i >= 0; --i)
-          if (logit(k, i) == top) first = min(first, w.e0 + 8 * (w.v0 + k * T + tid) + i);
-      sum = __int_as_float(__reduce_min_sync(0xffffffffu, first));
-    } else {
-      if (c.flat) {
-        auto e = [](float v) { return v > -INFINITY ? 1.f : 0.f; };
-        sum = x1 = e(x1);
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) sum += x[k][i] = e(logit(k, i));
-      } else {
-        // 2^(40 + (x - top) c): what lies below 2^-126 of the largest stays normal
-        // (d as small as 2^-200 needs stands for all that is less, -inf too: in
-        // bf16 the logit of that d, rounded down, unless that would overflow)
-        const float base = top > -INFINITY ? top : 0.f, low = -200.f * rcp(c.hi), edge = base + low;
-        const bool tame = fabsf(base) < 1e30f && fabsf(base) * c.hi < 1e37f;
-        const uint16_t edge16 = f2bf(edge - 0.0078125f * fabsf(edge));
-        const uint32_t edge2 = edge16 | (uint32_t)edge16 << 16;
-        const uint64_t base2 = pack2(-base, -base), hi2 = pack2(c.hi, c.hi), lo2 = pack2(c.lo, c.lo), ln2 = pack2(0.693147182f, 0.693147182f);
-        const uint64_t c40 = pack2(40.f, 40.f), one2 = pack2(1.f, 1.f), minus2 = pack2(-1.f, -1.f);
-        auto e2 = [&](uint64_t d, float& u, float& v) {
-          const uint64_t y = fma2(d, hi2, c40);
-          const uint64_t rest = fma2(d, lo2, fma2(d, hi2, fma2(y, minus2, c40)));  // what y's rounding left
-          unpack2(y, u, v);
-          const uint64_t e = mul2(pack2(ex2_ftz(u), ex2_ftz(v)), fma2(rest, ln2, one2));
-          unpack2(e, u, v);
-          return e;
-        };
-        auto diff = [&](float u, float v) {
-          unpack2(add2(pack2(u, v), base2), u, v);
-          return pack2(fmaxf(u, low), fmaxf(v, low));
-        };
-        uint64_t sums[2] = {0, 0};
-        if (F32 || !tame) {
-#pragma unroll
-          for (int k = 0; k < K; ++k)
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) sums[i / 2 & 1] = add2(sums[i / 2 & 1], e2(diff(logit(k, i), logit(k, i + 1)), x[k][i], x[k][i + 1]));
-        } else {
-#pragma unroll
-          for (int k = 0; k < K; ++k)
-#pragma unroll
-            for (int i = 0; i < 8; i += 2)
-              sums[i / 2 & 1] = add2(sums[i / 2 & 1], e2(add_bf16x2(max_bf16x2(u[k][i / 2], edge2), -base), x[k][i], x[k][i + 1]));
-        }
-        float y, z;
-        e2(diff(x1, -INFINITY), x1, z);
-        unpack2(add2(sums[0], sums[1]), y, z);
-        sum = x1 + (y + z);
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    }
-    // one exchange: every warp tells all blocks of the row.  (A block that is a
-    // row ahead writes to the other half, and cannot be two ahead.)
-    if (lane < C) {
-      const uint64_t v = (uint64_t)__float_as_uint(top) | ((uint64_t)__float_as_uint(sum) << 32);
-      if (C > 1) cluster_put(&tell[turn][rank * W + warp], lane, v);
-      else tell[turn][warp] = v;
-    }
-    __syncwarp();
-    if (C > 1) cluster_arrive();
-    else __syncthreads();
-    // the next row's vectors come in meanwhile (this one's have left shared
-    // memory: top depends on all of them)
-    const Row after = fetch(w.r + clusters);
-    if (C > 1) cluster_wait();
-    float all = -INFINITY, total = 0.f;
-    int first = V;
-    {
-      float tops[8 * W / 32], sums[8 * W / 32];
-#pragma unroll
-      for (int j = 0; j < 8 * W / 32; ++j) {
-        const bool in = 32 * j + lane < C * W;
-        const uint64_t v = in ? tell[turn][32 * j + lane] : 0;
-        tops[j] = in ? __uint_as_float((uint32_t)v) : -INFINITY;
-        sums[j] = __uint_as_float((uint32_t)(v >> 32));
-        all = max_nan(all, tops[j]);
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) all = max_nan(all, __shfl_xor_sync(0xffffffffu, all, o));
-#pragma unroll
-      for (int j = 0; j < 8 * W / 32; ++j) {
-        if (32 * j >= C * W) continue;
-        if (warm) total += sums[j] * exp_part(tops[j], all, c);
-        else if (tops[j] == all) first = min(first, __float_as_int(sums[j]));
-      }
-      if (warm) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-      } else {
-        first = __reduce_min_sync(0xffffffffu, first);
-      }
-    }
-    // a row with NaN or +inf, one with nothing but -inf, one of a single token
-    const bool bad = !(all < INFINITY);
-    if (warm && !bad && all > -INFINITY) {
-      const float f = top > -INFINITY ? exp_scaled(top, all, c) : 0.f, inv = __frcp_rn(total);
-      // in two steps where the scale would be subnormal
-      const bool whole = f * inv > 1e-37f;
-      const float f1 = whole ? f * inv : f, f2 = whole ? 1.f : inv;
-      const uint64_t g = pack2(f1, f1), h = pack2(f2, f2);
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          uint64_t y = mul2(pack2(x[k][i], x[k][i + 1]), g);
-          if (!whole) y = mul2(y, h);
-          unpack2(y, x[k][i], x[k][i + 1]);
-        }
-      x1 = x1 * f1 * f2;
-    } else {
-      const float fill = bad ? __int_as_float(0x7FFFFFFF) : 0.f;
-      const int is = !warm && !bad && all > -INFINITY ? first : -1;
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[k][i] = w.e0 + 8 * (w.v0 + k * T + tid) + i == is ? 1.f : fill;
-      x1 = w.one == is ? 1.f : fill;
-    }
-    float* out = a.out + (int64_t)w.r * a.out_ld;
-    const int mis = (int)(((uintptr_t)out / 4 + w.e0) & 7);  // floats of the vectors past a 32-byte boundary
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int v = w.v0 + k * T + tid;
-      if (v >= w.v1) continue;
-      float* to = out + w.e0 + 8 * v;
-      if (mis == 0) {
-        store8(to, x[k]);
-      } else if ((mis & 3) == 0) {
-        reinterpret_cast<float4*>(to)[0] = make_float4(x[k][0], x[k][1], x[k][2], x[k][3]);
-        reinterpret_cast<float4*>(to)[1] = make_float4(x[k][4], x[k][5], x[k][6], x[k][7]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) to[i] = x[k][i];
-      }
-    }
-    if (w.one >= 0) out[w.one] = x1;
-    w = after;
+    float u, v;
+    unpack2(ex.of(x1, -INFINITY, base), x1, v);
+    unpack2(add2(sums[0], sums[1]), u, v);
+    sum = x1 + (u + v);
   }
+  const Total all = meet(m, top, sum, first, warm, c, C, rank);
+
+  // a row with NaN or +inf, one with nothing but -inf, one of a single token
+  float* out = a.out + (int64_t)r * a.out_ld;
+  const int mis = (int)(((uintptr_t)out / 4 + s.e0) & 7);
+  const bool bad = !(all.top < INFINITY), some = !bad && all.top > -INFINITY;
+  if (warm && some) {
+    // in two steps where the scale would be subnormal
+    const float f = top > -INFINITY ? exp_scaled(top, all.top, c) : 0.f, inv = __frcp_rn(all.sum);
+    const bool whole = f * inv > 1e-37f;
+    const float f1 = whole ? f * inv : f, f2 = whole ? 1.f : inv;
+    const uint64_t g = pack2(f1, f1), h = pack2(f2, f2);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) unpack2(mul2(mul2(pack2(x[k][i], x[k][i + 1]), g), h), x[k][i], x[k][i + 1]);
+    x1 = x1 * f1 * f2;
+  } else {
+    const float fill = bad ? __int_as_float(0x7FFFFFFF) : 0.f;
+    const int is = !warm && some ? all.first : -2;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[k][i] = s.e0 + 8 * (s.v0 + k * T + tid) + i == is ? 1.f : fill;
+    x1 = s.one == is ? 1.f : fill;
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int v = s.v0 + k * T + tid;
+    if (v < s.v1) put8(out + s.e0 + 8 * (int64_t)v, mis, x[k]);
+  }
+  if (s.one >= 0) out[s.one] = x1;
 }
 
-// Rows that no cluster holds (more than 327 680 logits): a block a row, which
-// reads it three times, from L2 the second and third.
 template <bool F32>
-__global__ void __launch_bounds__(1024) token_probs_loop_kernel(const ProbArgs a) {
-  __shared__ float top_sh[32], sum_sh[32];
-  __shared__ int first_sh[32], bad_sh[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.x, V = a.V;
+__global__ void __launch_bounds__(PB_THREADS, 2) token_probs_loop_kernel(const ProbArgs a) {
+  constexpr int T = PB_THREADS, ES = F32 ? 4 : 2, F = F32 ? 2 : 4, Q = F32 ? 8 : 4;  // F vectors of Q words at a time
+  __shared__ Meeting m;
+  const int tid = threadIdx.x, C = a.blocks;
+  const int rank = C > 1 ? (int)cluster_rank() : 0, r = blockIdx.x / C;
+  if (C > 1) cluster_arrive();  // this block runs: the others may write to it
   pdl_wait();
   pdl_trigger();
-  const char* in = a.in + (int64_t)r * a.in_ld * (F32 ? 4 : 2);
-  float* out = a.out + (int64_t)r * a.out_ld;
+  const char* in = a.in + (int64_t)r * a.in_ld * ES;
   const float t = a.temperature ? __ldg(a.temperature + r) : 1.f;
-  float top = -INFINITY;
-  int first = V;
-  bool bad = false;
-  for (int i = tid; i < V; i += 1024) {
-    const float x = logit_at<F32>(in, i);
-    bad |= !(x < INFINITY);
-    if (x > top) {
-      top = x;
-      first = i;
-    }
-  }
-  auto better = [](float& top, int& first, float x, int i) {
-    if (x > top || (x == top && i < first)) {
-      top = x;
-      first = i;
-    }
-  };
-#pragma unroll
-  for (int o = 16; o; o >>= 1) better(top, first, __shfl_xor_sync(0xffffffffu, top, o), __shfl_xor_sync(0xffffffffu, first, o));
-  bad = __any_sync(0xffffffffu, bad);
-  if (lane == 0) {
-    top_sh[warp] = top;
-    first_sh[warp] = first;
-    bad_sh[warp] = bad;
-  }
-  __syncthreads();
-  for (int w = 0; w < 1024 / 32; ++w) {
-    better(top, first, top_sh[w], first_sh[w]);
-    bad |= bad_sh[w] != 0;
-  }
-  const bool none = top == -INFINITY;  // and no NaN
+  const Span s = span_of<F32>(in, a.V, C, rank);
+  const bool warm = t > 0.f;
   const Scale c = log2_scale(t);
-  float sum = 0.f;
-  if (t > 0.f && !none)
-    for (int i = tid; i < V; i += 1024) sum += exp_scaled(logit_at<F32>(in, i), top, c);
+  const Exp2 ex(c);
+  auto load = [&](uint32_t (&w)[F][Q], int v) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) sum_sh[warp] = sum;
-  __syncthreads();
-  sum = 0.f;
-  for (int w = 0; w < 1024 / 32; ++w) sum += sum_sh[w];
-  for (int i = tid; i < V; i += 1024) {
-    float p;
-    if (bad) p = __int_as_float(0x7FFFFFFF);
-    else if (none) p = 0.f;
-    else if (t > 0.f) p = __fdiv_rn(exp_scaled(logit_at<F32>(in, i), top, c), sum);
-    else p = i == first ? 1.f : 0.f;
-    out[i] = p;
-  }
-}
+    for (int f = 0; f < F; ++f)
+#pragma unroll
+      for (int q = 0; q < Q / 4; ++q) {
+        uint4 p = F32 ? make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u) : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+        if (v + f * T < s.v1) p = *reinterpret_cast<const uint4*>(in + ((int64_t)s.e0 + 8 * (int64_t)(v + f * T)) * ES + 16 * q);
+        w[f][4 * q] = p.x;
+        w[f][4 * q + 1] = p.y;
+        w[f][4 * q + 2] = p.z;
+        w[f][4 * q + 3] = p.w;
+      }
+  };
+  auto logit = [](const uint32_t (&w)[Q], int i) { return F32 ? __uint_as_float(w[i % Q]) : i & 1 ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]); };
 
-template <bool F32, int K, int T>
-mt_status probs_launch(ProbArgs a, const Launch& l, const DeviceInfo* di) {
-  constexpr int smem = K * T * (F32 ? 32 : 16);
-  const auto kernel = token_probs_kernel<F32, K, T>;
-  static std::atomic<int> fit[64][4];  // clusters of 1, 2, 4, 8 blocks that the device holds at a time
-  int dev = 0, size = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(e);
-  while (1 << size < a.blocks) ++size;
-  a.log2_blocks = size;
-  int clusters = dev >= 0 && dev < 64 ? fit[dev][size].load() : 0;
-  if (clusters < 1) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return cuda_fail(e);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.blocks);
-    cfg.blockDim = dim3(T);
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim = {(unsigned)a.blocks, 1, 1};
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
-    if (e != cudaSuccess) return cuda_fail(e);
-    if (clusters < 1) clusters = 1;
-    if (dev >= 0 && dev < 64) fit[dev][size].store(clusters);
+  // ---- the share's largest logit and its sum, a thread's own
+  float x1 = s.one >= 0 ? logit_at<F32>(in, s.one) : -INFINITY;
+  float top = warm ? x1 : -INFINITY, base = finite_or_0(top), sum = 0.f;
+  int first = 1 << 30;
+  bool tame = ex.tame(base);
+  uint32_t least = ex.least(base);
+  if (warm) {
+    float none;
+    if (c.flat) sum = is_there(x1);
+    else unpack2(ex.of(x1, -INFINITY, base), sum, none);
   }
-  // as many rows to each cluster, in one round of clusters
-  const int rows = (a.R + clusters - 1) / clusters;
-  const dim3 grid((unsigned)((a.R + rows - 1) / rows) * a.blocks);
-  return a.blocks > 1 ? launch_cluster(kernel, a.blocks, grid, dim3(T), smem, l, a) : launch(kernel, grid, dim3(T), smem, l, a);
-}
+#pragma unroll 1
+  for (int v = s.v0 + tid; v < s.v1; v += F * T) {
+    uint32_t w[F][Q];
+    load(w, v);
+    float most = -INFINITY;
+    if (F32) {
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) most = max_nan(most, logit(w[f], i), logit(w[f], i + 1));
+    } else {
+      uint32_t b = w[0][0];
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int i = f ? 0 : 1; i < 4; ++i) b = max_nan_bf16x2(b, w[f][i]);
+      most = max_nan(bf16lo(b), bf16hi(b));
+    }
+    if (!(most <= top)) {
+      if (!warm) {
+#pragma unroll
+        for (int f = F - 1; f >= 0; --f)
+#pragma unroll
+          for (int i = 7; i >= 0; --i)
+            if (logit(w[f], i) == most) first = s.e0 + 8 * (v + f * T) + i;
+      } else if (!c.flat) {
+        sum = top > -INFINITY ? sum * exp_scaled(top, most, c) : 0.f;
+      }
+      top = max_nan(top, most);
+      base = finite_or_0(top);
+      tame = ex.tame(base);
+      least = ex.least(base);
+    }
+    if (!warm) continue;
+    if (c.flat) {
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += is_there(logit(w[f], i));
+      continue;
+    }
+    uint64_t sums[2] = {0, 0};
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const uint64_t e = !F32 && tame ? ex.of(w[f][i / 2 % Q], least, base) : ex.of(logit(w[f], i), logit(w[f], i + 1), base);
+        sums[i / 2 & 1] = add2(sums[i / 2 & 1], e);
+      }
+    float y, z;
+    unpack2(add2(sums[0], sums[1]), y, z);
+    sum += y + z;
+  }
+  if (!warm && s.one >= 0) {  // before or behind the vectors
+    if (!(x1 < top)) first = x1 == top ? min(first, s.one) : s.one;
+    top = max_nan(top, x1);
+  }
+  const Total all = meet(m, top, sum, first, warm, c, C, rank);
 
-// The fewest blocks a row that hold it (their number costs little, but the last
-// vectors of their threads lie idle), more where the rows are few.
-template <bool F32>
-mt_status probs_run(ProbArgs a, const Launch& l, const DeviceInfo* di) {
-  const int nvec = a.V / 8;
-  auto per = [&](int C, int T) { return std::max(1, ((nvec + C - 1) / C + T - 1) / T); };  // vectors of a thread
-  if (per(8, PB_THREADS) > PB_MOST) {
-    a.blocks = 8;
-    if (per(8, 1024) <= PB_MOST) return probs_launch<F32, PB_MOST, 1024>(a, l, di);
-    return launch(token_probs_loop_kernel<F32>, dim3(a.R), dim3(1024), 0, l, a);
+  // ---- the output
+  float* out = a.out + (int64_t)r * a.out_ld;
+  const int mis = (int)(((uintptr_t)out / 4 + s.e0) & 7);
+  const bool bad = !(all.top < INFINITY), some = !bad && all.top > -INFINITY;
+  if (!warm || !some) {
+    // a row with NaN or +inf, one with nothing but -inf, one of a single token
+    const float fill = bad ? __int_as_float(0x7FFFFFFF) : 0.f;
+    const int is = !warm && some ? all.first : -2;
+#pragma unroll 1
+    for (int v = s.v0 + tid; v < s.v1; v += T) {
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = s.e0 + 8 * v + i == is ? 1.f : fill;
+      put8(out + s.e0 + 8 * (int64_t)v, mis, y);
+    }
+    if (s.one >= 0) out[s.one] = s.one == is ? 1.f : fill;
+    return;
   }
-  a.blocks = 1;
-  while (a.blocks < 8 && (per(a.blocks, PB_THREADS) > 4 || ((int64_t)a.R * a.blocks < di->sm_count && per(a.blocks, PB_THREADS) > 1))) a.blocks *= 2;
-  // many rows: blocks of half as many threads with twice the logits each, as
-  // what a warp does once a row then counts half
-  if ((int64_t)a.R * a.blocks >= 4 * di->sm_count) {
-    switch ((per(a.blocks, 256) + 1) / 2) {
-      case 1: return probs_launch<F32, 2, 256>(a, l, di);
-      case 2: return probs_launch<F32, 4, 256>(a, l, di);
-      case 3: return probs_launch<F32, 6, 256>(a, l, di);
-      case 4: return probs_launch<F32, 8, 256>(a, l, di);
-      default: return probs_launch<F32, 2 * PB_MOST, 256>(a, l, di);
+  base = all.top;
+  tame = ex.tame(base);
+  least = ex.least(base);
+  const float inv = __frcp_rn(all.sum);
+  const uint64_t g = pack2(inv, inv);
+#pragma unroll 1
+  for (int v = s.v0 + tid; v < s.v1; v += F * T) {
+    uint32_t w[F][Q];
+    load(w, v);
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        if (c.flat) {
+          y[i] = is_there(logit(w[f], i)) * inv;
+          y[i + 1] = is_there(logit(w[f], i + 1)) * inv;
+        } else {
+          const uint64_t e = !F32 && tame ? ex.of(w[f][i / 2 % Q], least, base) : ex.of(logit(w[f], i), logit(w[f], i + 1), base);
+          unpack2(mul2(e, g), y[i], y[i + 1]);
+        }
+      }
+      if (v + f * T < s.v1) put8(out + s.e0 + 8 * (int64_t)(v + f * T), mis, y);
     }
   }
-  switch (per(a.blocks, PB_THREADS)) {
-    case 1: return probs_launch<F32, 1, PB_THREADS>(a, l, di);
-    case 2: return probs_launch<F32, 2, PB_THREADS>(a, l, di);
-    case 3: return probs_launch<F32, 3, PB_THREADS>(a, l, di);
-    case 4: return probs_launch<F32, 4, PB_THREADS>(a, l, di);
-    default: return probs_launch<F32, PB_MOST, PB_THREADS>(a, l, di);
+  if (s.one >= 0) {
+    float none;
+    if (c.flat) x1 = is_there(x1) * inv;
+    else unpack2(mul2(ex.of(x1, -INFINITY, base), g), x1, none);
+    out[s.one] = x1;
   }
+}
+
+template <bool F32>
+mt_status probs_run(ProbArgs a, const Launch& l, int sms) {
+  const int nvec = a.V / 8;
+  auto per = [&](int C) { return std::max(1, ((nvec + C - 1) / C + PB_THREADS - 1) / PB_THREADS); };  // vectors of a thread
+  auto go = [&](auto kernel) {
+    const dim3 grid((unsigned)a.R * a.blocks);
+    return a.blocks > 1 ? launch_cluster(kernel, a.blocks, grid, dim3(PB_THREADS), 0, l, a) : launch(kernel, grid, dim3(PB_THREADS), 0, l, a);
+  };
+  // the fewest blocks a row that hold it, more where the rows are few
+  a.blocks = 1;
+  while (a.blocks < 8 && (per(a.blocks) > PB_MOST || ((int64_t)a.R * a.blocks < sms && per(a.blocks) > 1))) a.blocks *= 2;
+  if (per(a.blocks) <= PB_MOST && (int64_t)a.R * a.blocks <= 4 * sms) {
+    switch (per(a.blocks)) {
+      case 1: return go(token_probs_kernel<F32, 1>);
+      case 2: return go(token_probs_kernel<F32, 2>);
+      case 3: return go(token_probs_kernel<F32, 3>);
+      case 4: return go(token_probs_kernel<F32, 4>);
+      default: return go(token_probs_kernel<F32, PB_MOST>);
+    }
+  }
+  // shares of a row small enough that the last round of blocks is short
+  a.blocks = 1;
+  while (a.blocks < 8 && (int64_t)a.R * a.blocks < 8 * sms && per(a.blocks) > 4) a.blocks *= 2;
+  return go(token_probs_loop_kernel<F32>);
 }
 
 }  // namespace
@@ -524,7 +563,7 @@ extern "C" mt_status mt_token_probs(const void* logits, int64_t logits_ld, mt_dt
   int derr = 0;
   const DeviceInfo* di = device_info(&derr);
   if (!di) return cuda_fail((cudaError_t)derr);
-  const ProbArgs a = {(const char*)logits, probs, logits_ld, probs_ld, V, temperature, R, 1, 0};
+  const ProbArgs a = {(const char*)logits, probs, logits_ld, probs_ld, V, temperature, R, 1};
   const Launch l{(cudaStream_t)stream, mt_get_option(MT_OPT_PDL) != 0};
-  return dtype == MT_F32 ? probs_run<true>(a, l, di) : probs_run<false>(a, l, di);
+  return dtype == MT_F32 ? probs_run<true>(a, l, di->sm_count) : probs_run<false>(a, l, di->sm_count);
 }
