@@ -12,7 +12,7 @@
 //  * Many (token_probs_loop_kernel): a block passes over its share with a running
 //    maximum and sum, and over it again, from L2, for the output: nothing but one
 //    exchange stands between the loads and the stores.  448 rows of 128 256 bf16
-//    logits: LOOP_US.  (The first kernel: 100; with clusters that stay and the next
+//    logits: 73 us, 4.7 TB/s.  (The first kernel: 100; with clusters that stay and the next
 //    row's logits on their way 76, most of it waiting between the steps of a row.)
 #include <math.h>
 
@@ -526,7 +526,9 @@ mt_status probs_run(ProbArgs a, const Launch& l, int sms) {
   // the fewest blocks a row that hold it, more where the rows are few
   a.blocks = 1;
   while (a.blocks < 8 && (per(a.blocks) > PB_MOST || ((int64_t)a.R * a.blocks < sms && per(a.blocks) > 1))) a.blocks *= 2;
-  if (per(a.blocks) <= PB_MOST && (int64_t)a.R * a.blocks <= 4 * sms) {
+  // (64 rows of 50 257 bf16 logits: 7.2 us in registers, 8.6 in two passes; of
+  // 128 256, 512 blocks: 16.6 and 14.6; 448 of 4000, a block each: 5.4 and 10.3)
+  if (per(a.blocks) <= PB_MOST && (a.blocks == 1 || (int64_t)a.R * a.blocks <= 2 * sms)) {
     switch (per(a.blocks)) {
       case 1: return go(token_probs_kernel<F32, 1>);
       case 2: return go(token_probs_kernel<F32, 2>);
@@ -535,9 +537,19 @@ mt_status probs_run(ProbArgs a, const Launch& l, int sms) {
       default: return go(token_probs_kernel<F32, PB_MOST>);
     }
   }
-  // shares of a row small enough that the last round of blocks is short
-  a.blocks = 1;
-  while (a.blocks < 8 && (int64_t)a.R * a.blocks < 8 * sms && per(a.blocks) > 4) a.blocks *= 2;
+  // A share costs as much as its logits and 12 000 more; an SM does two at a time,
+  // and one alone is not twice as fast.  (448 rows of 128 256 bf16 logits by 1, 2,
+  // 4 and 8 blocks: 88, 73, 82 and 101 us; of 50 257: 34, 39, 49 and 91; 100 rows of
+  // 151 936: 36, 29, 29 and 36; 64 of 128 256: 27, 17, 15 and 18.)
+  double least = 0;
+  for (int C = 1; C <= 8; C *= 2) {
+    const int64_t n = ((int64_t)a.R * C + sms - 1) / sms;
+    const double cost = (n + (n % 2 ? 0.4 : 0.0)) * (12000.0 + (double)a.V / C);
+    if (C == 1 || cost < least) {
+      least = cost;
+      a.blocks = C;
+    }
+  }
   return go(token_probs_loop_kernel<F32>);
 }
 
