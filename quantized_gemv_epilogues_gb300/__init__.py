@@ -474,25 +474,6 @@ def mt_paged_attention(q, k_cache, v_cache, pages, q_start, kv_len, max_q, scale
     """Attention of the new tokens q [T, q_heads, dim] over the paged cache;
     out [T, q_heads, dim] (bf16 or fp32), lse float [T, q_heads] or None,
     window 0 for none.  max_q: the most new tokens of a sequence (a hint)."""
-    _attention("mt_paged_attention", q, k_cache, v_cache, pages, q_start, kv_len, None, max_q, scale, out, workspace, lse, window,
-               sinks, stream)
-
-
-def _bit_rows(name, t, T):
-    """Address, row stride and words of int32 [T, words] rows of bits."""
-    i32 = _torch.int32
-    if t.dtype is not i32 or t.dim() != 2:
-        _typed(name, t, i32, 2)
-    rows, words = t.shape
-    ld, one = t.stride()
-    if rows != T or (words > 1 and one != 1):
-        raise ValueError(f"{name}: {T} contiguous rows are required")
-    if words >> 31:
-        raise ValueError(f"{name}: rows of fewer than 2^31 words are required")
-    return t.data_ptr(), (ld if T > 1 else words), words
-
-
-def _attention(call, q, k_cache, v_cache, pages, q_start, kv_len, visible, max_q, scale, out, workspace, lse, window, sinks, stream):
     torch = _torch or _get_torch()
     shape = q.shape
     if len(shape) != 3:
@@ -512,24 +493,93 @@ def _attention(call, q, k_cache, v_cache, pages, q_start, kv_len, visible, max_q
         lp = lse.data_ptr()
     if not workspace.is_contiguous():
         raise ValueError("workspace: a contiguous tensor is required")
-    if visible is not None:
-        bp, bld, words = _bit_rows("visible", visible, T)
     # a C int would take the lower 32 bits of what is wider than any text
     if not -1 < window < 1 << 31:
         window = -1 if window < 0 else 0x7FFFFFFF
     if not -1 < sinks < 1 << 31:
         sinks = -1 if sinks < 0 else 0x7FFFFFFF
     if not (q.is_cuda and k_cache.is_cuda and v_cache.is_cuda and pages.is_cuda and q_start.is_cuda and kv_len.is_cuda and out.is_cuda
-            and workspace.is_cuda and (lse is None or lse.is_cuda) and (visible is None or visible.is_cuda)):
-        _on_device(call, q=q, k_cache=k_cache, v_cache=v_cache, pages=pages, q_start=q_start, kv_len=kv_len, visible=visible, out=out,
+            and workspace.is_cuda and (lse is None or lse.is_cuda)):
+        _on_device("mt_paged_attention", q=q, k_cache=k_cache, v_cache=v_cache, pages=pages, q_start=q_start, kv_len=kv_len, out=out,
                    workspace=workspace, lse=lse)
-    dt, wp, wb = MT_F32 if f32 else MT_BF16, workspace.data_ptr(), workspace.nbytes
-    if visible is None:
-        st = _lib.mt_paged_attention(qp, qs, H, cache, batch, scale, window, sinks, op, os_, dt, lp, wp, wb, _stream(stream))
-    else:
-        st = _lib.mt_tree_attention(qp, qs, H, cache, batch, bp, bld, words, scale, window, sinks, op, os_, dt, lp, wp, wb,
-                                    _stream(stream))
-    _check(st, call)
+    _check(_lib.mt_paged_attention(qp, qs, H, cache, batch, scale, window, sinks, op, os_,
+                                   MT_F32 if f32 else MT_BF16, lp, workspace.data_ptr(), workspace.nbytes,
+                                   _stream(stream)), "mt_paged_attention")
+
+
+def mt_logit_penalties(logits, out, history=None, history_start=None, prompt_len=None, repetition=None, presence=None,
+                       frequency=None, bias_ids=None, bias_values=None, bias_start=None, allowed=None,
+                       stream=None) -> None:
+    """Biases, penalties for repeated tokens and allowed-token masks on logits
+    [B, V] (bf16 or fp32) into out (which may be logits); ragged int32 history
+    and bias lists with [B + 1] starts, allowed int32 [B, words] bits."""
+    torch = _torch or _get_torch()
+    i32, f32, dt = torch.int32, torch.float32, logits.dtype
+    shape = logits.shape
+    if (dt is not f32 and dt is not torch.bfloat16) or len(shape) != 2 or out.dtype is not dt:
+        _typed("logits", logits, f32 if dt is f32 else torch.bfloat16, 2)
+        _typed("out", out, dt, 2)
+    B, V = shape
+    ld, one = logits.stride()
+    out_ld, out_one = out.stride()
+    if out.shape != shape or (V > 1 and (one != 1 or out_one != 1)):
+        raise ValueError("logits and out must have the same shape and contiguous rows")
+    if B == 1:
+        ld = out_ld = V
+    hist = start = prompt = ids = values = bstart = ap = None
+    n_hist = n_bias = ald = 0
+    # an empty tensor has no address: a list without entries is no list
+    if history is not None:
+        n_hist = history.numel()
+        hist = _flat("history", history, i32) or None
+        start = _flat("history_start", history_start, i32, B + 1) if hist else None
+        prompt = _flat("prompt_len", prompt_len, i32, B) if hist else None
+    if bias_ids is not None:
+        n_bias = bias_ids.numel()
+        ids = _flat("bias_ids", bias_ids, i32) or None
+        values = _flat("bias_values", bias_values, f32, n_bias) if ids else None
+        bstart = _flat("bias_start", bias_start, i32, B + 1) if ids else None
+    if allowed is not None:
+        if allowed.dtype is not i32 or allowed.dim() != 2:
+            _typed("allowed", allowed, i32, 2)
+        rows, words = allowed.shape
+        ald, one = allowed.stride()
+        if rows != B or (words > 1 and one != 1):
+            raise ValueError(f"allowed: {B} contiguous rows are required")
+        if words * 32 < V:
+            raise ValueError(f"allowed: {(V + 31) // 32} words a row are required")
+        ap = allowed.data_ptr()
+        if B == 1:
+            ald = words
+    if (B | V | n_hist | n_bias) >> 31:
+        raise ValueError("logits and lists of fewer than 2^31 rows, tokens and entries are required")
+    if not (logits.is_cuda and out.is_cuda and (hist is None or history.is_cuda) and (start is None or history_start.is_cuda)
+            and (prompt is None or prompt_len.is_cuda) and (repetition is None or repetition.is_cuda)
+            and (presence is None or presence.is_cuda) and (frequency is None or frequency.is_cuda)
+            and (ids is None or bias_ids.is_cuda) and (values is None or bias_values.is_cuda)
+            and (bstart is None or bias_start.is_cuda)
+            and (allowed is None or allowed.is_cuda)):
+        _on_device("mt_logit_penalties", logits=logits, out=out, history=history, history_start=history_start,
+                   prompt_len=prompt_len, repetition=repetition, presence=presence, frequency=frequency, bias_ids=bias_ids,
+                   bias_values=bias_values, bias_start=bias_start, allowed=allowed)
+    _check(_lib.mt_logit_penalties(logits.data_ptr(), ld, out.data_ptr(), out_ld, MT_F32 if dt is f32 else MT_BF16, B, V,
+                                   hist, start, prompt, n_hist, _flat("repetition", repetition, f32, B),
+                                   _flat("presence", presence, f32, B), _flat("frequency", frequency, f32, B), ids, values,
+                                   bstart, n_bias, ap, ald, _stream(stream)), "mt_logit_penalties")
+
+
+def _bit_rows(name, t, T):
+    """Address, row stride and words of int32 [T, words] rows of bits."""
+    i32 = _torch.int32
+    if t.dtype is not i32 or t.dim() != 2:
+        _typed(name, t, i32, 2)
+    rows, words = t.shape
+    ld, one = t.stride()
+    if rows != T or (words > 1 and one != 1):
+        raise ValueError(f"{name}: {T} contiguous rows are required")
+    if words >> 31:
+        raise ValueError(f"{name}: rows of fewer than 2^31 words are required")
+    return t.data_ptr(), (ld if T > 1 else words), words
 
 
 def mt_tree_attention(q, k_cache, v_cache, pages, q_start, kv_len, visible, max_q, scale, out, workspace, lse=None, window=0,
@@ -538,10 +588,39 @@ def mt_tree_attention(q, k_cache, v_cache, pages, q_start, kv_len, visible, max_
     tokens, a token sees those whose bits are set in its row of visible, int32
     [T, words].  A window (0 for none) ends at the position that the number of
     its bits gives."""
+    torch = _torch or _get_torch()
+    shape = q.shape
+    if len(shape) != 3:
+        raise TypeError("q: a 3-dimensional tensor is required")
     if visible is None:
         raise TypeError("visible: rows of bits are required")
-    _attention("mt_tree_attention", q, k_cache, v_cache, pages, q_start, kv_len, visible, max_q, scale, out, workspace, lse, window,
-               sinks, stream)
+    T, H, D = shape
+    cache, batch, _, dim = _paged(k_cache, v_cache, pages, q_start, kv_len, T, max_q)
+    if D != dim:
+        raise ValueError(f"the cache's head size is {dim}, q's is {D}")
+    qp, qs = _head_rows("q", q, torch.bfloat16, shape)
+    f32 = out.dtype is torch.float32
+    op, os_ = _head_rows("out", out, torch.float32 if f32 else torch.bfloat16, shape)
+    bp, bld, words = _bit_rows("visible", visible, T)
+    lp = None
+    if lse is not None:
+        if lse.dtype is not torch.float32 or lse.shape != (T, H) or not lse.is_contiguous():
+            _typed("lse", lse, torch.float32, 2)
+            raise ValueError(f"lse: a contiguous tensor of shape {(T, H)} is required")
+        lp = lse.data_ptr()
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor is required")
+    if not -1 < window < 1 << 31:  # as in mt_paged_attention
+        window = -1 if window < 0 else 0x7FFFFFFF
+    if not -1 < sinks < 1 << 31:
+        sinks = -1 if sinks < 0 else 0x7FFFFFFF
+    if not (q.is_cuda and k_cache.is_cuda and v_cache.is_cuda and pages.is_cuda and q_start.is_cuda and kv_len.is_cuda and out.is_cuda
+            and workspace.is_cuda and (lse is None or lse.is_cuda) and visible.is_cuda):
+        _on_device("mt_tree_attention", q=q, k_cache=k_cache, v_cache=v_cache, pages=pages, q_start=q_start, kv_len=kv_len,
+                   visible=visible, out=out, workspace=workspace, lse=lse)
+    _check(_lib.mt_tree_attention(qp, qs, H, cache, batch, bp, bld, words, scale, window, sinks, op, os_,
+                                  MT_F32 if f32 else MT_BF16, lp, workspace.data_ptr(), workspace.nbytes,
+                                  _stream(stream)), "mt_tree_attention")
 
 
 def mt_tree_layout(parent, q_start, kv_len=None, positions=None, visible=None, stream=None) -> None:
@@ -661,67 +740,6 @@ def mt_cache_keep(caches, pages, q_start, kv_len, path, count, new_len=None, str
             _on_device("mt_cache_keep", k_cache=k, v_cache=v)
     _check(_lib.mt_cache_keep(cache, struct.pack(f"{n}P", *map(tensor.data_ptr, every)), n // 2, batch, path.data_ptr(), cp, cols, np_,
                               _stream(stream)), "mt_cache_keep")
-
-
-def mt_logit_penalties(logits, out, history=None, history_start=None, prompt_len=None, repetition=None, presence=None,
-                       frequency=None, bias_ids=None, bias_values=None, bias_start=None, allowed=None,
-                       stream=None) -> None:
-    """Biases, penalties for repeated tokens and allowed-token masks on logits
-    [B, V] (bf16 or fp32) into out (which may be logits); ragged int32 history
-    and bias lists with [B + 1] starts, allowed int32 [B, words] bits."""
-    torch = _torch or _get_torch()
-    i32, f32, dt = torch.int32, torch.float32, logits.dtype
-    shape = logits.shape
-    if (dt is not f32 and dt is not torch.bfloat16) or len(shape) != 2 or out.dtype is not dt:
-        _typed("logits", logits, f32 if dt is f32 else torch.bfloat16, 2)
-        _typed("out", out, dt, 2)
-    B, V = shape
-    ld, one = logits.stride()
-    out_ld, out_one = out.stride()
-    if out.shape != shape or (V > 1 and (one != 1 or out_one != 1)):
-        raise ValueError("logits and out must have the same shape and contiguous rows")
-    if B == 1:
-        ld = out_ld = V
-    hist = start = prompt = ids = values = bstart = ap = None
-    n_hist = n_bias = ald = 0
-    # an empty tensor has no address: a list without entries is no list
-    if history is not None:
-        n_hist = history.numel()
-        hist = _flat("history", history, i32) or None
-        start = _flat("history_start", history_start, i32, B + 1) if hist else None
-        prompt = _flat("prompt_len", prompt_len, i32, B) if hist else None
-    if bias_ids is not None:
-        n_bias = bias_ids.numel()
-        ids = _flat("bias_ids", bias_ids, i32) or None
-        values = _flat("bias_values", bias_values, f32, n_bias) if ids else None
-        bstart = _flat("bias_start", bias_start, i32, B + 1) if ids else None
-    if allowed is not None:
-        if allowed.dtype is not i32 or allowed.dim() != 2:
-            _typed("allowed", allowed, i32, 2)
-        rows, words = allowed.shape
-        ald, one = allowed.stride()
-        if rows != B or (words > 1 and one != 1):
-            raise ValueError(f"allowed: {B} contiguous rows are required")
-        if words * 32 < V:
-            raise ValueError(f"allowed: {(V + 31) // 32} words a row are required")
-        ap = allowed.data_ptr()
-        if B == 1:
-            ald = words
-    if (B | V | n_hist | n_bias) >> 31:
-        raise ValueError("logits and lists of fewer than 2^31 rows, tokens and entries are required")
-    if not (logits.is_cuda and out.is_cuda and (hist is None or history.is_cuda) and (start is None or history_start.is_cuda)
-            and (prompt is None or prompt_len.is_cuda) and (repetition is None or repetition.is_cuda)
-            and (presence is None or presence.is_cuda) and (frequency is None or frequency.is_cuda)
-            and (ids is None or bias_ids.is_cuda) and (values is None or bias_values.is_cuda)
-            and (bstart is None or bias_start.is_cuda)
-            and (allowed is None or allowed.is_cuda)):
-        _on_device("mt_logit_penalties", logits=logits, out=out, history=history, history_start=history_start,
-                   prompt_len=prompt_len, repetition=repetition, presence=presence, frequency=frequency, bias_ids=bias_ids,
-                   bias_values=bias_values, bias_start=bias_start, allowed=allowed)
-    _check(_lib.mt_logit_penalties(logits.data_ptr(), ld, out.data_ptr(), out_ld, MT_F32 if dt is f32 else MT_BF16, B, V,
-                                   hist, start, prompt, n_hist, _flat("repetition", repetition, f32, B),
-                                   _flat("presence", presence, f32, B), _flat("frequency", frequency, f32, B), ids, values,
-                                   bstart, n_bias, ap, ald, _stream(stream)), "mt_logit_penalties")
 
 
 def mt_set_option(opt: int, value: int) -> None:

@@ -359,12 +359,12 @@ __device__ __forceinline__ int64_t part_at(int64_t slot, int r, int d) {
 // Joins the tile cut at the end of CTA x's stretch.  A warp takes two rows at a
 // time, V columns a lane: the loads of both rows' parts are in flight
 // together.  Where a tile has more than eight parts, the block's eight warps
-// share out those of one row, and add up in order; where the block has several
-// such rows, a warp does one by itself, several parts at a time in flight, with the
-// sums in the same order (trees of 16 tokens, 112 rows, over 80 000: 47.7 ->
-// 35; one of 25 over 1200: 16.1 -> 16.3).
+// share out those of one row, and add up in order; trees (MANY), whose tiles have
+// many rows and, over long texts, many parts, have a warp do a row by itself where
+// a block has several, with the sums in the same order (16 tokens, 112 rows, over
+// 80 000: 47.7 -> 35 us; single tokens lose 1 % by the longer kernel).
 constexpr int JOIN_WARPS = 8;
-template <int R, int DP>
+template <int R, int DP, bool MANY>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) attn_join_kernel(const AttnArgs a) {
   constexpr int V = DP / 32;
   __shared__ float o_sh[JOIN_WARPS][DP];
@@ -454,8 +454,8 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) attn_join_kernel(const AttnAr
   const int per = (parts + JOIN_WARPS - 1) / JOIN_WARPS, p0 = min(parts, warp * per), p1 = min(parts, p0 + per);
   // a row takes a block about as long as 16 parts of one take a warp
   const int mine = (rows - (int)blockIdx.y + (int)gridDim.y - 1) / (int)gridDim.y;
-  if (mine > 1 && 16 * mine > parts) {
-    constexpr int F = V >= 8 ? 2 : 4;  // parts in flight, within the other path's registers
+  if (MANY && mine > 1 && 16 * mine > parts) {
+    constexpr int F = V >= 8 ? 2 : V == 4 ? 4 : 8;  // parts in flight
     for (int r = blockIdx.y + warp * gridDim.y; r < rows; r += JOIN_WARPS * gridDim.y) {
       Row sum, x;
       clear(sum);

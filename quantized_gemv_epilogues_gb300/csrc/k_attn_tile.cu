@@ -905,7 +905,7 @@ mt_status run_tile(AttnArgs a, void* ws, const Launch& l, const DeviceInfo* di) 
   w += (size_t)ctas * 2 * AT_R * sizeof(float2);
   a.part_o = reinterpret_cast<float*>(w);
   if (const mt_status st = launch(attn_tile_kernel<DP, TREE>, dim3(ctas), dim3(AT_THREADS), at_smem<DP>(), l, qmap, kmap, vmap, omap, a, box)) return st;
-  return launch(attn_join_kernel<AT_R, DP>, dim3(ctas, join_blocks(a)), dim3(32 * JOIN_WARPS), 0, l, a);
+  return launch(attn_join_kernel<AT_R, DP, TREE>, dim3(ctas, join_blocks(a)), dim3(32 * JOIN_WARPS), 0, l, a);
 }
 
 }  // namespace
