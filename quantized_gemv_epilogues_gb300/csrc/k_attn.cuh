@@ -24,6 +24,10 @@
 // tiles has rows.  (A chunk of 384 beside 15 single tokens: 78 us, and 85 with
 // equal blocks, 94 with 3 and 4; a prompt of 8000: 338, 343 and 341 us.)  A
 // stretch border within a block leaves the block to the later stretch.
+// Blocks of trees are 3 units each: whether one 128-row tile has rows or both, a
+// block takes about as long as its keys and values take to come (trees of 32 and
+// of 33 tokens in 24 texts: 117 and 127 us; trees of 26 to 64: 128, and 136 with
+// 3 and 2).
 //
 // Trees (mt_tree_attention, TREE): a row sees those of the sequence's new tokens
 // whose bits are set in its row of `visible`, and of the tokens before them all,
@@ -102,14 +106,14 @@ __device__ __forceinline__ int tile_count(const AttnArgs& a, const PagedSeq& s) 
   return (s.n * a.group + per - 1) / per;  // n <= 2^22, group <= 128: within 31 bits
 }
 
-template <int EXTRA>
+template <int EXTRA, bool TREE>
 __device__ __forceinline__ int block_units(const AttnArgs& a, const TileRows& r) {
-  return EXTRA == 0 ? 1 : r.rows > a.tile_tokens / 2 * a.group ? 3 : 2;
+  return EXTRA == 0 ? 1 : TREE || r.rows > a.tile_tokens / 2 * a.group ? 3 : 2;
 }
 template <int R, int BK, int EXTRA, bool TREE>
 __device__ __forceinline__ int tile_units(const AttnArgs& a, const PagedSeq& s, int rt) {
   const TileRows r = tile_rows<R>(a, s, rt);
-  return EXTRA + block_units<EXTRA>(a, r) * tile_span<BK, TREE>(s, r.i0, r.i1, a.window, a.sinks).n;
+  return EXTRA + block_units<EXTRA, TREE>(a, r) * tile_span<BK, TREE>(s, r.i0, r.i1, a.window, a.sinks).n;
 }
 
 // A position in the line of units.

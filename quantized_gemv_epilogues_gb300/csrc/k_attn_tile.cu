@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           if (k >= AT_PIECES && !wait1(piece_free(k), ((k / AT_PIECES) + 1) & 1)) break;
           Piece& p = sh.piece[k % AT_PIECES];
           // blocks [i0, i1) of the tile
-          const int w = block_units<AT_EXTRA>(a, c.r), all_units = AT_EXTRA + w * c.t.n;
+          const int w = block_units<AT_EXTRA, TREE>(a, c.r), all_units = AT_EXTRA + w * c.t.n;
           const int end = (int)min((long long)all_units, c.i + left);
           const int i0 = max(c.i - AT_EXTRA, 0) / w, i1 = (end - AT_EXTRA) / w;
           // (a stretch that ends before a tile's first block does leaves the tile to the next)
