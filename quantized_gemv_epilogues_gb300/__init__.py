@@ -709,37 +709,53 @@ _DTYPE, _IS_CUDA = operator.attrgetter("dtype"), operator.attrgetter("is_cuda")
 
 def mt_cache_keep(caches, pages, q_start, kv_len, path, count, new_len=None, stream=None) -> None:
     """Moves the keys and values of the new tokens path[b][:count[b]] (int32 [B,
-    cols], int32 [B]) together in each of the caches, (k_cache, v_cache) pairs
-    of equal shapes and strides; new_len int32 [B] (or None) takes the
-    sequences' lengths with them."""
+    cols], int32 [B]) together in each of the caches; new_len int32 [B] (or
+    None) takes the sequences' lengths with them.  caches: (k_cache, v_cache)
+    pairs of equal shapes and strides, or all of them as one tensor [layers, 2,
+    pages, page, heads, dim], which takes half the time to check."""
     torch = _torch or _get_torch()
-    i32, bf = torch.int32, torch.bfloat16
-    if not caches:
-        raise ValueError("caches: at least one pair is required")
+    i32, bf, tensor = torch.int32, torch.bfloat16, torch.Tensor
     most = 1 << 22  # rows of the step: none is read here
-    cache, batch, _, _ = _paged(*caches[0], pages, q_start, kv_len, most, 1)
-    # (36 layers have 72 tensors, and a loop over them takes 50 us: attributes by map)
-    every = [t for pair in caches for t in pair]
-    n = len(every)
-    k0, tensor = every[0], torch.Tensor
-    if (n != 2 * len(caches) or list(map(tensor.size, every)) != [k0.shape] * n
-            or list(map(tensor.stride, every)) != [k0.stride()] * n or set(map(_DTYPE, every)) != {bf}):
-        raise ValueError("caches: pairs of bf16 tensors of equal shapes and strides are required")
+    if isinstance(caches, tensor):
+        if caches.dim() != 6 or caches.dtype is not bf:
+            _typed("caches", caches, bf, 6)
+        n = 2 * caches.shape[0]
+        if caches.shape[1] != 2 or not n:
+            raise ValueError(f"caches: shape [layers, 2, pages, page, heads, dim] is required, got {tuple(caches.shape)}")
+        one = caches[0]
+        cache, batch, _, _ = _paged(one[0], one[1], pages, q_start, kv_len, most, 1)
+        at, (layer, side) = caches.data_ptr(), caches.stride()[:2]
+        places, step = [at] * n, 2 * layer or 1  # layers that share elements are refused below
+        places[0::2] = range(at, at + n // 2 * step, step)
+        places[1::2] = range(at + 2 * side, at + 2 * side + n // 2 * step, step)
+        every = (caches,)
+    else:
+        # (36 layers have 72 tensors, and a loop over them takes 50 us: attributes by map)
+        every = [t for pair in caches for t in pair]
+        n = len(every)
+        if not n or n != 2 * len(caches):
+            raise ValueError("caches: pairs of tensors, one at least, are required")
+        k0 = every[0]
+        cache, batch, _, _ = _paged(k0, every[1], pages, q_start, kv_len, most, 1)
+        if (list(map(tensor.size, every)) != [k0.shape] * n or list(map(tensor.stride, every)) != [k0.stride()] * n
+                or set(map(_DTYPE, every)) != {bf}):
+            raise ValueError("caches: pairs of bf16 tensors of equal shapes and strides are required")
+        places = map(tensor.data_ptr, every)
     B = pages.shape[0]
     if path.dtype is not i32 or path.dim() != 2 or path.shape[0] != B or not path.is_contiguous():
         _typed("path", path, i32, 2)
         raise ValueError(f"path: {B} contiguous rows are required")
     cols = path.shape[1]
     cp, np_ = _flat("count", count, i32, B), _flat("new_len", new_len, i32, B)
-    if cols >> 31:
-        raise ValueError("path: fewer than 2^31 columns are required")
+    if (cols | n) >> 31:
+        raise ValueError("fewer than 2^31 columns and caches are required")
     if not (pages.is_cuda and q_start.is_cuda and kv_len.is_cuda and path.is_cuda and count.is_cuda
             and (new_len is None or new_len.is_cuda) and all(map(_IS_CUDA, every))):
         _on_device("mt_cache_keep", pages=pages, q_start=q_start, kv_len=kv_len, path=path, count=count, new_len=new_len)
-        for k, v in caches:
-            _on_device("mt_cache_keep", k_cache=k, v_cache=v)
-    _check(_lib.mt_cache_keep(cache, struct.pack(f"{n}P", *map(tensor.data_ptr, every)), n // 2, batch, path.data_ptr(), cp, cols, np_,
-                              _stream(stream)), "mt_cache_keep")
+        for t in every:
+            _on_device("mt_cache_keep", caches=t)
+    _check(_lib.mt_cache_keep(cache, struct.pack(f"{n}P", *places), n // 2, batch, path.data_ptr(), cp, cols, np_, _stream(stream)),
+           "mt_cache_keep")
 
 
 def mt_set_option(opt: int, value: int) -> None:

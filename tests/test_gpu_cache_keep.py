@@ -62,11 +62,11 @@ class Case:
             news.append(base + kept)
         return got, news
 
-    def check(self, mt, stream=None):
+    def check(self, mt, stream=None, whole=False):
         want, news = self.want()
         i32 = dict(dtype=torch.int32, device="cuda")
         new = torch.full((len(self.lens),), 99, **i32)
-        args = ([(x[0], x[1]) for x in self.cache], self.table.cuda(), torch.tensor(self.starts, **i32),
+        args = (self.cache if whole else [(x[0], x[1]) for x in self.cache], self.table.cuda(), torch.tensor(self.starts, **i32),
                 torch.tensor([kv for _, kv in self.lens], **i32), self.path.cuda(), self.count.cuda())
         torch.cuda.synchronize()
         mt.mt_cache_keep(*args, new_len=new, stream=stream)
@@ -81,6 +81,24 @@ def test_paths(mt, page, order):
     lens = [(25, 100), (9, 9), (1, 50), (64, 64), (5, 20), (0, 30), (30, 31)]
     paths = [[0, 3, 4, 9, 24], [0, 1, 2, 8], [0], [0, 2, 4, 6, 8, 10, 12, 60, 61, 62, 63], [], [], [3, 4, 5, 6, 7, 29]]
     Case(lens, paths, page=page, order=order).check(mt)
+
+
+@pytest.mark.parametrize("order", ["nhd", "hnd", "layers"])
+def test_caches_in_one_tensor(mt, order):
+    lens, paths = [(25, 100), (9, 9), (64, 64)], [[0, 3, 4, 9, 24], [0, 1, 2, 8], [0, 2, 4, 60, 63]]
+    for L in (1, 5, 66):
+        Case(lens, paths, L=L, order=order, hkv=3, d=24, seed=L).check(mt, whole=True)
+
+
+def test_caches_in_one_tensor_that_share_elements(mt):
+    c = Case([(12, 40)], [[0, 5, 6]], L=1)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    args = (c.table.cuda(), torch.tensor(c.starts, **i32), torch.tensor([40], **i32), c.path.cuda(), c.count.cuda())
+    shape = c.cache.shape[2:]
+    for bad in (c.cache.expand(3, 2, *shape), c.cache[:, :1].expand(1, 2, *shape), c.cache[:, :1].expand(2, 2, *shape)):
+        with pytest.raises(mt.MTError) as e:
+            mt.mt_cache_keep(bad, *args)
+        assert e.value.status == mt.MT_ERR_ALIAS
 
 
 @pytest.mark.parametrize("hkv,d", [(1, 16), (8, 128), (2, 256), (3, 72), (5, 40), (16, 128)])

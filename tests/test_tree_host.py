@@ -182,6 +182,11 @@ BAD = [("mt_tree_attention", dict(visible=i32(1, 3).view(2, 1)), ValueError), ("
        ("mt_tree_verify", dict(q_start=i32(0, 1, 3)), ValueError), ("mt_tree_verify", dict(target=torch.zeros(3, 50, dtype=torch.bfloat16)), TypeError),
        ("mt_cache_keep", dict(caches=[]), ValueError), ("mt_cache_keep", dict(path=i32(0, 2)), TypeError), ("mt_cache_keep", dict(count=i32(1, 2)), ValueError),
        ("mt_cache_keep", dict(new_len=torch.zeros(1)), TypeError),
+       ("mt_cache_keep", dict(caches=[(torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16),)]), ValueError),
+       ("mt_cache_keep", dict(caches=torch.zeros(3, 2, 4, 16, 2, 64)), TypeError),
+       ("mt_cache_keep", dict(caches=torch.zeros(3, 3, 4, 16, 2, 64, dtype=torch.bfloat16)), ValueError),
+       ("mt_cache_keep", dict(caches=torch.zeros(0, 2, 4, 16, 2, 64, dtype=torch.bfloat16)), ValueError),
+       ("mt_cache_keep", dict(caches=torch.zeros(2, 4, 16, 2, 64, dtype=torch.bfloat16)), TypeError),
        ("mt_cache_keep", dict(caches=[(torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16),) * 2, (torch.zeros(3, 16, 2, 64, dtype=torch.bfloat16),) * 2]), ValueError)]
 
 
@@ -192,6 +197,12 @@ def test_python_refusals(mt, call, kw, err):
 
 
 CALLS = ["mt_tree_attention", "mt_tree_layout", "mt_token_probs", "mt_tree_verify", "mt_cache_keep"]
+
+
+def test_host_caches_in_one_tensor(mt):
+    kw = calls(mt)["mt_cache_keep"]
+    with pytest.raises(mt.MTError, match="in host memory"):
+        mt.mt_cache_keep(**{**kw, "caches": torch.zeros(3, 2, 4, 16, 2, 64, dtype=torch.bfloat16)}, stream=0)
 
 
 @pytest.mark.parametrize("call", CALLS)
