@@ -725,9 +725,10 @@ def mt_cache_keep(caches, pages, q_start, kv_len, path, count, new_len=None, str
         one = caches[0]
         cache, batch, _, _ = _paged(one[0], one[1], pages, q_start, kv_len, most, 1)
         at, (layer, side) = caches.data_ptr(), caches.stride()[:2]
-        places, step = [at] * n, 2 * layer or 1  # layers that share elements are refused below
-        places[0::2] = range(at, at + n // 2 * step, step)
-        places[1::2] = range(at + 2 * side, at + 2 * side + n // 2 * step, step)
+        places = [at, at + 2 * side] * (n // 2)
+        if layer:  # (without a stride they share their elements, which is refused below)
+            places[0::2] = range(at, at + n * layer, 2 * layer)
+            places[1::2] = range(at + 2 * side, at + 2 * side + n * layer, 2 * layer)
         every = (caches,)
     else:
         # (36 layers have 72 tensors, and a loop over them takes 50 us: attributes by map)

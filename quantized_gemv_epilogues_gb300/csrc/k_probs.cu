@@ -8,12 +8,13 @@
 // A cluster of up to eight blocks shares out a row; its blocks' largest logits,
 // sums and first places meet in one exchange through distributed shared memory.
 //  * Few rows (token_probs_kernel): the row lies in the blocks' registers, 8 K
-//    logits a thread.  9 rows of 151 936 fp32 logits take 6.5 us.
+//    logits a thread.  9 rows of 151 936 fp32 logits take 5.9 us.
 //  * Many (token_probs_loop_kernel): a block passes over its share with a running
 //    maximum and sum, and over it again, from L2, for the output: nothing but one
 //    exchange stands between the loads and the stores.  448 rows of 128 256 bf16
-//    logits: 73 us, 4.7 TB/s.  (The first kernel: 100; with clusters that stay and the next
-//    row's logits on their way 76, most of it waiting between the steps of a row.)
+//    logits: 68 us, 5.1 TB/s; 73 without the next vectors on their way.  (The
+//    first kernel: 100; with clusters that stay and the next row's logits on their
+//    way 76, most of it waiting between the steps of a row.)
 #include <math.h>
 
 #include <algorithm>
@@ -392,6 +393,12 @@ __global__ void __launch_bounds__(PB_THREADS, 2) token_probs_loop_kernel(const P
         w[f][4 * q + 3] = p.w;
       }
   };
+  auto take = [](uint32_t (&w)[F][Q], const uint32_t (&from)[F][Q]) {
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+#pragma unroll
+      for (int q = 0; q < Q; ++q) w[f][q] = from[f][q];
+  };
   auto logit = [](const uint32_t (&w)[Q], int i) { return F32 ? __uint_as_float(w[i % Q]) : i & 1 ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]); };
 
   // ---- the share's largest logit and its sum, a thread's own
@@ -405,10 +412,13 @@ __global__ void __launch_bounds__(PB_THREADS, 2) token_probs_loop_kernel(const P
     if (c.flat) sum = is_there(x1);
     else unpack2(ex.of(x1, -INFINITY, base), sum, none);
   }
+  uint32_t ahead[F][Q];  // the next vectors, on their way
+  load(ahead, s.v0 + tid);
 #pragma unroll 1
   for (int v = s.v0 + tid; v < s.v1; v += F * T) {
     uint32_t w[F][Q];
-    load(w, v);
+    take(w, ahead);
+    load(ahead, v + F * T);
     float most = -INFINITY;
     if (F32) {
 #pragma unroll
@@ -487,10 +497,12 @@ __global__ void __launch_bounds__(PB_THREADS, 2) token_probs_loop_kernel(const P
   least = ex.least(base);
   const float inv = __frcp_rn(all.sum);
   const uint64_t g = pack2(inv, inv);
+  load(ahead, s.v0 + tid);
 #pragma unroll 1
   for (int v = s.v0 + tid; v < s.v1; v += F * T) {
     uint32_t w[F][Q];
-    load(w, v);
+    take(w, ahead);
+    load(ahead, v + F * T);
 #pragma unroll
     for (int f = 0; f < F; ++f) {
       float y[8];
