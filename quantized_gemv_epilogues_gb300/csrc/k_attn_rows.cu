@@ -1,6 +1,6 @@
-// k_attn_rows.cu - attention over a paged cache for the layouts that the chunk
-// kernel (k_attn_tile.cu) does not take: fp32 outputs, head sizes below 64 or
-// above 128, pages that are no multiple of 8 tokens.
+// k_attn_rows.cu - attention over a paged cache, of chunks and of trees, for the
+// layouts that the chunk kernel (k_attn_tile.cu) does not take: fp32 outputs, head
+// sizes below 64 or above 128, pages that are no multiple of 8 tokens.
 //
 // Bound: memory for single tokens.  A key and its value (4 D bytes) are read
 // once for 16 rows, so a CTA does 16 * 4 D flops for 4 D bytes: 48 ragged texts

@@ -26,15 +26,6 @@ __device__ __forceinline__ void cluster_put(uint64_t* p, uint32_t rank, uint64_t
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
 }
 
-// The same, counted (8 bytes) on the barrier at the same place as `bar` there: a
-// thread that has waited for that barrier sees it.
-__device__ __forceinline__ void cluster_send(uint64_t* p, uint64_t* bar, uint32_t rank, uint64_t v) {
-  uint32_t at, on;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(on) : "r"(smem_u32(bar)), "r"(rank));
-  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u64 [%0], %1, [%2];" ::"r"(at), "l"(v), "r"(on) : "memory");
-}
-
 // launch() with clusters of `size` blocks along x (grid.x is a multiple of it).
 template <typename... KArgs, typename... Args>
 mt_status launch_cluster(void (*kernel)(KArgs...), int size, dim3 grid, dim3 block, size_t smem, const Launch& l, Args&&... args) {
