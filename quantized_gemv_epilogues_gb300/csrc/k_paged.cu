@@ -69,7 +69,21 @@ bool paged_layers_apart(const mt_paged_cache* c, void* const* layers, int L) {
   std::sort(at, at + 2 * L);
   Dim d[3];
   const int n = cache_dims(c, d);
-  // most caches span no other; the rows of those that do are compared
+  // Layers side by side within each page (or token, or head), where every cache
+  // spans all others: what a cache has in one step of a dimension repeats with its
+  // stride, so places in that step that are apart are apart everywhere.  (36
+  // layers: 60 us by the comparison of all pairs below, 1024: 35 ms.)
+  for (int k = n - 1; k >= 0; --k) {
+    if (k < n - 1 && d[k + 1].stride % d[k].stride) break;
+    int64_t in[2 * PG_MAX_LAYERS], span = c->head_dim;
+    for (int i = 0; i < k; ++i) span += (d[i].n - 1) * d[i].stride;
+    for (int i = 0; i < 2 * L; ++i) in[i] = (at[i] - at[0]) / 2 % d[k].stride;
+    std::sort(in, in + 2 * L);
+    bool apart = in[2 * L - 1] + span <= in[0] + d[k].stride;
+    for (int i = 1; apart && i < 2 * L; ++i) apart = in[i] - in[i - 1] >= span;
+    if (apart) return true;
+  }
+  // otherwise most caches span no other; the rows of those that do are compared
   for (int i = 0; i < 2 * L; ++i)
     for (int j = i + 1; j < 2 * L && at[j] - at[i] < bytes; ++j)
       if (rows_meet((at[j] - at[i]) / 2, d, n, c->head_dim)) return false;

@@ -2,6 +2,7 @@
 checked before anything is launched)."""
 import ctypes
 import math
+import random
 
 import pytest
 import torch
@@ -138,6 +139,35 @@ def test_layers_side_by_side_in_one_allocation(mt):
         assert keep(mt, caches) == mt.MT_ERR_CUDA
     caches[3] = cache(mt, k=at(3, 0), v=at(3, 1, -8), page_stride=2 * L * row)
     assert keep(mt, caches) == ALIAS
+
+
+def test_layers_anywhere_against_their_elements(mt):
+    # small caches at places and with strides of all kinds: an alias where, and only where, two share an element
+    rng = random.Random(5)
+    seen = {True: 0, False: 0}
+    for _ in range(1500):
+        pages, page, heads, dim, L = rng.randint(1, 3), rng.randint(1, 3), rng.randint(1, 3), 16, rng.randint(1, 3)
+        dims = [["pages", pages], ["page", page], ["heads", heads], ["layers", L], ["sides", 2]]
+        rng.shuffle(dims)
+        stride, step = {}, dim
+        for name, n in dims:
+            stride[name] = step
+            step *= n
+            if rng.random() < 0.2:
+                step += 8 * rng.randint(1, 3)
+        at = [stride["layers"] * i + stride["sides"] * j for i in range(L) for j in range(2)]
+        if rng.random() < 0.5:
+            at[rng.randrange(2 * L)] += 8 * rng.randint(0, 2 * step // 8)
+        rows = [p * stride["pages"] + t * stride["page"] + h * stride["heads"] for p in range(pages) for t in range(page) for h in range(heads)]
+        taken = [x + r + d for x in at for r in rows for d in range(0, dim, 8)]
+        share = len(set(taken)) < len(taken)
+        seen[share] += 1
+        kw = dict(num_pages=pages, page_size=page, kv_heads=heads, head_dim=dim, page_stride=stride["pages"], token_stride=stride["page"],
+                  head_stride=stride["heads"])
+        caches = [cache(mt, k=A(0) + 2 * at[2 * i], v=A(0) + 2 * at[2 * i + 1], **kw) for i in range(L)]
+        if share or not torch.cuda.is_available():  # (nothing is launched on made-up addresses)
+            assert keep(mt, caches) == (ALIAS if share else mt.MT_ERR_CUDA), (dims, stride, at)
+    assert min(seen.values()) > 100
 
 
 def test_nothing_to_do(mt):
