@@ -746,6 +746,9 @@ mt_status mt_token_probs(const void* logits, int64_t logits_ld, mt_dtype dtype, 
  * Probabilities count in steps of 2^-56 (above 1 as 1, below 0 and NaN as 0),
  * their sums and products are 64-bit integers: results are the same on every
  * run, whatever the order.  Rows should sum to about 1 (at most 255).
+ * Every draft's child that is refused while another is left costs a pass over
+ * the rows of p and q; without a draft, time grows with the square of a token's
+ * refused children.
  * Limits: 1 <= B <= 1024; 0 <= T <= 2^22 (0 does nothing); 1 <= V <= 2^24;
  *         1 <= cols <= 2^20; target_ld, draft_ld >= V; pointers 4-byte aligned.
  */
