@@ -722,8 +722,8 @@ def mt_cache_keep(caches, pages, q_start, kv_len, path, count, new_len=None, str
         n = 2 * caches.shape[0]
         if caches.shape[1] != 2 or not n:
             raise ValueError(f"caches: shape [layers, 2, pages, page, heads, dim] is required, got {tuple(caches.shape)}")
-        one = caches[0]
-        cache, batch, _, _ = _paged(one[0], one[1], pages, q_start, kv_len, most, 1)
+        k0 = caches[0, 0]  # (views cost 2 us each)
+        cache, batch, _, _ = _paged(k0, k0, pages, q_start, kv_len, most, 1)
         at, (layer, side) = caches.data_ptr(), caches.stride()[:2]
         places = [at, at + 2 * side] * (n // 2)
         if layer:  # (without a stride they share their elements, which is refused below)

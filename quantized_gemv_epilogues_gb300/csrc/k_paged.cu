@@ -67,6 +67,10 @@ bool paged_layers_apart(const mt_paged_cache* c, void* const* layers, int L) {
   int64_t at[2 * PG_MAX_LAYERS];
   for (int i = 0; i < 2 * L; ++i) at[i] = (int64_t)(uintptr_t)layers[i];
   std::sort(at, at + 2 * L);
+  // Most caches lie one behind the other.
+  bool behind = true;
+  for (int i = 1; i < 2 * L; ++i) behind &= at[i] - at[i - 1] >= bytes;
+  if (behind) return true;
   Dim d[3];
   const int n = cache_dims(c, d);
   // Layers side by side within each page (or token, or head), where every cache
@@ -83,7 +87,7 @@ bool paged_layers_apart(const mt_paged_cache* c, void* const* layers, int L) {
     for (int i = 1; apart && i < 2 * L; ++i) apart = in[i] - in[i - 1] >= span;
     if (apart) return true;
   }
-  // otherwise most caches span no other; the rows of those that do are compared
+  // otherwise the rows of each pair whose spans meet
   for (int i = 0; i < 2 * L; ++i)
     for (int j = i + 1; j < 2 * L && at[j] - at[i] < bytes; ++j)
       if (rows_meet((at[j] - at[i]) / 2, d, n, c->head_dim)) return false;
