@@ -744,8 +744,9 @@ mt_status mt_token_probs(const void* logits, int64_t logits_ld, mt_dtype dtype, 
  *   out_count  : int32 [B]: tokens of the path, as many as out_tokens has; 0
  *                for a sequence without new tokens
  * Probabilities count in steps of 2^-56 (above 1 as 1, below 0 and NaN as 0),
- * their sums and products are 64-bit integers: results are the same on every
- * run, whatever the order.  Rows should sum to about 1 (at most 255).
+ * their sums and products are integers of 64 bits, S of 96: results are the
+ * same on every run, whatever the order and however many children are refused.
+ * Rows should sum to about 1 (at most 255).
  * Every draft's child that is refused while another is left costs a pass over
  * the rows of p and q; without a draft, time grows with the square of a token's
  * refused children.

@@ -13,7 +13,9 @@
 // own step is larger; 2^-57 off below) and all sums are 64-bit integers: a
 // distribution function summed in fp32 over 10^5 tokens is off by some 2^-24,
 // which is as much as a rare token's share, and would draw other tokens in
-// another order of the sum.
+// another order of the sum.  R is at most a row's sum, below 256; S, which grows by
+// R with every refused child of a token, has a second word (children that the
+// target does not have leave R as it is, so that 256 of them take S past 2^64).
 //
 // Bound: latency, then memory: a float for each child that is tried and one row
 // of p (and of q) for the token that is drawn.  A cluster of blocks shares out a
@@ -106,10 +108,31 @@ __device__ __forceinline__ uint64_t chance(float u) { return steps(fminf(__satur
 __device__ __forceinline__ uint64_t times(uint64_t a, uint64_t b) { return (__umul64hi(a, b) << 8) | ((a * b) >> 56); }
 __device__ __forceinline__ uint64_t less(uint64_t a, uint64_t b) { return a > b ? a - b : 0; }
 
+// S: 0 before a child is refused, then the sum of R over the refused ones, of which
+// there are at most 2^22: hi stays below 2^22.
+struct Cut {
+  uint64_t lo;
+  uint32_t hi;
+  __device__ __forceinline__ bool none() const { return (lo | hi) == 0; }
+  __device__ __forceinline__ bool one() const { return hi == 0 && lo == VF_ONE; }
+  __device__ __forceinline__ void add(uint64_t R) {
+    lo += R;
+    hi += lo < R;
+  }
+  // S q, cut to a step; from 2^56 steps on as those (p has no more).
+  __device__ __forceinline__ uint64_t of(uint64_t q) const {
+    const uint64_t low = times(lo, q);
+    if (hi == 0) return low;
+    const uint64_t high = hi * q;
+    if ((__umul64hi(hi, q) | high >> 48) != 0) return VF_ONE;
+    return (high << 8) + low;  // q < 2^48, so that low < 2^56
+  }
+};
+
 template <bool DRAFT>
-__device__ __forceinline__ uint64_t left_of(const float* p, const float* q, int v, uint64_t S) {
+__device__ __forceinline__ uint64_t left_of(const float* p, const float* q, int v, const Cut& S) {
   const uint64_t x = steps(__ldg(p + v));
-  return DRAFT && S ? less(x, times(S, steps(__ldg(q + v)))) : x;
+  return DRAFT && !S.none() ? less(x, S.of(steps(__ldg(q + v)))) : x;
 }
 
 // The sum of x over a warp.
@@ -128,13 +151,16 @@ __device__ __forceinline__ uint64_t warp_upto(uint64_t x, int lane) {
   return x;
 }
 
+// Two blocks an SM: 64 registers, 20 bytes of them spilled with a draft (98 without
+// the bound, and one block).
 template <bool DRAFT>
-__global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(VF_THREADS, 2) tree_verify_kernel(const VerifyArgs a) {
   __shared__ int32_t t_parent[VF_TREE], t_token[VF_TREE];
   __shared__ uint64_t t_random[VF_TREE], t_p[VF_TREE], t_q[DRAFT ? VF_TREE : 1];  // in steps
   __shared__ uint64_t part[VF_WARPS];  // sums of each warp's stretch of this block's share of the vocabulary
   __shared__ uint64_t share[2][16];    // of each block's share, in turn
-  __shared__ uint64_t s_S, s_U;
+  __shared__ uint64_t s_U;
+  __shared__ Cut s_S;
   __shared__ int s_node, s_more, s_refused, s_count;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, C = a.blocks, V = a.V;
   const int rank = C > 1 ? (int)cluster_rank() : 0, b = blockIdx.x / C;
@@ -208,13 +234,13 @@ __global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArg
     }
     return sum;
   };
-  auto sum_stretch = [&](int node, uint64_t S) {
+  auto sum_stretch = [&](int node, const Cut& S) {
     const float* p = target(node);
     const float* q = draft(node);
     uint64_t sum = 0;
     int v = v0 + lane;
     if (fours) {
-      if (!DRAFT || S == 0) {
+      if (!DRAFT || S.none()) {
         sum = sum_fours(p, nullptr, [](const auto& x, const auto&) {
           Steps s = {0, 0, 0};
 #pragma unroll
@@ -224,7 +250,7 @@ __global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArg
           }
           return whole(s);
         });
-      } else if (S == VF_ONE) {
+      } else if (S.one()) {
         // one refused, as in every chain: p - q where that is positive
         sum = sum_fours(p, q, [](const auto& x, const auto& y) {
           Steps s = {0, 0, 0};
@@ -245,7 +271,7 @@ __global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArg
       } else {
         sum = sum_fours(p, q, [&](const auto& x, const auto& y) {
           uint64_t s = 0;
-          auto one = [&](float x, float y) { s += less(steps(x), times(S, steps(y))); };
+          auto one = [&](float x, float y) { s += less(steps(x), S.of(steps(y))); };
 #pragma unroll
           for (int i = 0; i < (int)(sizeof(x) / sizeof(x[0])); ++i) {
             one(x[i].x, y[i].x);
@@ -294,11 +320,12 @@ __global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArg
     // ---- the walk; the other warps add up rows for it
     int node = 0, count = 0;
     bool refused = false, known = true;  // is R?
-    uint64_t S = 0, R = VF_ONE;
+    Cut S = {0, 0};
+    uint64_t R = VF_ONE;
     for (;;) {
       if (lane == 0 && writes) out_path[count] = node;
       ++count;
-      S = 0;
+      S = {0, 0};
       R = VF_ONE;
       refused = false;
       known = true;
@@ -343,12 +370,12 @@ __global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArg
             known = true;
           }
           const int who = __ffs(kids) - 1;
-          const uint64_t left = S ? less(p, times(S, q)) : p;
+          const uint64_t left = S.none() ? p : less(p, S.of(q));
           if (__shfl_sync(0xffffffffu, (int)(__umul64hi(times(R, q), U) < left), who)) {
             next = c0 + who;
             break;
           }
-          S += R;
+          S.add(R);
           known = false;
         }
       }
@@ -379,7 +406,7 @@ __global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArg
   }
   // ---- the draw
   const int node = s_node;
-  uint64_t S = s_S;
+  Cut S = s_S;
   bool without = !DRAFT && s_refused;  // the refused tokens are out
   for (int round = 0; round < 2; ++round) {
     sum_stretch(node, S);
@@ -455,9 +482,9 @@ __global__ void __launch_bounds__(VF_THREADS) tree_verify_kernel(const VerifyArg
     }
     // nothing left: from the target's row itself
     __syncthreads();
-    if (!without && S == 0) break;
+    if (!without && S.none()) break;
     without = false;
-    S = 0;
+    S = {0, 0};
   }
   if (writes && tid == 0) out_tokens[s_count - 1] = -1;
 }
