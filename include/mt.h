@@ -705,8 +705,12 @@ mt_status mt_tree_attention(const void* q, int64_t q_stride, int q_heads, const 
  *   temperature : float [R], or NULL (1)
  *   probs       : float [R][V], rows probs_ld elements apart; may be logits
  *                 (fp32, the same address and stride)
- * Arithmetic is fp32 (the exponent's argument to twice that), one rounding at
- * the end.
+ * Arithmetic is fp32.  A probability is off by at most 2^-20 of itself (an
+ * exponential, a share's exponential and six roundings), by the rounding of x -
+ * max x (2^-24 of |x - max x| / temperature; the quotient is exact to 2^-40),
+ * and by what the row's sum is off, the same for all of the row: 2^-20 and V /
+ * 512 + 130 roundings of 2^-24 at the most.  Probabilities below 2^-126 count in
+ * steps of 2^-149.
  * Limits: 0 <= R <= 2^22 (0 does nothing), 1 <= V <= 2^24; logits_ld, probs_ld
  *         >= V; arrays aligned to their elements.
  */

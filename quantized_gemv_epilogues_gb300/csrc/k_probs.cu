@@ -12,9 +12,9 @@
 //  * Many (token_probs_loop_kernel): a block passes over its share with a running
 //    maximum and sum, and over it again, from L2, for the output: nothing but one
 //    exchange stands between the loads and the stores.  448 rows of 128 256 bf16
-//    logits: 68 us, 5.1 TB/s; 73 without the next vectors on their way.  (The
-//    first kernel: 100; with clusters that stay and the next row's logits on their
-//    way 76, most of it waiting between the steps of a row.)
+//    logits: 70 us, 4.9 TB/s; some 5 more without the next vectors on their way.
+//    (The first kernel: 100; with clusters that stay and the next row's logits on
+//    their way 76, most of it waiting between the steps of a row.)
 #include <math.h>
 
 #include <algorithm>
@@ -37,8 +37,9 @@ struct ProbArgs {
   int R, blocks;  // blocks of a row
 };
 
-// 1 / t in units of log2 e, as a sum of two floats: the exponent's argument is
-// off by 2^-40 of itself, not by the 2^-23 that would be 2^-17 of a small p.
+// 1 / t in units of log2 e, as a sum of two floats: the exponent's argument, (x -
+// base) / t with the difference as fp32 gives it, is off by 2^-40 of itself, not by
+// the 2^-23 that would be 2^-17 of a small p.
 __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -150,14 +151,19 @@ __device__ __forceinline__ void put8(float* to, int mis, const float (&y)[8]) {
 }
 
 // Pairs of 2^(40 + (x - base) c), x <= base: so that what lies below 2^-126 of the
-// largest stays normal.
+// largest stays normal.  The argument d c + 40 is y + rest.  y is a multiple of 2^-16
+// (d hi + 384 is in [184, 384], where floats are 2^-15 or 2^-16 apart), so that y, 40
+// - y and what d hi is beyond them are without a rounding but the last's, which is
+// 2^-40 or less; a y rounded to its own step, which is smaller where it is near 0,
+// would be lost in 40 - y by up to 2^-18.  (One more addition for two logits: 448
+// rows of 128 256 bf16 logits 68 -> 70 us, fp32 ones no change.)
 struct Exp2 {
   uint64_t hi, lo;
   float low, c_hi;  // d as small as 2^-200 needs stands for all that is less, -inf too
   __device__ __forceinline__ explicit Exp2(const Scale& c) : hi(pack2(c.hi, c.hi)), lo(pack2(c.lo, c.lo)), low(-200.f * rcp(c.hi)), c_hi(c.hi) {}
   __device__ __forceinline__ uint64_t of(uint64_t d) const {
-    const uint64_t c40 = pack2(40.f, 40.f), y = fma2(d, hi, c40);
-    const uint64_t rest = fma2(d, lo, fma2(d, hi, fma2(y, pack2(-1.f, -1.f), c40)));  // what y's rounding left
+    const uint64_t y = add2(fma2(d, hi, pack2(384.f, 384.f)), pack2(-344.f, -344.f));
+    const uint64_t rest = fma2(d, lo, fma2(d, hi, fma2(y, pack2(-1.f, -1.f), pack2(40.f, 40.f))));
     float u, v;
     unpack2(y, u, v);
     return mul2(pack2(ex2_ftz(u), ex2_ftz(v)), fma2(rest, pack2(0.693147182f, 0.693147182f), pack2(1.f, 1.f)));
@@ -538,8 +544,8 @@ mt_status probs_run(ProbArgs a, const Launch& l, int sms) {
   // the fewest blocks a row that hold it, more where the rows are few
   a.blocks = 1;
   while (a.blocks < 8 && (per(a.blocks) > PB_MOST || ((int64_t)a.R * a.blocks < sms && per(a.blocks) > 1))) a.blocks *= 2;
-  // (64 rows of 50 257 bf16 logits: 7.2 us in registers, 8.6 in two passes; of
-  // 128 256, 512 blocks: 16.6 and 14.6; 448 of 4000, a block each: 5.4 and 10.3)
+  // (64 rows of 50 257 bf16 logits: 7.7 us in registers, 8.6 in two passes; of
+  // 128 256, 512 blocks: 16.7 and 15.4; 448 of 4000, a block each: 5.5 and 11.6)
   if (per(a.blocks) <= PB_MOST && (a.blocks == 1 || (int64_t)a.R * a.blocks <= 2 * sms)) {
     switch (per(a.blocks)) {
       case 1: return go(token_probs_kernel<F32, 1>);
@@ -551,8 +557,8 @@ mt_status probs_run(ProbArgs a, const Launch& l, int sms) {
   }
   // A share costs as much as its logits and 12 000 more; an SM does two at a time,
   // and one alone is not twice as fast.  (448 rows of 128 256 bf16 logits by 1, 2,
-  // 4 and 8 blocks: 88, 73, 82 and 101 us; of 50 257: 34, 39, 49 and 91; 100 rows of
-  // 151 936: 36, 29, 29 and 36; 64 of 128 256: 27, 17, 15 and 18.)
+  // 4 and 8 blocks: 74, 70, 83 and 109 us; of 50 257: 32, 39, 53 and 98; 100 rows of
+  // 151 936: 30, 29, 28 and 37; 64 of 128 256: 24, 15, 15 and 19.)
   double least = 0;
   for (int C = 1; C <= 8; C *= 2) {
     const int64_t n = ((int64_t)a.R * C + sms - 1) / sms;
