@@ -681,6 +681,12 @@ mt_status mt_tree_layout(const int32_t* parent, const int32_t* q_start, const in
  * roundings, limits and workspace (mt_paged_attention_workspace_bytes) these
  * are.
  *   visible   : uint32 [T][words], rows visible_ld words apart
+ * A row has bits for 1024 new tokens at the most, and those from 32 * words on are
+ * seen by none, themselves included: a batch in which some sequences have trees
+ * and another a prompt's chunk of more than 32 * words tokens takes two calls, this
+ * one with the trees' part of q_start, kv_len and pages and mt_paged_attention with
+ * the others'.  Rows outside a call's part are left as they are, and one workspace
+ * does for both, one call after the other on a stream.
  * Page-table entries of a sequence are followed for its first `sinks` tokens and
  * from key base - window + 1 on.  New tokens that none of a tile's tokens sees
  * do not reach its output, NaN or not.

@@ -587,7 +587,9 @@ def mt_tree_attention(q, k_cache, v_cache, pages, q_start, kv_len, visible, max_
     """:func:`mt_paged_attention` for drafted trees: of the sequence's new
     tokens, a token sees those whose bits are set in its row of visible, int32
     [T, words].  A window (0 for none) ends at the position that the number of
-    its bits gives."""
+    its bits gives.  New tokens from 32 * words on are seen by none: sequences
+    with longer chunks belong into a :func:`mt_paged_attention` call of their own,
+    with their part of pages, q_start and kv_len."""
     torch = _torch or _get_torch()
     shape = q.shape
     if len(shape) != 3:
