@@ -13,8 +13,9 @@
 // maximum and sum, joined through shared memory at the tile's end.  K and V
 // blocks come by 16-byte cp.async into a ring of ST stages, which runs on
 // across tiles; page indices are fetched a block ahead of the copies that
-// need them.  (Head size 256: 255 registers and 84 bytes of spills.)  P enters the second product as bf16 hi + lo (2^-16 of each
-// weight; the tensor pipe has the time).
+// need them.  (Head size 256: 255 registers and 84 bytes of spilled stores, 276
+// with trees.)  P enters the second product as bf16 hi + lo (2^-16 of each weight;
+// the tensor pipe has the time).
 #include <math.h>
 
 #include <atomic>

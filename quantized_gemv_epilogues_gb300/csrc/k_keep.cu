@@ -7,8 +7,9 @@
 // the path's indices increase and each is at least its place in the path, so a
 // place is written only after the token that lay there was read, and no thread
 // waits for another.  36 layers of 8 heads of 128: one text's three moved tokens
-// 3.1 us, 64 texts' 240 (67 MB) 15.2, where the bytes take 9.9; the four loads one
-// after another before a token moves (lengths, path, page, row) are what is left.
+// 3.1 us, 64 texts' 234 (69 MB read and written) 15.2, where the bytes take 10.2; the
+// four loads one after another before a token moves (lengths, path, page, row) are
+// what is left.
 #include <algorithm>
 
 #include "k_paged.cuh"

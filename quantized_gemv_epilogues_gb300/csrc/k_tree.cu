@@ -11,7 +11,7 @@
 // then every token hops from block to block through shared memory, at most 31
 // hops in a chunk of 1024 tokens.  A token that leaves its chunk takes the rest
 // of its row, and of its depth, from that ancestor's, which the block wrote
-// before.  One block a sequence.
+// before.  One block a sequence, two an SM (32 registers, 16 bytes of them spilled).
 #include "k_paged.cuh"
 
 namespace mt {
