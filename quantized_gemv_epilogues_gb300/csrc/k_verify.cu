@@ -24,9 +24,9 @@
 // walks the tree for itself in shared memory, all children of a token in a warp
 // at a time; sums over the vocabulary meet through distributed shared memory.
 // R is summed up only where another child comes: not in chains.
-// Measured: 4.7 us for one token and 1000 words, of which the launch and three
+// Measured: 4.5 us for one token and 1000 words, of which the launch and three
 // loads one after the other (starts, parents, probabilities) are most; 0.5 us more
-// a level of the walk; one tree of 25 over 151 936 tokens 9.6 us; 64 chains over
+// a level of the walk; one tree of 25 over 151 936 tokens 9.1 us; 64 chains over
 // 128 256 23 us, 8.7 of them the rows' bytes.
 #include <math.h>
 
